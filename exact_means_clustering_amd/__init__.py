@@ -1,7 +1,7 @@
 """Exact Lloyd k-means on MI355X (gfx950): Python binding of libflashkm.so.
 
 The functions below only marshal torch tensors into the C ABI declared in
-``include/flashkm.h`` (same names without the ``kmeans_`` prefix): every step
+``include/flashkm.h`` and ``include/flashkm_codebook.h`` (same names without the ``kmeans_`` prefix): every step
 of the computation runs in the library's HIP kernels, on the current torch
 stream.  PyTorch provides device memory and streams, nothing else.  There is
 no CPU fallback: importing raises if the library is missing, and every call
@@ -21,7 +21,8 @@ import torch
 
 __all__ = ["KMeansError", "lib_path", "workspace_bytes", "assign", "assign_top2", "assign_soft", "gauss_sum", "seed", "update",
            "fit", "fit_streamed", "tune", "tune_save", "tune_load", "assign_configs", "assign_noalloc",
-           "stream_timeline", "DTYPES"]
+           "stream_timeline", "embed", "embed_grad", "embed_grad_workspace_bytes", "balance", "balance_grad",
+           "balance_workspace_bytes", "DTYPES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libflashkm.so"
@@ -77,6 +78,19 @@ def _load(path=None):
     lib.kmeans_assign_configs.restype = ctypes.c_int
     lib.kmeans_tune_load.argtypes = [ctypes.c_char_p]
     lib.kmeans_tune_load.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.kmeans_embed.argtypes = [P, i32, i64, i32, i32, i32, P, f32, P, i32, P]
+    lib.kmeans_embed.restype = ctypes.c_int
+    lib.kmeans_embed_grad_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.kmeans_embed_grad_workspace_bytes.restype = sz
+    lib.kmeans_embed_grad.argtypes = [P, i32, i64, i32, i32, i32, P, f32, i32, P, i32, P, sz, P]
+    lib.kmeans_embed_grad.restype = ctypes.c_int
+    lib.kmeans_balance_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.kmeans_balance_workspace_bytes.restype = sz
+    lib.kmeans_balance.argtypes = [P, i32, i64, i32, i32, P, i32, P, P, P, P, P, P, P, sz, P]
+    lib.kmeans_balance.restype = ctypes.c_int
+    lib.kmeans_balance_grad.argtypes = [P, i32, i64, i32, i32, P, P, P, P, P]
+    lib.kmeans_balance_grad.restype = ctypes.c_int
     lib.kmeans_last_error.argtypes = []
     lib.kmeans_last_error.restype = ctypes.c_char_p
     return lib
@@ -424,3 +438,168 @@ def fit_streamed(X_host, C0, iters: int, device_x_budget: int, *, history: bool 
                                     _ptr(labels), _ptr(C), ctypes.byref(inertia),
                                     hist if hist is not None else None, _stream(stream)))
     return labels, C, inertia.value, (list(hist) if hist is not None else None)
+
+
+# ---- codebook operators (include/flashkm_codebook.h) ------------------------------
+
+
+def _on_stream(fn):
+    """Run fn with its first CUDA tensor's device, and ``stream`` if one is given, current: what it allocates then
+    belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def run(*args, stream=None, **kwargs):
+        t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
+        if t is None:
+            return fn(*args, **kwargs)
+        if stream is not None:
+            if stream.device != t.device:
+                raise KMeansError(KM_EINVAL, f"stream is on {stream.device}, the tensors on {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(*args, **kwargs)
+        if t.device.index == torch.cuda.current_device():
+            return fn(*args, **kwargs)
+        with torch.cuda.device(t.device):
+            return fn(*args, **kwargs)
+    return run
+
+
+def _int32(v, name):
+    v = int(v)
+    if not -(1 << 31) <= v < 1 << 31:
+        raise KMeansError(KM_EINVAL, f"{name}={v} does not fit 32 bits")
+    return v
+
+
+def _ids(ids, name, like, lead):
+    """int32 ids of the rows ``lead`` ([N] or [B, N])."""
+    _need(ids, name, torch.int32, like=like)
+    if tuple(ids.shape) != tuple(lead):
+        raise KMeansError(KM_EINVAL, f"{name} must be {tuple(lead)} (got {tuple(ids.shape)})")
+
+
+def _into(t, name, shape, dtype, like):
+    """A caller's output tensor of exactly this shape and type."""
+    _need(t, name, dtype, like=like)
+    if tuple(t.shape) != tuple(shape):
+        raise KMeansError(KM_EINVAL, f"{name} must be {tuple(shape)} (got {tuple(t.shape)})")
+
+
+def _scratch(need, device, ws):
+    """A caller workspace or a new one; returns (tensor, its size in bytes).  No need of one: a shape was refused."""
+    if need == 0:
+        msg = _lib.kmeans_last_error().decode(errors="replace")
+        raise KMeansError(KM_EUNSUPPORTED if msg.startswith("unsupported") else KM_EINVAL, msg)
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise KMeansError(KM_EINVAL, f"ws must be a contiguous tensor on {device}")
+    return ws, ws.numel() * ws.element_size()
+
+
+@_on_stream
+def embed(table, ids, *, scale: float = 1.0, out_dtype=None, out=None):
+    """Table lookup with scaling: out[.., i, :] = scale * table[.., ids[.., i], :], rounded once; zeros for ids outside
+    [0, K).  table [K, D] with ids [N], or [B, K, D] with ids [B, N] int32; out_dtype defaults to the table's."""
+    _need(table, "table")
+    dt = _dtype(table)
+    if table.dim() not in (2, 3):
+        raise KMeansError(KM_EINVAL, "table must be [K, D] or [B, K, D]")
+    _need(ids, "ids", torch.int32, like=table)
+    if ids.dim() != table.dim() - 1 or (table.dim() == 3 and ids.shape[0] != table.shape[0]):
+        raise KMeansError(KM_EINVAL, f"ids must be [N] for a table [K, D], [B, N] for [B, K, D] (got {tuple(ids.shape)} "
+                                     f"with {tuple(table.shape)})")
+    B = _int32(table.shape[0], "B") if table.dim() == 3 else 1
+    K, D = _int32(table.shape[-2], "K"), _int32(table.shape[-1], "D")
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=out_dtype or table.dtype, device=table.device)
+    else:
+        _into(out, "out", (*ids.shape, D), out_dtype, table)
+    _check(_lib.kmeans_embed(_ptr(table), dt, ids.shape[-1], K, D, B, _ptr(ids), float(scale), _ptr(out), _dtype(out),
+                             _stream(None)))
+    return out
+
+
+def embed_grad_workspace_bytes(N: int, K: int, D: int, B: int = 1) -> int:
+    return int(_lib.kmeans_embed_grad_workspace_bytes(N, _int32(K, "K"), _int32(D, "D"), _int32(B, "B")))
+
+
+@_on_stream
+def embed_grad(dout, ids, K: int, *, scale: float = 1.0, grad_dtype=None, out=None, accumulate: bool = False, ws=None):
+    """Gradient of embed with respect to the table: [.., K, D], the sum of scale * dout[.., i, :] over the rows i with
+    ids[.., i] = k (deterministic, fp32 sums rounded once into grad_dtype, fp32 by default).  accumulate adds to ``out``
+    and leaves the entries that no row names untouched."""
+    _need(dout, "dout")
+    dt = _dtype(dout)
+    if dout.dim() not in (2, 3):
+        raise KMeansError(KM_EINVAL, "dout must be [N, D] or [B, N, D]")
+    _ids(ids, "ids", dout, dout.shape[:-1])
+    B = dout.shape[0] if dout.dim() == 3 else 1
+    N, D = dout.shape[-2:]
+    K = _int32(K, "K")
+    need = embed_grad_workspace_bytes(N, K, D, B)
+    ws, ws_bytes = _scratch(need, dout.device, ws)
+    shape = (K, D) if dout.dim() == 2 else (B, K, D)
+    if out is None:
+        if accumulate:
+            raise KMeansError(KM_EINVAL, "accumulate needs out")
+        out = torch.empty(shape, dtype=grad_dtype or torch.float32, device=dout.device)
+    else:
+        _into(out, "out", shape, grad_dtype, dout)
+    _check(_lib.kmeans_embed_grad(_ptr(dout), dt, N, K, D, B, _ptr(ids), float(scale), int(bool(accumulate)), _ptr(out),
+                                  _dtype(out), _ptr(ws), ws_bytes, _stream(None)))
+    return out
+
+
+def balance_workspace_bytes(N: int, K: int, B: int = 1, S: int = 1) -> int:
+    return int(_lib.kmeans_balance_workspace_bytes(N, _int32(K, "K"), _int32(B, "B"), _int32(S, "S")))
+
+
+def _logits(logits):
+    _need(logits, "logits")
+    if logits.dim() not in (2, 3):
+        raise KMeansError(KM_EINVAL, "logits must be [N, K] or [B, N, K]")
+    B = _int32(logits.shape[0], "B") if logits.dim() == 3 else 1
+    return _dtype(logits), B, logits.shape[-2], _int32(logits.shape[-1], "K")
+
+
+@_on_stream
+def balance(logits, labels, *, valid=None, ws=None):
+    """Balance loss of the use of K choices: logits [.., N, K], labels [.., N] or [.., N, S] int32 (the selections, for
+    instance from assign or assign_top2), valid [.., N] bool or None.  Returns (loss fp32 [B], counts int32 [.., K],
+    mean probabilities fp32 [.., K], (lse fp32 [.., N], coef fp32 [.., K])); the last pair is what balance_grad needs."""
+    dt, B, N, K = _logits(logits)
+    _need(labels, "labels", torch.int32, like=logits)
+    lead = tuple(logits.shape[:-1])
+    if labels.dim() not in (len(lead), len(lead) + 1) or tuple(labels.shape[:len(lead)]) != lead:
+        raise KMeansError(KM_EINVAL, f"labels must be {lead} or {lead} + (S,) (got {tuple(labels.shape)})")
+    S = labels.shape[-1] if labels.dim() > len(lead) else 1
+    if valid is not None:
+        _into(valid, "valid", lead, torch.bool, logits)
+    ws, ws_bytes = _scratch(balance_workspace_bytes(N, K, B, S), logits.device, ws)
+    per = (K,) if logits.dim() == 2 else (B, K)
+    loss = torch.empty(B, dtype=torch.float32, device=logits.device)
+    counts = torch.empty(per, dtype=torch.int32, device=logits.device)
+    prob = torch.empty(per, dtype=torch.float32, device=logits.device)
+    coef = torch.empty(per, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(lead, dtype=torch.float32, device=logits.device)
+    _check(_lib.kmeans_balance(_ptr(logits), dt, N, K, B, _ptr(labels), S, _ptr(valid), _ptr(loss), _ptr(counts),
+                               _ptr(prob), _ptr(lse), _ptr(coef), _ptr(ws), ws_bytes, _stream(None)))
+    return loss, counts, prob, (lse, coef)
+
+
+@_on_stream
+def balance_grad(logits, saved, dloss, *, out=None):
+    """Gradient of the balance loss with respect to the logits: ``saved`` = the (lse, coef) of balance, dloss fp32 [B]
+    the derivative of what follows with respect to the loss.  Returns dlogits, of the logits' shape and type."""
+    dt, B, N, K = _logits(logits)
+    lse, coef = saved
+    _into(lse, "lse", logits.shape[:-1], torch.float32, logits)
+    _into(coef, "coef", (K,) if logits.dim() == 2 else (B, K), torch.float32, logits)
+    _into(dloss, "dloss", (B,), torch.float32, logits)
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _into(out, "out", logits.shape, logits.dtype, logits)
+    _check(_lib.kmeans_balance_grad(_ptr(logits), dt, N, K, B, _ptr(lse), _ptr(coef), _ptr(dloss), _ptr(out),
+                                    _stream(None)))
+    return out

@@ -226,4 +226,28 @@ hipError_t launch_mean_from_sums(const double* S, const int64_t* n, int D, int64
                                  float* C_new, hipStream_t s);
 hipError_t launch_zero_bytes(void* p, size_t bytes, hipStream_t s);
 
+// ---- codebook operators ---------------------------------------------------------
+// Row lookup with scaling: out[i] = scale * table[b * K + ids[i]] for the n = B * N rows (b = i / N), zeros for ids
+// outside [0, K).
+hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids, int64_t N, int K, int D, int B,
+                        float scale, void* out, hipStream_t s);
+// Its gradient from the id-sorted rows (n = 0: no rows, `sorted` unused): grad[k] = (acc ? grad[k] : 0) + scale *
+// (sum of the rows of dout with key k).  Keys are b * (K + 1) + id, with id K for rows that leave nothing.
+hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const uint2* sorted, int64_t n, int K, int D, int B,
+                             float scale, bool acc, void* grad, hipStream_t s);
+
+// Balance loss and its gradient (see flashkm_codebook.h for the formulas).
+struct BalanceBuffers {
+  double* part;     // [B, balance_chunks(N), K] column sums of the probabilities
+  int32_t* nvalid;  // [B]
+  float2* ms;       // [B, N] row maximum and 1 / sum of exponentials
+};
+constexpr int kBalanceRows = 256;  // rows per column-sum chunk
+inline int64_t balance_chunks(int64_t N) { return N > 0 ? (N + kBalanceRows - 1) / kBalanceRows : 1; }
+hipError_t launch_balance(int dt, const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
+                          const uint8_t* valid, float* loss, int32_t* counts, float* prob, float* lse, float* coef,
+                          const BalanceBuffers& buf, hipStream_t s);
+hipError_t launch_balance_grad(int dt, const void* logits, int64_t N, int K, int B, const float* lse,
+                               const float* coef, const float* dloss, void* dlogits, hipStream_t s);
+
 }  // namespace fkm
