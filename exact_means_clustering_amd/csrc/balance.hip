@@ -1,8 +1,23 @@
 // Balance loss of the use of K choices by N rows, with counts, and its
-// gradient (formulas in flashkm_codebook.h).
+// gradient (formulas in flashkm_codebook.h).  Both are bound by reading the
+// logits (and writing the gradient) once.
 //
-// Exponentials are taken of differences from the row's maximum, formed before the scaling by log2(e), so logits of the
-// type's lowest value stay finite differences.
+// Rows up to kMaxK choices stay in registers.  A team of LPR lanes, or of W
+// whole waves, holds one row, E elements a lane, as 16-byte words where the
+// row allows it.  Forward, a lane owns its columns: after the row's maximum
+// and sum it adds its probabilities to its own column sums, in fp32 for up to
+// kFold rows and then into fp64, so the probabilities are never written and
+// the logits are read once.  A workgroup covers a chunk of rows of one
+// instance and leaves one partial sum per column (and its counts, from an LDS
+// histogram of integers); a second launch adds the chunks in a fixed order.
+// An instance of one chunk is finished by its own workgroup.  Longer rows
+// take two reads: row statistics, then column sums.
+//
+// Exponentials are taken of differences from a row's maximum (forward) or
+// lse (backward), formed before the scaling by log2(e), so logits of the
+// type's lowest value stay finite differences.  The backward pass divides by
+// the sum of those exponentials again: an lse of large magnitude does not
+// hold the sum's logarithm, but any shift near it gives the same quotients.
 #include "kernels.h"
 #include "vecio.h"
 
@@ -10,12 +25,382 @@ namespace fkm {
 
 namespace {
 
-__device__ __forceinline__ float wave_max_f32(float v) {
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kFold = 64;  // rows a column sum takes in fp32 before it is added in fp64
+
+__device__ __forceinline__ float exp_diff(float x, float shift) {
+  return __builtin_amdgcn_exp2f((x - shift) * kLog2e);
+}
+
+template <int LPR>
+__device__ __forceinline__ float team_max(float v) {
 #pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  for (int o = LPR / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float team_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
 
+// What the forward pass writes for one instance.
+struct BalanceOut {
+  float* loss;
+  int32_t* counts;
+  float* prob;
+  float* coef;
+};
+// Entry k of an instance from its column sum, count and valid rows; returns
+// its term of the loss.
+__device__ __forceinline__ double balance_entry(const BalanceOut& o, int64_t at, int K, int S, double T, double sum,
+                                                int count) {
+  const double per = T > 0 ? 1.0 / T : 0.0;
+  const double p = sum * per;
+  const double share = (double)count * ((double)K / S) * per;
+  o.counts[at] = count;
+  o.prob[at] = (float)p;
+  o.coef[at] = (float)(share * per);
+  return share * p;
+}
+
+// Sum over the workgroup in a fixed order (WAVES waves); every thread gets it.
+template <int WAVES>
+__device__ __forceinline__ double block_sum_f64(double v, double* tmp) {
+  v = wave_sum_f64(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) s += tmp[i];
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// rows in registers
+// ---------------------------------------------------------------------------
+// T type, V elements per load, NV loads per lane, LPR lanes per row (W = 1)
+// or W whole waves per row (LPR = 64).
+template <class T, int V, int NV, int LPR, int W>
+struct Rows {
+  static constexpr int E = V * NV;
+  static constexpr int MAXK = LPR * W * E;
+  static constexpr int BLOCK = W == 16 ? 1024 : 256;
+  static constexpr int WAVES = BLOCK / 64;
+  static constexpr int TEAMS = WAVES / W;       // teams of whole waves per workgroup
+  static constexpr int SL = 64 / LPR;           // rows per wave and step
+  static constexpr int STEP = TEAMS * SL;       // rows per workgroup and step
+  static_assert(W == 1 || (LPR == 64 && TEAMS == 1), "a wide team is the workgroup");
+  Pack<T, V> p[NV];
+  // the row's words of lane g of the team; zeros past it and for a row
+  // that is not live
+  __device__ __forceinline__ void load(const typename T::raw* row, int g, int K, bool live) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * LPR * W + g) * V;
+      if (live && c < K) p[j].load(row + c);
+      else p[j].zero();
+    }
+  }
+  // values as fp32, -inf past the row
+  __device__ __forceinline__ void values(float (&x)[E], int g, int K) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[V];
+      p[j].unpack(f);
+      const bool in = (j * LPR * W + g) * V < K;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j * V + v] = in ? f[v] : -INFINITY;
+    }
+  }
+};
+
+template <class T, int V, int NV, int LPR, int W>
+__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_kernel(
+    const typename T::raw* __restrict__ logits, int64_t N, int K, const int32_t* __restrict__ labels, int S,
+    const uint8_t* __restrict__ valid, float* __restrict__ lse, int64_t chunks, int steps, float* __restrict__ part,
+    int32_t* __restrict__ cpart, int32_t* __restrict__ vpart, BalanceOut out) {
+  using R = Rows<T, V, NV, LPR, W>;
+  constexpr int E = R::E, WAVES = R::WAVES;
+  __shared__ int hist[R::MAXK];
+  __shared__ double col[W == 1 ? R::MAXK : 1];
+  __shared__ float2 xch[2][W == 1 ? 1 : W];
+  __shared__ double tmp[WAVES];
+  __shared__ int nval;
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int g = W == 1 ? lane % LPR : tid;          // lane of the team
+  const int slot = W == 1 ? w * R::SL + lane / LPR : 0;
+  const int64_t b = blockIdx.x / chunks, c = blockIdx.x - b * chunks;
+  const int64_t i0 = c * steps * R::STEP;
+  const int64_t i1 = i0 + (int64_t)steps * R::STEP < N ? i0 + (int64_t)steps * R::STEP : N;
+  const int64_t base = b * N;
+
+  for (int k = tid; k < K; k += R::BLOCK) hist[k] = 0;
+  if (tid == 0) nval = 0;
+
+  float acc[E];
+  double sum[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f, sum[e] = 0.0;
+  int mine = 0;  // valid rows of this team
+  auto is_live = [&](int64_t i) { return i < i1 && (!valid || valid[base + i]); };
+  R next;
+  bool next_live = is_live(i0 + slot);
+  next.load(logits + (base + i0 + slot) * K, g, K, next_live);
+  __syncthreads();  // the histogram is clear
+  int fold = 0;
+  for (int t = 0; t < steps; ++t) {
+    const int64_t i = i0 + (int64_t)t * R::STEP + slot;
+    if (i0 + (int64_t)t * R::STEP >= i1) break;      // uniform over the workgroup
+    const R cur = next;
+    const bool live = next_live;
+    next_live = t + 1 < steps && is_live(i + R::STEP);
+    next.load(logits + (base + i + R::STEP) * K, g, K, next_live);
+    float x[E];
+    cur.values(x, g, K);
+    float m = x[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
+    m = team_max<LPR>(m);
+    // a wave (or team) without a finite maximum: shift by 0, so that -inf
+    // gives 0 (and NaN and +inf stay what they are)
+    float shift = m == -INFINITY ? 0.f : m;
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] = exp_diff(x[e], shift);
+      s += x[e];
+    }
+    s = team_sum<LPR>(s);
+    float scale = 1.f;  // from this wave's exponentials to the row's
+    if constexpr (W > 1) {
+      if (lane == 0) xch[t & 1][w] = make_float2(m, s);
+      __syncthreads();
+      float mm = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < W; ++q) mm = fmaxf(mm, xch[t & 1][q].x);
+      const float sh = mm == -INFINITY ? 0.f : mm;
+      float ss = 0.f;
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        const float2 o = xch[t & 1][q];
+        // a wave's sum is relative to its own shift (0 if it had none)
+        ss += o.y * exp_diff(o.x == -INFINITY ? (o.y == 0.f ? sh : 0.f) : o.x, sh);
+      }
+      scale = exp_diff(m == -INFINITY ? sh : m, sh);
+      m = mm, s = ss;
+    }
+    if (g == 0 && i < i1) {
+      lse[base + i] = !live ? INFINITY : s == 0.f ? -INFINITY : m + logf(s);
+      mine += live;
+    }
+    // a row that leaves no probability adds nothing, whatever its words hold
+    const bool adds = live && s != 0.f;
+    const float q = adds ? scale / s : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] += adds ? x[e] * q : 0.f;
+    if (++fold == kFold) {
+      fold = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += (double)acc[e], acc[e] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] += (double)acc[e];
+
+  // counts of the chunk's labels: integer LDS atomics, exact in any order
+  const int64_t l0 = (base + i0) * S, l1 = (base + i1) * S;
+  for (int64_t l = l0 + tid; l < l1; l += R::BLOCK) {
+    const uint32_t k = (uint32_t)labels[l];
+    if (k < (uint32_t)K && (!valid || valid[(uint32_t)l / (uint32_t)S])) atomicAdd(&hist[k], 1);
+  }
+  if (mine) atomicAdd(&nval, mine);
+
+  // column sums: lanes of one column add in a fixed order, then the waves
+  if constexpr (W == 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int o = LPR; o < 64; o <<= 1) sum[e] += __shfl_xor(sum[e], o);
+    for (int q = 0; q < WAVES; ++q) {
+      if (w == q && lane < LPR) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int k = ((e / V) * LPR + g) * V + e % V;
+          if (k < K) col[k] = q ? col[k] + sum[e] : sum[e];
+        }
+      }
+      __syncthreads();
+    }
+  } else {
+    __syncthreads();
+  }
+  const double T_ = nval;
+  const int64_t at = (b * chunks + c) * K;
+  double term = 0.0;
+  if constexpr (W == 1) {
+    for (int k = tid; k < K; k += R::BLOCK) {
+      if (chunks == 1) {
+        term += balance_entry(out, b * K + k, K, S, T_, col[k], hist[k]);
+      } else {
+        part[at + k] = (float)col[k];
+        cpart[at + k] = hist[k];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int k = ((e / V) * R::BLOCK + g) * V + e % V;
+      if (k >= K) continue;
+      if (chunks == 1) {
+        term += balance_entry(out, b * K + k, K, S, T_, sum[e], hist[k]);
+      } else {
+        part[at + k] = (float)sum[e];
+        cpart[at + k] = hist[k];
+      }
+    }
+  }
+  if (chunks == 1) {
+    term = block_sum_f64<WAVES>(term, tmp);
+    if (tid == 0) out.loss[b] = (float)term;
+  } else if (tid == 0) {
+    vpart[b * chunks + c] = nval;
+  }
+}
+
+// Chunk sums joined: 1,024 threads take CB columns of one instance, 1024 / CB
+// groups of chunks in order, joined by halving.  With one column block the
+// loss is finished here, else each block leaves its term.
+template <int CB>
+__global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part, int64_t chunks,
+                                                            const int32_t* cpart, int64_t cchunks,
+                                                            const int32_t* __restrict__ vpart, int64_t vchunks, int K,
+                                                            int S, int kblocks, int64_t units, BalanceOut out,
+                                                            double* __restrict__ terms) {
+  constexpr int G = 1024 / CB;
+  __shared__ double sp[1024];
+  __shared__ int sc[1024];
+  __shared__ double tmp[16];
+  const int tid = threadIdx.x;
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t b = u / kblocks;
+    const int kb = (int)(u - b * kblocks);
+    const int k = kb * CB + tid % CB, g = tid / CB;
+    int64_t nv = 0;
+    for (int64_t c = tid; c < vchunks; c += 1024) nv += vpart[b * vchunks + c];
+    double p = 0.0;
+    int n = 0;
+    if (k < K) {
+#pragma unroll 8
+      for (int64_t c = g; c < chunks; c += G) p += (double)part[(b * chunks + c) * K + k];
+#pragma unroll 8
+      for (int64_t c = g; c < cchunks; c += G) n += cpart[(b * cchunks + c) * K + k];
+    }
+    const double T_ = block_sum_f64<16>((double)nv, tmp);
+    sp[tid] = p;
+    sc[tid] = n;
+    for (int h = 512; h >= CB; h >>= 1) {
+      __syncthreads();
+      if (tid < h) sp[tid] += sp[tid + h], sc[tid] += sc[tid + h];
+    }
+    double term = 0.0;
+    if (tid < CB && k < K) term = balance_entry(out, b * K + k, K, S, T_, sp[tid], sc[tid]);
+    term = block_sum_f64<16>(term, tmp);  // its barriers also end this unit's use of sp and sc
+    if (tid == 0) {
+      if (kblocks == 1) out.loss[b] = (float)term;
+      else terms[u] = term;
+    }
+  }
+}
+
+// loss[b] = the column blocks' terms in a fixed order; one wave per instance.
+__global__ __launch_bounds__(256) void balance_loss_kernel(const double* __restrict__ terms, int kblocks, int B,
+                                                           float* __restrict__ loss) {
+  const int lane = lane_id();
+  for (int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); b < B; b += (int64_t)gridDim.x * 4) {
+    double s = 0.0;
+    for (int k = lane; k < kblocks; k += 64) s += terms[b * kblocks + k];
+    s = wave_sum_f64(s);
+    if (lane == 0) loss[b] = (float)s;
+  }
+}
+
+template <class T, int V, int NV, int LPR, int W>
+__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_rows_kernel(
+    const typename T::raw* __restrict__ logits, int64_t N, int K, const float* __restrict__ lse,
+    const float* __restrict__ coef, const float* __restrict__ dloss, int64_t chunks, int steps,
+    typename T::raw* __restrict__ dlogits) {
+  using R = Rows<T, V, NV, LPR, W>;
+  constexpr int E = R::E;
+  __shared__ float2 xch[2][W == 1 ? 1 : W];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int g = W == 1 ? lane % LPR : tid;
+  const int slot = W == 1 ? w * R::SL + lane / LPR : 0;
+  const int64_t b = blockIdx.x / chunks, c = blockIdx.x - b * chunks;
+  const int64_t i0 = c * steps * R::STEP;
+  const int64_t i1 = i0 + (int64_t)steps * R::STEP < N ? i0 + (int64_t)steps * R::STEP : N;
+  const int64_t base = b * N;
+  const float dl = dloss[b];
+  float cf[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = ((e / V) * LPR * W + g) * V + e % V;
+    cf[e] = k < K ? coef[b * K + k] : 0.f;
+  }
+  auto z_of = [&](int64_t i) { return i < i1 ? lse[base + i] : INFINITY; };
+  auto is_live = [](float z) { return z != INFINITY && z != -INFINITY; };
+  R next;
+  float next_z = z_of(i0 + slot);
+  next.load(logits + (base + i0 + slot) * K, g, K, is_live(next_z));
+  for (int t = 0; t < steps; ++t) {
+    const int64_t i = i0 + (int64_t)t * R::STEP + slot;
+    if (i0 + (int64_t)t * R::STEP >= i1) break;  // uniform over the workgroup
+    const R cur = next;
+    const float z = next_z;
+    next_z = t + 1 < steps ? z_of(i + R::STEP) : INFINITY;
+    next.load(logits + (base + i + R::STEP) * K, g, K, is_live(next_z));
+    float x[E];
+    cur.values(x, g, K);
+    float s = 0.f, d = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] = exp_diff(x[e], z);
+      s += x[e];
+      d = fmaf(x[e], cf[e], d);
+    }
+    s = team_sum<LPR>(s);
+    d = team_sum<LPR>(d);
+    if constexpr (W > 1) {
+      if (lane == 0) xch[t & 1][w] = make_float2(s, d);
+      __syncthreads();
+      s = 0.f, d = 0.f;
+#pragma unroll
+      for (int q = 0; q < W; ++q) s += xch[t & 1][q].x, d += xch[t & 1][q].y;
+    }
+    const float inv = 1.f / s;
+    const float mean = d * inv, scale = dl * inv;
+    const bool live = is_live(z);
+    if (i < i1) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int k = (j * LPR * W + g) * V;
+        if (k >= K) continue;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = live ? scale * x[j * V + v] * (cf[j * V + v] - mean) : 0.f;
+        Pack<T, V> q;
+        q.pack(o);
+        q.store(dlogits + (base + i) * K + k);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// rows longer than the registers hold
+// ---------------------------------------------------------------------------
 // lse of every row (+inf for an invalid one) and its (maximum, 1 / sum of
 // exponentials), (0, 0) for a row that leaves no probability: the
 // probabilities come from these, since a large lse has lost the sum's low
@@ -32,32 +417,25 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
     }
     const typename T::raw* row = logits + i * K;
     float m = -INFINITY;
-    bool nan = false;
-    for (int k = lane; k < K; k += 64) {
-      const float f = T::to_f32(row[k]);
-      nan |= f != f;
-      m = fmaxf(m, f);
-    }
-    m = wave_max_f32(m);
+    for (int k = lane; k < K; k += 64) m = fmaxf(m, T::to_f32(row[k]));
+    m = team_max<64>(m);
+    const float shift = m == -INFINITY ? 0.f : m;
     float sum = 0.f;
-    if (m > -INFINITY)
-      for (int k = lane; k < K; k += 64) sum += expf(T::to_f32(row[k]) - m);
-    sum = wave_sum_f32(sum);
-    if (__ballot(nan)) sum = NAN;
-    const bool none = m == -INFINITY && sum == 0.f;
+    for (int k = lane; k < K; k += 64) sum += exp_diff(T::to_f32(row[k]), shift);
+    sum = team_sum<64>(sum);
     if (lane == 0) {
-      lse[i] = none ? -INFINITY : m + logf(sum);
-      ms[i] = none ? make_float2(0.f, 0.f) : make_float2(m, 1.f / sum);
+      lse[i] = sum == 0.f ? -INFINITY : m + logf(sum);
+      ms[i] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(shift, 1.f / sum);
     }
   }
 }
 
-// part[b, chunk, k] = fp64 sum of p[b, i, k] over the chunk's valid rows; one
+// part[b, chunk, k] = sum of p[b, i, k] over the chunk's valid rows; one
 // thread per column.
 template <class T>
 __global__ __launch_bounds__(256) void balance_cols_kernel(const typename T::raw* __restrict__ logits, int64_t N,
                                                            int K, int64_t chunks, int kblocks, int64_t units,
-                                                           const float2* __restrict__ ms, double* __restrict__ part) {
+                                                           const float2* __restrict__ ms, float* __restrict__ part) {
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t bc = u / kblocks;
     const int k = (int)(u - bc * kblocks) * 256 + threadIdx.x;
@@ -68,9 +446,9 @@ __global__ __launch_bounds__(256) void balance_cols_kernel(const typename T::raw
     for (int64_t i = i0; i < i1; ++i) {
       const float2 z = ms[b * N + i];
       if (z.y == 0.f) continue;
-      sum += (double)(expf(T::to_f32(logits[(b * N + i) * K + k]) - z.x) * z.y);
+      sum += (double)(exp_diff(T::to_f32(logits[(b * N + i) * K + k]), z.x) * z.y);
     }
-    part[bc * K + k] = sum;
+    part[bc * K + k] = (float)sum;
   }
 }
 
@@ -98,97 +476,157 @@ __global__ __launch_bounds__(256) void balance_count_kernel(const int32_t* __res
   }
 }
 
-// One workgroup per instance: prob, coef and the loss.
-__global__ __launch_bounds__(256) void balance_finish_kernel(const double* __restrict__ part, int64_t chunks, int K,
-                                                             int S, const int32_t* __restrict__ counts,
-                                                             const int32_t* __restrict__ nvalid,
-                                                             float* __restrict__ loss, float* __restrict__ prob,
-                                                             float* __restrict__ coef) {
-  __shared__ double tmp[4];
-  const int64_t b = blockIdx.x;
-  const double T = nvalid[b];
-  const double per = T > 0 ? 1.0 / T : 0.0;
-  double sum = 0.0;
-  for (int k = threadIdx.x; k < K; k += 256) {
-    double p = 0.0;
-    for (int64_t c = 0; c < chunks; ++c) p += part[(b * chunks + c) * K + k];
-    p *= per;
-    const double share = (double)counts[b * K + k] * ((double)K / S) * per;
-    prob[b * K + k] = (float)p;
-    coef[b * K + k] = (float)(share * per);
-    sum += share * p;
-  }
-  sum = wave_sum_f64(sum);
-  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) loss[b] = (float)(((tmp[0] + tmp[1]) + tmp[2]) + tmp[3]);
-}
-
 template <class T>
-__global__ __launch_bounds__(256) void balance_grad_kernel(const typename T::raw* __restrict__ logits, int64_t n,
-                                                           uint32_t N, int K, const float* __restrict__ lse,
-                                                           const float* __restrict__ coef,
-                                                           const float* __restrict__ dloss,
-                                                           typename T::raw* __restrict__ dlogits) {
+__global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T::raw* __restrict__ logits, int64_t n,
+                                                                uint32_t N, int K, const float* __restrict__ lse,
+                                                                const float* __restrict__ coef,
+                                                                const float* __restrict__ dloss,
+                                                                typename T::raw* __restrict__ dlogits) {
   const int lane = lane_id();
   for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
     const int64_t b = (uint32_t)i / N;
     const float z = lse[i];
     const bool none = z == INFINITY || z == -INFINITY;
     const float* cf = coef + b * K;
-    // the row's maximum and sum again: an lse of large magnitude does not hold
-    // the sum's logarithm
-    float m = -INFINITY, sum = 0.f, dot = 0.f;
-    if (!none) {
-      for (int k = lane; k < K; k += 64) m = fmaxf(m, T::to_f32(logits[i * K + k]));
-      m = wave_max_f32(m);
+    float s = 0.f, d = 0.f;
+    if (!none)
       for (int k = lane; k < K; k += 64) {
-        const float e = expf(T::to_f32(logits[i * K + k]) - m);
-        sum += e;
-        dot = fmaf(e, cf[k], dot);
+        const float e = exp_diff(T::to_f32(logits[i * K + k]), z);
+        s += e;
+        d = fmaf(e, cf[k], d);
       }
-    }
-    sum = wave_sum_f32(sum);
-    dot = wave_sum_f32(dot) / sum;
-    const float w = dloss[b] / sum;
+    s = team_sum<64>(s);
+    d = team_sum<64>(d);
+    const float inv = 1.f / s, mean = d * inv, scale = dloss[b] * inv;
     for (int k = lane; k < K; k += 64)
       dlogits[i * K + k] =
-          round_to<T>(none ? 0.f : w * expf(T::to_f32(logits[i * K + k]) - m) * (cf[k] - dot));
+          round_to<T>(none ? 0.f : scale * exp_diff(T::to_f32(logits[i * K + k]), z) * (cf[k] - mean));
   }
 }
 
 int64_t capped(int64_t blocks) { return blocks < 1 ? 1 : blocks < (1 << 22) ? blocks : (1 << 22); }
 
+// Chunk sums in `part`, counts in `cpart` (cchunks of them), valid rows in
+// vpart, to the outputs.
+struct JoinIn {
+  const float* part;
+  int64_t chunks;
+  const int32_t* cpart;
+  int64_t cchunks;
+  const int32_t* vpart;
+  int64_t vchunks;
+};
+template <int CB>
+void join_launch(const JoinIn& in, int K, int S, int B, const BalanceOut& out, double* terms, hipStream_t s) {
+  const int kblocks = (K + CB - 1) / CB;
+  const int64_t units = (int64_t)B * kblocks;
+  const int64_t grid = units < (1 << 20) ? units : (1 << 20);
+  balance_join_kernel<CB><<<dim3((unsigned)grid), dim3(1024), 0, s>>>(in.part, in.chunks, in.cpart, in.cchunks,
+                                                                      in.vpart, in.vchunks, K, S, kblocks, units, out,
+                                                                      terms);
+  if (kblocks > 1)
+    balance_loss_kernel<<<dim3((unsigned)capped((B + 3) / 4)), dim3(256), 0, s>>>(terms, kblocks, B, out.loss);
+}
+hipError_t join(const JoinIn& in, int K, int S, int B, const BalanceOut& out, double* terms, hipStream_t s) {
+  // one workgroup per instance while it reads little, else 32 columns each
+  const bool one = K <= 1024 && in.chunks * K <= 65536;
+  if (K <= 32 || !one) join_launch<kBalanceJoinCols>(in, K, S, B, out, terms, s);
+  else if (K <= 64) join_launch<64>(in, K, S, B, out, terms, s);
+  else if (K <= 128) join_launch<128>(in, K, S, B, out, terms, s);
+  else if (K <= 256) join_launch<256>(in, K, S, B, out, terms, s);
+  else if (K <= 512) join_launch<512>(in, K, S, B, out, terms, s);
+  else join_launch<1024>(in, K, S, B, out, terms, s);
+  return hipGetLastError();
+}
+
+template <class T, int V, int NV, int LPR, int W>
+hipError_t rows_forward(const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
+                        const uint8_t* valid, float* lse, const BalanceOut& out, const BalanceBuffers& buf,
+                        hipStream_t s) {
+  using R = Rows<T, V, NV, LPR, W>;
+  static_assert(R::STEP == balance_step(R::MAXK), "the workspace's chunks are these");
+  const BalanceSplit sp = balance_split(N, B, K);
+  balance_rows_kernel<T, V, NV, LPR, W><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
+      static_cast<const typename T::raw*>(logits), N, K, labels, S, valid, lse, sp.chunks, sp.steps, buf.part,
+      buf.cpart, buf.vpart, out);
+  if (sp.chunks == 1) return hipGetLastError();
+  return join(JoinIn{buf.part, sp.chunks, buf.cpart, sp.chunks, buf.vpart, sp.chunks}, K, S, B, out, buf.terms, s);
+}
+
+template <class T, int V, int NV, int LPR, int W>
+hipError_t rows_backward(const void* logits, int64_t N, int K, int B, const float* lse, const float* coef,
+                         const float* dloss, void* dlogits, hipStream_t s) {
+  using R = Rows<T, V, NV, LPR, W>;
+  static_assert(R::STEP == balance_step(R::MAXK), "the workspace's chunks are these");
+  const BalanceSplit sp = balance_split(N, B, K);
+  balance_grad_rows_kernel<T, V, NV, LPR, W><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
+      static_cast<const typename T::raw*>(logits), N, K, lse, coef, dloss, sp.chunks, sp.steps,
+      static_cast<typename T::raw*>(dlogits));
+  return hipGetLastError();
+}
+
+// f(Team) with the smallest team that holds a row of K elements.
+template <int V_, int NV_, int LPR_, int W_>
+struct Team {
+  static constexpr int V = V_, NV = NV_, LPR = LPR_, W = W_;
+};
+template <int V, class F>
+hipError_t with_team(int K, F&& f) {
+  constexpr int A = 8 / V, C = 16 / V;  // loads for 8 and 16 elements
+  if (K <= 8) return f(Team<V, A, 1, 1>{});
+  if (K <= 16) return f(Team<V, A, 2, 1>{});
+  if (K <= 32) return f(Team<V, A, 4, 1>{});
+  if (K <= 64) return f(Team<V, A, 8, 1>{});
+  if (K <= 128) return f(Team<V, A, 16, 1>{});
+  if (K <= 256) return f(Team<V, A, 32, 1>{});
+  if (K <= 512) return f(Team<V, A, 64, 1>{});
+  if (K <= 1024) return f(Team<V, C, 64, 1>{});
+  if (K <= 4096) return f(Team<V, C, 64, 4>{});
+  return f(Team<V, C, 64, 16>{});
+}
+
 template <class T>
 hipError_t balance_t(const void* logits, int64_t N, int K, int B, const int32_t* labels, int S, const uint8_t* valid,
-                     float* loss, int32_t* counts, float* prob, float* lse, float* coef, const BalanceBuffers& buf,
-                     hipStream_t s) {
+                     float* lse, const BalanceOut& out, const BalanceBuffers& buf, hipStream_t s) {
+  constexpr int VEC = 16 / T::SZ;
+  if (K <= kBalanceMaxK) {
+    auto go = [&](auto team) {
+      using P = decltype(team);
+      return rows_forward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
+    };
+    return vec_width(K, logits, T::SZ, logits, T::SZ) >= VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+  }
   const int64_t n = N * B;
   const auto* x = static_cast<const typename T::raw*>(logits);
   const int64_t entries = (int64_t)B * K;
-  balance_zero_kernel<<<dim3((unsigned)capped((entries + 255) / 256)), dim3(256), 0, s>>>(counts, entries, buf.nvalid,
-                                                                                           B);
+  balance_zero_kernel<<<dim3((unsigned)capped((entries + 255) / 256)), dim3(256), 0, s>>>(out.counts, entries,
+                                                                                           buf.vpart, B);
   if (n) {
     balance_lse_kernel<T><<<dim3((unsigned)capped((n + 3) / 4)), dim3(256), 0, s>>>(x, n, K, valid, lse, buf.ms);
-    balance_count_kernel<<<dim3((unsigned)capped((n + 255) / 256)), dim3(256), 0, s>>>(labels, n, (uint32_t)N,
-                                                                                        (uint32_t)K, S, valid, counts,
-                                                                                        buf.nvalid);
+    balance_count_kernel<<<dim3((unsigned)capped((n + 255) / 256)), dim3(256), 0, s>>>(
+        labels, n, (uint32_t)N, (uint32_t)K, S, valid, out.counts, buf.vpart);
   }
-  const int64_t chunks = balance_chunks(N);
+  const int64_t chunks = balance_wide_chunks(N);
   const int kblocks = (K + 255) / 256;
   const int64_t units = B * chunks * kblocks;
   balance_cols_kernel<T><<<dim3((unsigned)capped(units)), dim3(256), 0, s>>>(x, N, K, chunks, kblocks, units, buf.ms,
                                                                               buf.part);
-  balance_finish_kernel<<<dim3((unsigned)B), dim3(256), 0, s>>>(buf.part, chunks, K, S, counts, buf.nvalid, loss, prob,
-                                                                coef);
-  return hipGetLastError();
+  return join(JoinIn{buf.part, chunks, out.counts, 1, buf.vpart, 1}, K, S, B, out, buf.terms, s);
 }
 
 template <class T>
 hipError_t balance_grad_t(const void* logits, int64_t N, int K, int B, const float* lse, const float* coef,
                           const float* dloss, void* dlogits, hipStream_t s) {
+  constexpr int VEC = 16 / T::SZ;
+  if (K <= kBalanceMaxK) {
+    auto go = [&](auto team) {
+      using P = decltype(team);
+      return rows_backward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, lse, coef, dloss, dlogits, s);
+    };
+    return vec_width(K, logits, T::SZ, dlogits, T::SZ) >= VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+  }
   const int64_t n = N * B;
-  balance_grad_kernel<T><<<dim3((unsigned)capped((n + 3) / 4)), dim3(256), 0, s>>>(
+  balance_grad_wide_kernel<T><<<dim3((unsigned)capped((n + 3) / 4)), dim3(256), 0, s>>>(
       static_cast<const typename T::raw*>(logits), n, (uint32_t)N, K, lse, coef, dloss,
       static_cast<typename T::raw*>(dlogits));
   return hipGetLastError();
@@ -199,10 +637,11 @@ hipError_t balance_grad_t(const void* logits, int64_t N, int K, int B, const flo
 hipError_t launch_balance(int dt, const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
                           const uint8_t* valid, float* loss, int32_t* counts, float* prob, float* lse, float* coef,
                           const BalanceBuffers& buf, hipStream_t s) {
+  const BalanceOut out{loss, counts, prob, coef};
   switch (dt) {
-    case DT_F32: return balance_t<F32>(logits, N, K, B, labels, S, valid, loss, counts, prob, lse, coef, buf, s);
-    case DT_F16: return balance_t<F16>(logits, N, K, B, labels, S, valid, loss, counts, prob, lse, coef, buf, s);
-    case DT_BF16: return balance_t<BF16>(logits, N, K, B, labels, S, valid, loss, counts, prob, lse, coef, buf, s);
+    case DT_F32: return balance_t<F32>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
+    case DT_F16: return balance_t<F16>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
+    case DT_BF16: return balance_t<BF16>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -90,14 +90,19 @@ GradLayout grad_layout(int64_t N, int K, int B) {
 }
 
 struct BalanceLayout {
-  size_t part, nvalid, ms, total;
+  size_t part, cpart, vpart, terms, ms, total;
 };
 BalanceLayout balance_layout(int64_t N, int K, int B) {
   BalanceLayout L{};
-  size_t o = 0;
-  L.part = o;    o = al256(o + (size_t)B * balance_chunks(N) * K * 8);
-  L.nvalid = o;  o = al256(o + (size_t)B * 4);
-  L.ms = o;      o = al256(o + (size_t)B * N * 8);
+  const bool wide = K > kBalanceMaxK;
+  const int64_t chunks = wide ? balance_wide_chunks(N) : balance_split(N, B, K).chunks;
+  const size_t cells = wide || chunks > 1 ? (size_t)B * chunks * K : 0;  // one chunk is finished where it is summed
+  size_t o = 256;
+  L.part = o;   o = al256(o + cells * 4);
+  L.cpart = o;  o = al256(o + (wide ? 0 : cells * 4));
+  L.vpart = o;  o = al256(o + (wide ? (size_t)B : (size_t)B * chunks) * 4);
+  L.terms = o;  o = al256(o + (size_t)B * ((K + kBalanceJoinCols - 1) / kBalanceJoinCols) * 8);
+  L.ms = o;     o = al256(o + (wide ? (size_t)B * N * 8 : 0));
   L.total = o;
   return L;
 }
@@ -108,8 +113,14 @@ int check_grad_shape(int64_t N, int32_t K, int32_t D, int32_t B) {
   return check_d(D);
 }
 
-int check_balance_shape(int64_t N, int32_t K, int32_t B, int32_t S) {
+// A workgroup per instance at least, and a launch's threads are counted in 32 bits.
+int check_balance_sizes(int64_t N, int32_t K, int32_t B) {
   if (int rc = check_sizes(N, K, B)) return rc;
+  if (B > (1 << 22)) return fail(KM_EINVAL, "B=%d must be <= %d", B, 1 << 22);
+  return KM_OK;
+}
+int check_balance_shape(int64_t N, int32_t K, int32_t B, int32_t S) {
+  if (int rc = check_balance_sizes(N, K, B)) return rc;
   if (S < 1) return fail(KM_EINVAL, "S=%d must be >= 1", S);
   if (N * B * (int64_t)S >= kMax31) return fail(KM_EINVAL, "B*N*S must be < 2^31");
   return KM_OK;
@@ -202,8 +213,12 @@ int kmeans_balance(const void* logits, int32_t dtype, int64_t N, int32_t K, int3
                       {"workspace", ws, L.total, 1, true}};
   if (int rc = check_arrays(arrs)) return rc;
   char* base = static_cast<char*>(ws);
-  const BalanceBuffers buf{reinterpret_cast<double*>(base + L.part), reinterpret_cast<int32_t*>(base + L.nvalid),
-                           reinterpret_cast<float2*>(base + L.ms)};
+  BalanceBuffers buf{};
+  buf.part = reinterpret_cast<float*>(base + L.part);
+  buf.cpart = reinterpret_cast<int32_t*>(base + L.cpart);
+  buf.vpart = reinterpret_cast<int32_t*>(base + L.vpart);
+  buf.terms = reinterpret_cast<double*>(base + L.terms);
+  buf.ms = reinterpret_cast<float2*>(base + L.ms);
   KM_HIP(launch_balance(dtype, logits, N, K, B, labels, S, valid, loss, counts, prob, lse, coef, buf,
                         (hipStream_t)stream),
          "balance launch");
@@ -214,7 +229,7 @@ int kmeans_balance_grad(const void* logits, int32_t dtype, int64_t N, int32_t K,
                         const float* coef, const float* dloss, void* dlogits, void* stream) {
   err_buf()[0] = 0;
   if (int rc = check_type(dtype, "dtype")) return rc;
-  if (int rc = check_sizes(N, K, B)) return rc;
+  if (int rc = check_balance_sizes(N, K, B)) return rc;
   const uint64_t n = (uint64_t)N * B, e = (uint64_t)B * K, sz = dtype_size(dtype);
   const Arr arrs[] = {{"logits", logits, n * K * sz, (unsigned)sz, false},
                       {"lse", lse, n * 4, 4, false},

@@ -237,13 +237,37 @@ hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const uint2* so
                              float scale, bool acc, void* grad, hipStream_t s);
 
 // Balance loss and its gradient (see flashkm_codebook.h for the formulas).
-struct BalanceBuffers {
-  double* part;     // [B, balance_chunks(N), K] column sums of the probabilities
-  int32_t* nvalid;  // [B]
-  float2* ms;       // [B, N] row maximum and 1 / sum of exponentials
+constexpr int kBalanceMaxK = 16384;   // longest rows kept in registers
+constexpr int kBalanceJoinCols = 32;  // fewest columns per workgroup that joins chunk sums
+constexpr int kBalanceRows = 256;     // rows per column-sum chunk of longer rows
+// Rows a workgroup takes at a time: 4 waves of 64 / LPR rows, LPR lanes of 8
+// elements a row, up to 512; then a wave (16 elements a lane), 4 or 16 waves a row.
+constexpr int balance_step(int K) {
+  int lpr = 1;
+  while (lpr < 64 && lpr * 8 < K) lpr *= 2;
+  return K > 1024 ? 1 : 4 * (64 / lpr);
+}
+// Steps per workgroup and chunks (workgroups) per instance of N rows.
+struct BalanceSplit {
+  int steps;
+  int64_t chunks;
 };
-constexpr int kBalanceRows = 256;  // rows per column-sum chunk
-inline int64_t balance_chunks(int64_t N) { return N > 0 ? (N + kBalanceRows - 1) / kBalanceRows : 1; }
+inline BalanceSplit balance_split(int64_t N, int B, int K) {
+  const int64_t blocks = K > 4096 ? 512 : 2048;  // 1,024 or 256 threads each
+  const int64_t want = blocks / B > 1 ? blocks / B : 1;
+  const int64_t all = (N + balance_step(K) - 1) / balance_step(K);
+  int64_t steps = (all + want - 1) / want;
+  if (steps < 4) steps = 4;
+  return BalanceSplit{(int)steps, all > 0 ? (all + steps - 1) / steps : 1};
+}
+inline int64_t balance_wide_chunks(int64_t N) { return N > 0 ? (N + kBalanceRows - 1) / kBalanceRows : 1; }
+struct BalanceBuffers {
+  float* part;     // [B, chunks, K] column sums of the probabilities
+  int32_t* cpart;  // [B, chunks, K] counts (rows in registers)
+  int32_t* vpart;  // [B, chunks] valid rows (longer rows: [B])
+  double* terms;   // [B, ceil(K / kBalanceJoinCols)] terms of the loss
+  float2* ms;      // [B, N] row maximum and 1 / sum of exponentials (longer rows)
+};
 hipError_t launch_balance(int dt, const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
                           const uint8_t* valid, float* loss, int32_t* counts, float* prob, float* lse, float* coef,
                           const BalanceBuffers& buf, hipStream_t s);

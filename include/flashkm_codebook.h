@@ -74,6 +74,7 @@ KM_API size_t kmeans_balance_workspace_bytes(int64_t N, int32_t K, int32_t B, in
  * outside [0,K) names nothing but stays in the S T that counts are divided
  * by), valid [B,N] bytes (nullable: every row; non-zero = valid); loss [B]
  * fp32, counts [B,K] int32, prob [B,K] fp32, lse [B,N] fp32, coef [B,K] fp32.
+ * At most 2^22 instances.
  * T = 0 gives loss, prob and coef 0.  A valid row whose logits are all -inf
  * has lse -inf and leaves no probability (it still counts in T).  A choice with
  * logit -inf has probability 0.  Balanced use gives loss 1. */
