@@ -75,16 +75,23 @@ int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
 
 // ---- workspaces --------------------------------------------------------------
 struct GradLayout {
-  size_t kv0, kv1, hist, dtot, total;
+  size_t kv0, kv1, hist, dtot, frag[3], any[3], total;
 };
-GradLayout grad_layout(int64_t N, int K, int B) {
+GradLayout grad_layout(int64_t N, int K, int D, int B) {
   GradLayout L{};
   const int64_t n = N * B;
-  size_t o = 0;
-  L.kv0 = o;   o = al256(o + (size_t)n * 8);
-  L.kv1 = o;   o = al256(o + (size_t)n * 8);
-  L.hist = o;  o = al256(o + (n ? (size_t)sort_hist_words(N, B, K + 1) * 4 : 0));
-  L.dtot = o;  o = al256(o + ((size_t)1 << kSortWideBits) * 4);
+  size_t o = 256;
+  if (n > kGradDirect) {
+    L.kv0 = o;   o = al256(o + (size_t)n * 8);
+    L.kv1 = o;   o = al256(o + (size_t)n * 8);
+    L.hist = o;  o = al256(o + (size_t)sort_hist_words(N, B, K) * 4);
+    L.dtot = o;  o = al256(o + ((size_t)1 << kSortWideBits) * 4);
+    for (int i = 0; i < 3; ++i) {
+      const size_t units = (size_t)grad_units(n, D, i);
+      L.frag[i] = o;  o = al256(o + units * 2 * ((D + 3) / 4 * 4) * 4);
+      L.any[i] = o;   o = al256(o + units * 2 * 4);
+    }
+  }
   L.total = o;
   return L;
 }
@@ -109,7 +116,6 @@ BalanceLayout balance_layout(int64_t N, int K, int B) {
 
 int check_grad_shape(int64_t N, int32_t K, int32_t D, int32_t B) {
   if (int rc = check_sizes(N, K, B)) return rc;
-  if ((int64_t)B * K + B >= kMax31) return fail(KM_EINVAL, "B*(K+1) must be < 2^31");
   return check_d(D);
 }
 
@@ -150,7 +156,7 @@ int kmeans_embed(const void* table, int32_t table_dtype, int64_t N, int32_t K, i
 
 size_t kmeans_embed_grad_workspace_bytes(int64_t N, int32_t K, int32_t D, int32_t B) {
   if (check_grad_shape(N, K, D, B) != KM_OK) return 0;
-  return grad_layout(N, K, B).total;
+  return grad_layout(N, K, D, B).total;
 }
 
 int kmeans_embed_grad(const void* dout, int32_t dout_dtype, int64_t N, int32_t K, int32_t D, int32_t B,
@@ -160,7 +166,7 @@ int kmeans_embed_grad(const void* dout, int32_t dout_dtype, int64_t N, int32_t K
   if (int rc = check_type(dout_dtype, "dout dtype")) return rc;
   if (int rc = check_type(grad_dtype, "grad dtype")) return rc;
   if (int rc = check_grad_shape(N, K, D, B)) return rc;
-  const GradLayout L = grad_layout(N, K, B);
+  const GradLayout L = grad_layout(N, K, D, B);
   if (int rc = check_workspace(ws, ws_bytes, L.total)) return rc;
   const uint64_t n = (uint64_t)N * B, isz = dtype_size(dout_dtype), gsz = dtype_size(grad_dtype);
   const Arr arrs[] = {{"dout", dout, n * D * isz, (unsigned)isz, false},
@@ -171,19 +177,17 @@ int kmeans_embed_grad(const void* dout, int32_t dout_dtype, int64_t N, int32_t K
   if (n == 0 && accumulate) return KM_OK;
   char* base = static_cast<char*>(ws);
   hipStream_t s = (hipStream_t)stream;
-  const uint2* sorted = nullptr;
-  if (n) {
-    SortBuffers sort{};
-    sort.kv[0] = reinterpret_cast<uint2*>(base + L.kv0);
-    sort.kv[1] = reinterpret_cast<uint2*>(base + L.kv1);
-    sort.hist = reinterpret_cast<uint32_t*>(base + L.hist);
-    sort.hist_words = (int64_t)((L.dtot - L.hist) / 4);
-    sort.dtot = reinterpret_cast<uint32_t*>(base + L.dtot);
-    // id K of every instance collects the ids outside [0, K): the sort clamps
-    // what lies outside [0, K + 1) to it
-    KM_HIP(launch_argsort_labels(ids, N, B, K + 1, sort, &sorted, s), "argsort launch");
+  GradBuffers buf{};
+  buf.sort.kv[0] = reinterpret_cast<uint2*>(base + L.kv0);
+  buf.sort.kv[1] = reinterpret_cast<uint2*>(base + L.kv1);
+  buf.sort.hist = reinterpret_cast<uint32_t*>(base + L.hist);
+  buf.sort.hist_words = (int64_t)((L.dtot - L.hist) / 4);
+  buf.sort.dtot = reinterpret_cast<uint32_t*>(base + L.dtot);
+  for (int i = 0; i < 3; ++i) {
+    buf.frag[i] = reinterpret_cast<float*>(base + L.frag[i]);
+    buf.any[i] = reinterpret_cast<uint32_t*>(base + L.any[i]);
   }
-  KM_HIP(launch_embed_grad(dout_dtype, grad_dtype, dout, sorted, (int64_t)n, K, D, B, scale, accumulate != 0, grad, s),
+  KM_HIP(launch_embed_grad(dout_dtype, grad_dtype, dout, ids, N, K, D, B, scale, accumulate != 0, grad, buf, s),
          "embed gradient launch");
   return KM_OK;
 }

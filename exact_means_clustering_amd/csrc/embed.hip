@@ -10,6 +10,13 @@ namespace fkm {
 
 namespace {
 
+// Entries a wave zeroes at a time: about 32 KB of them, 64 at most.
+int zero_per(int64_t row_bytes) {
+  const int64_t e = 32768 / row_bytes;
+  return e < 1 ? 1 : e > 64 ? 64 : (int)e;
+}
+int64_t zero_grid(int64_t blocks) { return blocks < (1 << 20) ? blocks : (1 << 20); }
+
 constexpr int kVecs = 4;                  // vectors in flight per thread
 constexpr int kTileVecs = 256 * kVecs;    // vectors per workgroup tile
 
@@ -85,68 +92,407 @@ hipError_t embed_v(const void* table, const int32_t* ids, int64_t N, int K, int 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// One wave per table entry and slab of 64 vectors.
-template <class TI, class TO, int V>
-__global__ __launch_bounds__(256) void embed_grad_kernel(const typename TI::raw* __restrict__ dout,
-                                                         const uint2* __restrict__ kv, int64_t n, uint32_t K,
-                                                         int64_t entries, int nv, int nslab, float scale, bool acc,
-                                                         typename TO::raw* __restrict__ grad) {
-  const int lane = lane_id();
-  const int64_t units = entries * nslab;
-  for (int64_t u = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); u < units; u += (int64_t)gridDim.x * 4) {
-    const int64_t e = u / nslab;
-    const int c = (int)(u - e * nslab) * 64 + lane;
-    const uint32_t key = (uint32_t)(e + e / K);  // b * (K + 1) + id
-    int64_t lo = 0, hi = n;                      // first sorted position with this key
-    while (lo < hi) {
-      const int64_t m = (lo + hi) >> 1;
-      if (kv[m].x < key) lo = m + 1;
-      else hi = m;
-    }
-    float a[V];
+// Entry e of the gradient gets the sum `a` of its rows (V values at column
+// `col` of it); `any`: whether a row that counts was among them.  An entry
+// without such a row is zero, or stays as it is when accumulating.
+template <class TO, int V>
+__device__ __forceinline__ void put_grad(typename TO::raw* grad, int64_t at, const float (&a)[V], float scale, bool acc,
+                                         bool any) {
+  if (acc && !any) return;
+  Pack<TO, V> o;
+  float r[V];
+  if (acc) {
+    o.load(grad + at);
+    o.unpack(r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = 0.f;
-    int64_t j = lo;
-    for (; j < n; ++j) {
-      const uint2 q = kv[j];
-      if (q.x != key) break;
-      if (c < nv) {
-        Pack<TI, V> p;
-        float f[V];
-        p.load(dout + ((int64_t)q.y * nv + c) * V);
-        p.unpack(f);
+    for (int i = 0; i < V; ++i) r[i] = fmaf(scale, a[i], r[i]);
+  } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) a[i] += f[i];
-      }
-    }
-    if (c >= nv || (acc && j == lo)) continue;
-    typename TO::raw* g = grad + (e * nv + c) * V;
-    Pack<TO, V> o;
-    float old[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) old[i] = 0.f;
-    if (acc) {
-      o.load(g);
-      o.unpack(old);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) a[i] = j == lo ? 0.f : acc ? fmaf(scale, a[i], old[i]) : scale * a[i];
-    o.pack(a);
-    o.store(g);
+    for (int i = 0; i < V; ++i) r[i] = any ? scale * a[i] : 0.f;
+  }
+  o.pack(r);
+  o.store(grad + at);
+}
+
+// Zeros into `count` entries from e0 whose bit in `absent` is set; one wave.
+template <class TO, int V>
+__device__ __forceinline__ void zero_entries(typename TO::raw* __restrict__ grad, int64_t e0, uint64_t absent,
+                                             int nv, int lane) {
+  Pack<TO, V> z;
+  z.zero();
+  for (; absent; absent &= absent - 1) {
+    const int64_t e = e0 + __ffsll((unsigned long long)absent) - 1;
+    for (int c = lane; c < nv; c += 64) z.store(grad + (e * nv + c) * V);
   }
 }
 
+// Few rows (n <= kGradDirect): no sort.  A wave takes row i and a slab of 64
+// vectors; if no earlier row has its id, it adds every row of that id in
+// order.  Further workgroups zero the entries that no row names, each
+// looking for its own range of entries among the ids.
 template <class TI, class TO, int V>
-hipError_t embed_grad_v(const void* dout, const uint2* sorted, int64_t n, int K, int D, int B, float scale, bool acc,
-                        void* grad, hipStream_t s) {
+__global__ __launch_bounds__(256) void embed_grad_direct_kernel(const typename TI::raw* __restrict__ dout,
+                                                                const int32_t* __restrict__ ids, int n, uint32_t N,
+                                                                uint32_t K, int64_t entries, int nv, int nslab,
+                                                                int64_t row_blocks, int64_t units, int per, float scale,
+                                                                bool acc, typename TO::raw* __restrict__ grad) {
+  __shared__ uint32_t key[kGradDirect];  // entry of every row, ~0 for none
+  __shared__ unsigned long long named[4];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  if (tid < n) {
+    const uint32_t id = (uint32_t)ids[tid];
+    key[tid] = id < K ? (uint32_t)tid / N * K + id : ~0u;
+  }
+  if (tid < 4) named[tid] = 0;
+  __syncthreads();
+  if ((int64_t)blockIdx.x < row_blocks) {
+    const int64_t u = (int64_t)blockIdx.x * 4 + w;
+    const int i = (int)(u / nslab);
+    if (i >= n) return;
+    const uint32_t k = key[i];
+    if (k == ~0u) return;
+    uint64_t same[kGradDirect / 64];
+#pragma unroll
+    for (int q = 0; q < kGradDirect / 64; ++q) {
+      const int j = q * 64 + lane;
+      same[q] = __ballot(j < n && key[j] == k);
+      // an earlier row of this entry: that row's wave does the work
+      const int below = i - q * 64;
+      const uint64_t earlier = below <= 0 ? 0ull : below >= 64 ? ~0ull : (1ull << below) - 1;
+      if (same[q] & earlier) return;
+    }
+    const int c = (int)(u - (int64_t)i * nslab) * 64 + lane;
+    if (c >= nv) return;
+    float a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = 0.f;
+#pragma unroll
+    for (int q = 0; q < kGradDirect / 64; ++q) {
+#pragma unroll 4
+      for (uint64_t m = same[q]; m; m &= m - 1) {
+        const int j = q * 64 + __ffsll((unsigned long long)m) - 1;
+        Pack<TI, V> p;
+        float f[V];
+        p.load(dout + ((int64_t)j * nv + c) * V);
+        p.unpack(f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] += f[v];
+      }
+    }
+    put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, true);
+    return;
+  }
+  // zeros: a workgroup takes 4 waves of `per` (at most 64) entries at a time
+  for (int64_t u = (int64_t)blockIdx.x - row_blocks; u < units; u += gridDim.x - row_blocks) {
+    const int64_t e0 = (u * 4) * per, e1 = e0 + 4 * per;
+    if (tid < n) {
+      const uint32_t k = key[tid];
+      if (k != ~0u && (int64_t)k >= e0 && (int64_t)k < e1)
+        atomicOr(&named[(k - e0) / per], 1ull << ((k - e0) % per));
+    }
+    __syncthreads();
+    const int64_t we = e0 + (int64_t)w * per;
+    const int64_t left = entries - we;
+    const int cnt = left <= 0 ? 0 : left < per ? (int)left : per;
+    const uint64_t range = cnt <= 0 ? 0ull : cnt >= 64 ? ~0ull : (1ull << cnt) - 1;
+    zero_entries<TO, V>(grad, we, ~named[w] & range, nv, lane);
+    __syncthreads();
+    if (tid < 4) named[tid] = 0;
+    __syncthreads();
+  }
+}
+
+// Level 1.  A group of LPR lanes, one vector each, takes a unit of U sorted
+// rows and a slab of LPR vectors, and adds the rows of each segment in order,
+// 8 row loads in flight.  A segment inside the unit is finished here; a piece
+// that continues from the left goes to the unit's fragment 0, one that starts
+// here and continues to the right to fragment 1.  Rows whose word carries the
+// mark leave nothing.  The workgroups past the sums zero the entries no row
+// has (not when accumulating), finding each by a binary search.
+constexpr int kAhead = 8;
+template <class TI, class TO, int V, int LPR>
+__global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::raw* __restrict__ dout,
+                                                             const uint2* __restrict__ kv, int64_t n, uint32_t mark,
+                                                             int U, int64_t units, int64_t sum_blocks, int nv,
+                                                             int nslab, int64_t entries, int per, float scale, bool acc,
+                                                             typename TO::raw* __restrict__ grad,
+                                                             float* __restrict__ frag, uint32_t* __restrict__ fany,
+                                                             int Dp) {
+  const int lane = lane_id();
+  const int w = threadIdx.x >> 6;
+  if ((int64_t)blockIdx.x >= sum_blocks) {
+    const int64_t zero_units = (entries + per - 1) / per;
+    for (int64_t u = ((int64_t)blockIdx.x - sum_blocks) * 4 + w; u < zero_units;
+         u += ((int64_t)gridDim.x - sum_blocks) * 4) {
+      const int64_t e = u * per + lane;
+      bool absent = false;
+      if (lane < per && e < entries) {
+        int64_t lo = 0, hi = n;  // first sorted position with a key of at least e
+        while (lo < hi) {
+          const int64_t m = (lo + hi) >> 1;
+          if ((int64_t)kv[m].x < e) lo = m + 1;
+          else hi = m;
+        }
+        absent = lo == n || (int64_t)kv[lo].x != e;
+      }
+      zero_entries<TO, V>(grad, u * per, __ballot(absent), nv, lane);
+    }
+    return;
+  }
+  constexpr int GPB = 256 / LPR;  // groups per workgroup
+  const int64_t q = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR;
+  const int64_t unit = q / nslab;
+  if (unit >= units) return;
+  const int slab = (int)(q - unit * nslab);
+  const int c = slab * LPR + threadIdx.x % LPR;
+  const bool on = c < nv;
+  const int64_t j0 = unit * U, j1 = j0 + U < n ? j0 + U : n;
+  uint32_t cur = kv[j0].x;
+  bool left = j0 > 0 && kv[j0 - 1].x == cur;
+  const bool more = j1 < n && kv[j1].x == kv[j1 - 1].x;  // the last segment continues to the right
+  float a[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = 0.f;
+  bool any = false;
+  auto to_frag = [&](int which) {
+    if (on) {
+      float* f = frag + (unit * 2 + which) * Dp + c * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = a[v];
+    }
+    if (slab == 0 && threadIdx.x % LPR == 0) fany[unit * 2 + which] = any;
+  };
+  const typename TI::raw* base = dout + (int64_t)c * V;
+  const int64_t pitch = (int64_t)nv * V;
+  for (int64_t j = j0; j < j1; j += kAhead) {
+    uint2 e[kAhead];
+    if (j + kAhead <= j1) {
+      const uint4* p = reinterpret_cast<const uint4*>(kv + j);  // units start at multiples of 16 rows
+#pragma unroll
+      for (int i = 0; i < kAhead / 2; ++i) {
+        const uint4 t = p[i];
+        e[2 * i] = make_uint2(t.x, t.y), e[2 * i + 1] = make_uint2(t.z, t.w);
+      }
+    } else {
+      const uint32_t last = kv[j1 - 1].x;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) e[i] = j + i < j1 ? kv[j + i] : make_uint2(last, mark);
+    }
+    Pack<TI, V> p[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (on && !(e[i].y & mark)) p[i].load(base + (int64_t)e[i].y * pitch);
+      else p[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (e[i].x != cur) {
+        if (left) to_frag(0);
+        else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, scale, acc, any);
+        cur = e[i].x;
+        left = any = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] = 0.f;
+      }
+      float f[V];
+      p[i].unpack(f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) a[v] += f[v];
+      any |= !(e[i].y & mark);
+    }
+  }
+  if (left) to_frag(0);
+  else if (more) to_frag(1);
+  else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, scale, acc, any);
+}
+
+// Joins the fragments of up to 64 consecutive units of W sorted rows from
+// unit u0 (of `units`), one wave, V columns a lane.  Segments that end inside
+// are finished; what crosses the joined range's edges goes to its fragments
+// by the same rule.
+template <class TO, int V>
+__device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t n, int64_t W, int64_t u0,
+                                           int64_t units, const float* frag, const uint32_t* fany, int64_t fbase,
+                                           int Dp, int nv, int c, bool on, float scale, bool acc,
+                                           typename TO::raw* __restrict__ grad, float* ofrag, uint32_t* oany,
+                                           int64_t obase, int oDp, int oc, bool flag_lane) {
+  const int lane = lane_id();
+  const int64_t u = u0 + lane;
+  bool from_left = false, to_right = false, one = false;
+  uint32_t kl = 0, kf = 0;
+  if (lane < 64 && u < units) {
+    const int64_t r0 = u * W, r1 = r0 + W < n ? r0 + W : n;
+    kf = kv[r0].x, kl = kv[r1 - 1].x;
+    from_left = r0 > 0 && kv[r0 - 1].x == kf;
+    to_right = r1 < n && kv[r1].x == kl;
+    one = kf == kl;
+  }
+  const uint64_t L = __ballot(from_left), R = __ballot(to_right), O = __ballot(one);
+  const int count = units - u0 < 64 ? (int)(units - u0) : 64;
+  float a[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = 0.f;
+  bool any = false, left = true, open = (L & 1) != 0;  // a piece that comes from the left of the range is open at its start
+  constexpr int kB = 4;  // units whose fragments are loaded together
+  for (int i0 = 0; i0 < count; i0 += kB) {
+    if (((L | R) >> i0 & ((1ull << kB) - 1)) == 0) continue;
+    float f0[kB][V], f1[kB][V];
+    uint32_t n0[kB], n1[kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int b = i0 + i;
+      const bool l = b < 64 && (L >> b & 1), r = b < 64 && (R >> b & 1) && !(l && (O >> b & 1));
+      n0[i] = n1[i] = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) f0[i][v] = f1[i][v] = 0.f;
+      const int64_t at = (u0 + b - fbase) * 2;
+      if (l) {
+        n0[i] = fany[at];
+        if (on) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) f0[i][v] = frag[at * Dp + c * V + v];
+        }
+      }
+      if (r) {
+        n1[i] = fany[at + 1];
+        if (on) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) f1[i][v] = frag[(at + 1) * Dp + c * V + v];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int b = i0 + i;
+      if (b >= count) break;
+      const bool l = L >> b & 1, r = R >> b & 1, whole = l && r && (O >> b & 1);
+      if (l) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] += f0[i][v];
+        any |= n0[i] != 0;
+        if (!whole) {  // the segment ends in this unit
+          const uint32_t k = __shfl(kf, b);
+          if (left) {
+            if (on) {
+#pragma unroll
+              for (int v = 0; v < V; ++v) ofrag[(obase * 2) * oDp + oc * V + v] = a[v];
+            }
+            if (flag_lane) oany[obase * 2] = any;
+          } else if (on) {
+            put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, any);
+          }
+          open = false;
+        }
+      }
+      if (r && !whole) {  // a segment starts here and goes on
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] = f1[i][v];
+        any = n1[i] != 0;
+        left = false;
+        open = true;
+      } else if (!l) {
+        left = false;
+      }
+    }
+  }
+  if (open) {  // a piece continues to the right of the range
+    const int which = left ? 0 : 1;
+    if (on) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) ofrag[(obase * 2 + which) * oDp + oc * V + v] = a[v];
+    }
+    if (flag_lane) oany[obase * 2 + which] = any;
+  }
+}
+
+// One workgroup joins kJoin units (16 waves of 64, then one wave joins the
+// 16) for a slab of 64 vectors of V columns.
+template <class TO, int V>
+__global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __restrict__ kv, int64_t n, int64_t W,
+                                                               int64_t units, int nslab, const float* __restrict__ frag,
+                                                               const uint32_t* __restrict__ fany, int Dp, int nv,
+                                                               float scale, bool acc,
+                                                               typename TO::raw* __restrict__ grad,
+                                                               float* __restrict__ ofrag, uint32_t* __restrict__ oany) {
+  __shared__ float sfrag[16 * 2][64 * V];
+  __shared__ uint32_t sany[16 * 2];
+  const int lane = lane_id();
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t g = blockIdx.x / nslab;
+  const int slab = (int)(blockIdx.x - g * nslab);
+  const int c = slab * 64 + lane;
+  const bool on = c < nv;
+  const int64_t u0 = g * kJoin + w * 64;
+  if (u0 < units)
+    join_units<TO, V>(kv, n, W, u0, units, frag, fany, 0, Dp, nv, c, on, scale, acc, grad, &sfrag[0][0], sany, w,
+                      64 * V, lane, lane == 0);
+  __syncthreads();
+  if (w == 0) {
+    const int64_t all = (units + 63) / 64, s0 = g * 16;
+    const int64_t s1 = s0 + 16 < all ? s0 + 16 : all;
+    // the 16 joined ranges are units of 64 W rows; their fragments are in LDS
+    join_units<TO, V>(kv, n, 64 * W, s0, s1, &sfrag[0][0] + (lane - c) * V, sany, s0, 64 * V, nv, c, on, scale, acc,
+                      grad, ofrag, oany, g, Dp, c, lane == 0 && slab == 0);
+  }
+}
+
+template <class TI, class TO, int V, int LPR>
+void sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, int U, int64_t units, int nv,
+                int64_t entries, float scale, bool acc, void* grad, float* frag, uint32_t* fany, int Dp,
+                hipStream_t s) {
+  const int nslab = (nv + LPR - 1) / LPR;
+  const int64_t sum_blocks = (units * nslab + 256 / LPR - 1) / (256 / LPR);
+  const int per = zero_per(nv * V * TO::SZ);
+  const int64_t zero_blocks = acc ? 0 : zero_grid((entries + 4 * per - 1) / (4 * per));
+  if (sum_blocks + zero_blocks == 0) return;
+  embed_grad_sum_kernel<TI, TO, V, LPR><<<dim3((unsigned)(sum_blocks + zero_blocks)), dim3(256), 0, s>>>(
+      static_cast<const typename TI::raw*>(dout), kv, n, mark, U, units, sum_blocks, nv, nslab, entries, per, scale,
+      acc, static_cast<typename TO::raw*>(grad), frag, fany, Dp);
+}
+
+template <class TI, class TO, int V>
+hipError_t embed_grad_v(const void* dout, const int32_t* ids, int64_t N, int K, int D, int B, float scale, bool acc,
+                        void* grad, GradBuffers& buf, hipStream_t s) {
+  const int64_t n = N * B, entries = (int64_t)B * K;
   const int nv = D / V;
-  const int nslab = (nv + 63) / 64;
-  const int64_t entries = (int64_t)B * K;
-  const int64_t blocks = (entries * nslab + 3) / 4;
-  const int64_t grid = blocks < (1 << 22) ? blocks : (1 << 22);
-  embed_grad_kernel<TI, TO, V><<<dim3((unsigned)grid), dim3(256), 0, s>>>(
-      static_cast<const typename TI::raw*>(dout), sorted, n, (uint32_t)K, entries, nv, nslab, scale, acc,
-      static_cast<typename TO::raw*>(grad));
+  if (n <= kGradDirect) {
+    const int nslab = (nv + 63) / 64;
+    const int per = zero_per(D * TO::SZ);
+    const int64_t row_blocks = (n * nslab + 3) / 4;
+    const int64_t units = acc ? 0 : (entries + 4 * per - 1) / (4 * per);
+    const int64_t blocks = row_blocks + zero_grid(units);
+    embed_grad_direct_kernel<TI, TO, V><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(
+        static_cast<const typename TI::raw*>(dout), ids, (int)n, (uint32_t)N, (uint32_t)K, entries, nv, nslab,
+        row_blocks, units, per, scale, acc, static_cast<typename TO::raw*>(grad));
+    return hipGetLastError();
+  }
+  const uint2* kv = nullptr;
+  uint32_t mark = 0;
+  const hipError_t e = launch_argsort_marked(ids, N, B, K, buf.sort, &kv, &mark, s);
+  if (e != hipSuccess) return e;
+  const int U = grad_unit(n, D);
+  const int Dp = (D + 3) / 4 * 4;
+  int64_t units = grad_units(n, D, 0);
+#define FKM_SUM(LPR) \
+  sum_launch<TI, TO, V, LPR>(dout, kv, n, mark, U, units, nv, entries, scale, acc, grad, buf.frag[0], buf.any[0], Dp, s)
+  if (nv <= 4) FKM_SUM(4);
+  else if (nv <= 8) FKM_SUM(8);
+  else if (nv <= 16) FKM_SUM(16);
+  else if (nv <= 32) FKM_SUM(32);
+  else FKM_SUM(64);
+#undef FKM_SUM
+  constexpr int VJ = V >= 4 ? 4 : 1;
+  const int nslab = (D / VJ + 63) / 64;
+  int64_t W = U;
+  for (int level = 0; units > 1; ++level) {
+    const int64_t groups = (units + kJoin - 1) / kJoin;
+    const int waves = units < kJoin ? (int)((units + 63) / 64) : 16;
+    embed_grad_join_kernel<TO, VJ><<<dim3((unsigned)(groups * nslab)), dim3(waves * 64), 0, s>>>(
+        kv, n, W, units, nslab, buf.frag[level], buf.any[level], Dp, D / VJ, scale, acc,
+        static_cast<typename TO::raw*>(grad), buf.frag[level + 1], buf.any[level + 1]);
+    W *= kJoin;
+    units = groups;
+  }
   return hipGetLastError();
 }
 
@@ -182,14 +528,14 @@ hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids,
   });
 }
 
-hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const uint2* sorted, int64_t n, int K, int D, int B,
-                             float scale, bool acc, void* grad, hipStream_t s) {
+hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* ids, int64_t N, int K, int D, int B,
+                             float scale, bool acc, void* grad, GradBuffers& buf, hipStream_t s) {
   const int w = vec_width(D, dout, dtype_size(idt), grad, dtype_size(gdt));
   return with_type(idt, [&](auto ti) {
     return with_type(gdt, [&](auto to) {
       using TI = decltype(ti);
       using TO = decltype(to);
-      FKM_PAIR(embed_grad_v, w, dout, sorted, n, K, D, B, scale, acc, grad, s)
+      FKM_PAIR(embed_grad_v, w, dout, ids, N, K, D, B, scale, acc, grad, buf, s)
     });
   });
 }

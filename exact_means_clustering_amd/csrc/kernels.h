@@ -164,6 +164,10 @@ struct SortBuffers {
 // first pass's histogram launch.
 hipError_t launch_argsort_labels(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf,
                                  const uint2** sorted, hipStream_t s, const InertiaJob* side = nullptr);
+// The same order, in which the row word of a label outside [0, K) carries the
+// bit *mark (rows are below it).
+hipError_t launch_argsort_marked(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf,
+                                 const uint2** sorted, uint32_t* mark, hipStream_t s);
 
 // ---- segment-local reductions ----------------------------------------------
 #ifndef FKM_SEG_ROWS
@@ -231,10 +235,32 @@ hipError_t launch_zero_bytes(void* p, size_t bytes, hipStream_t s);
 // outside [0, K).
 hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids, int64_t N, int K, int D, int B,
                         float scale, void* out, hipStream_t s);
-// Its gradient from the id-sorted rows (n = 0: no rows, `sorted` unused): grad[k] = (acc ? grad[k] : 0) + scale *
-// (sum of the rows of dout with key k).  Keys are b * (K + 1) + id, with id K for rows that leave nothing.
-hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const uint2* sorted, int64_t n, int K, int D, int B,
-                             float scale, bool acc, void* grad, hipStream_t s);
+// Its gradient: grad[k] = (acc ? grad[k] : 0) + scale * (sum of the rows i of dout with key k = b * K + ids[i]).
+// The rows of the sorted order are summed by units of U rows and slabs of columns; pieces of an entry's segment that
+// cross a unit's edge go to fragments, two per unit, which are joined kJoin units at a time.
+constexpr int64_t kGradDirect = 256;  // up to this many rows the gradient needs no sort
+constexpr int kJoin = 1024;           // units joined by one workgroup (16 waves of 64)
+// Rows per unit for n rows of D columns: 16 to 256, so that the waves (of 512 columns) number about 8,192.
+inline int grad_unit(int64_t n, int D) {
+  const int64_t slabs = (D + 511) / 512, per = D <= 256 ? 512 / (D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256) : 1;
+  int u = 16;
+  while (u < 256 && n * slabs / per / u > 8192) u *= 2;
+  return u;
+}
+struct GradBuffers {
+  SortBuffers sort;
+  // per level: [units, 2, D rounded up to 4] pieces continuing from the left / starting here, and [units, 2] whether
+  // a piece has a row that counts; one unit is left after three levels at most, and a single unit has no fragments
+  float* frag[4];
+  uint32_t* any[4];
+};
+inline int64_t grad_units(int64_t n, int D, int level) {
+  int64_t u = (n + grad_unit(n, D) - 1) / grad_unit(n, D);
+  for (int i = 0; i < level; ++i) u = (u + kJoin - 1) / kJoin;
+  return u;
+}
+hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* ids, int64_t N, int K, int D, int B,
+                             float scale, bool acc, void* grad, GradBuffers& buf, hipStream_t s);
 
 // Balance loss and its gradient (see flashkm_codebook.h for the formulas).
 constexpr int kBalanceMaxK = 16384;   // longest rows kept in registers

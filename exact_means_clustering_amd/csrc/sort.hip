@@ -34,13 +34,21 @@ constexpr int kT = 256;
 
 // Source of the (key, row) pair at position i of a pass's input.  The first
 // pass makes it from the labels (row = i); later passes read the previous
-// pass's output.
-struct LabelSrc {
+// pass's output.  MARK: rows whose label is out of range carry the bit `mark`
+// in their row word (they sort with the last label, like any clamped row).
+template <bool MARK>
+struct LabelSrcT {
   const int32_t* labels;
   int64_t N;      // rows per instance
   uint32_t K;     // centroids per instance
   int B;          // instances
   double invN;    // 1.0 / N, for the instance index
+  uint32_t mark = 0;
+  // row word of label value l at position i
+  __device__ __forceinline__ uint32_t row(uint32_t l, int64_t i) const {
+    if constexpr (MARK) return (uint32_t)i | (l < K ? 0u : mark);
+    else return (uint32_t)i;
+  }
   // key of label value l at position i
   __device__ __forceinline__ uint32_t key(int32_t l, int64_t i) const {
     const uint32_t lab = (uint32_t)l < K ? (uint32_t)l : K - 1;  // out-of-range labels clamp (caller error)
@@ -51,13 +59,16 @@ struct LabelSrc {
     if (b * N > i) --b;
     return (uint32_t)b * K + lab;
   }
-  __device__ __forceinline__ uint2 operator()(int64_t i) const { return make_uint2(key(labels[i], i), (uint32_t)i); }
+  __device__ __forceinline__ uint2 operator()(int64_t i) const {
+    const int32_t l = labels[i];
+    return make_uint2(key(l, i), row((uint32_t)l, i));
+  }
   // A segmented pass's tile lies inside one instance, whose key offset koff
   // = b * K the tile already knows: the key is koff + the clamped label, with
   // no per-element instance division.
   __device__ __forceinline__ uint2 in_instance(int64_t i, uint32_t koff) const {
     const uint32_t l = (uint32_t)labels[i];
-    return make_uint2(koff + (l < K ? l : K - 1), (uint32_t)i);
+    return make_uint2(koff + (l < K ? l : K - 1), row(l, i));
   }
 };
 struct PairSrc {
@@ -80,8 +91,8 @@ struct PackedSrc {
 };
 template <class Src>
 constexpr bool is_label_src = false;
-template <>
-constexpr bool is_label_src<LabelSrc> = true;
+template <bool MARK>
+constexpr bool is_label_src<LabelSrcT<MARK>> = true;
 template <class Src>
 constexpr bool is_pair_src = false;
 template <>
@@ -492,8 +503,8 @@ __global__ __launch_bounds__(kT) void radix_scatter_kernel(Src src, int64_t n, i
 #pragma unroll
     for (int r = 0; r < RW; ++r) {
       const int64_t li = first + r * 64 + lane;
-      e[r] = li < p.lim ? make_uint2(src.key((int32_t)tw[r * 64 + lane], p.row0 + li), (uint32_t)(p.row0 + li))
-                        : make_uint2(0u, 0u);
+      const uint32_t l = tw[r * 64 + lane];
+      e[r] = li < p.lim ? make_uint2(src.key((int32_t)l, p.row0 + li), src.row(l, p.row0 + li)) : make_uint2(0u, 0u);
     }
   }
   if constexpr (kPk) {
@@ -612,16 +623,16 @@ hipError_t one_pass(Src src, int64_t n, int shift, SortBuffers& buf, uint2* out,
 // sorted (key, row) pairs to out.  Half the bytes of the 8-byte intermediate
 // are written, counted and read back.  The low pass's totals stay in
 // dtot[256..511].
-template <int TILE>
-hipError_t packed_two_pass_t(const LabelSrc& ls, int64_t n, SortBuffers& buf, uint2* out, hipStream_t s,
+template <int TILE, class Src>
+hipError_t packed_two_pass_t(const Src& ls, int64_t n, SortBuffers& buf, uint2* out, hipStream_t s,
                              const InertiaJob& side) {
   const int64_t nblk = (n + TILE - 1) / TILE;
   const int64_t extra = side_blocks(side);
   uint32_t* dlo = buf.dtot + 256;
-  radix_hist_kernel<LabelSrc, TILE, false><<<dim3((unsigned)(nblk + extra)), dim3(kT), 0, s>>>(
+  radix_hist_kernel<Src, TILE, false><<<dim3((unsigned)(nblk + extra)), dim3(kT), 0, s>>>(
       ls, n, 0, buf.hist, nblk, nblk, 1, Segs{}, side);
   radix_scan_kernel<<<dim3(256), dim3(kT), 0, s>>>(buf.hist, nblk, dlo);
-  radix_scatter_kernel<LabelSrc, TILE, true, false, 8, true><<<dim3((unsigned)nblk), dim3(kT), 0, s>>>(
+  radix_scatter_kernel<Src, TILE, true, false, 8, true><<<dim3((unsigned)nblk), dim3(kT), 0, s>>>(
       ls, n, 0, buf.hist, dlo, nblk, Segs{}, buf.kv[0]);
   const PackedSrc ps{reinterpret_cast<const uint32_t*>(buf.kv[0]), dlo};
   radix_hist_kernel<PackedSrc, TILE, false><<<dim3((unsigned)nblk), dim3(kT), 0, s>>>(
@@ -646,40 +657,42 @@ hipError_t wide_pass_t(Src src, int64_t n, SortBuffers& buf, uint2* out, hipStre
   return hipGetLastError();
 }
 
-template <int RB>
-hipError_t wide_pass(const LabelSrc& src, int64_t n, SortBuffers& buf, uint2* out, hipStream_t s,
-                     const InertiaJob& side) {
-  return wide_pass_t<LabelSrc, kSortTileSmall, RB>(src, n, buf, out, s, side);  // sort_wide_bits: small tiles only
+template <int RB, class Src>
+hipError_t wide_pass(const Src& src, int64_t n, SortBuffers& buf, uint2* out, hipStream_t s, const InertiaJob& side) {
+  return wide_pass_t<Src, kSortTileSmall, RB>(src, n, buf, out, s, side);  // sort_wide_bits: small tiles only
 }
 
 // One segmented pass: B segments of N keys b*K + label with K <= 256, each
 // tiled on its own, ntb = ceil(N / TILE) <= kScanFreeTiles tiles per segment,
 // B * ntb tiles in all (the histogram holds sort_seg_blocks(N, B) tiles).
-template <int TILE>
-hipError_t seg_pass_t(const LabelSrc& src, int64_t N, int B, uint32_t K, SortBuffers& buf, uint2* out,
+template <int TILE, class Src>
+hipError_t seg_pass_t(const Src& src, int64_t N, int B, uint32_t K, SortBuffers& buf, uint2* out,
                       hipStream_t s, const InertiaJob& side) {
   const int64_t n = N * (int64_t)B;
   const Segs sg{N, (N + TILE - 1) / TILE, K};
   const int64_t nblk = sg.ntb * B;
   const int64_t extra = side_blocks(side);
-  radix_hist_kernel<LabelSrc, TILE, true><<<dim3((unsigned)(nblk + extra)), dim3(kT), 0, s>>>(
+  radix_hist_kernel<Src, TILE, true><<<dim3((unsigned)(nblk + extra)), dim3(kT), 0, s>>>(
       src, n, 0, buf.hist, nblk, 1, 256, sg, side);
-  radix_scatter_kernel<LabelSrc, TILE, false, true><<<dim3((unsigned)nblk), dim3(kT), 0, s>>>(
+  radix_scatter_kernel<Src, TILE, false, true><<<dim3((unsigned)nblk), dim3(kT), 0, s>>>(
       src, n, 0, buf.hist, buf.dtot, nblk, sg, out);
   return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_argsort_labels(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf,
-                                 const uint2** sorted, hipStream_t s, const InertiaJob* side) {
+template <bool MARK>
+hipError_t argsort_labels(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf, const uint2** sorted,
+                          uint32_t* mark, hipStream_t s, const InertiaJob* side) {
   const int64_t n = N * (int64_t)B;
   const int passes = (sort_key_bits(B, K) + 7) / 8;
-  LabelSrc ls{labels, N, (uint32_t)K, B, 1.0 / (double)N};
+  // the row word's free top bit; a packed intermediate keeps 24 bits of it
+  const bool packed = passes == 2 && n < ((int64_t)1 << 24) && sort_blocks(n) > kScanFreeTiles &&
+                      (!MARK || n <= ((int64_t)1 << 23));
+  LabelSrcT<MARK> ls{labels, N, (uint32_t)K, B, 1.0 / (double)N};
   // A workspace laid out for more rows than this call sorts (the streamed
   // path's last chunk) may not hold the histogram of the one-pass variants,
   // whose size is not monotone in the row count: they are taken only if the
   // histogram fits, and the plain passes always fit a layout for at least n.
+  if constexpr (MARK) ls.mark = *mark = 1u << 31;
   const int64_t T = sort_tile(n);
   const bool seg_fits = 256 * ((N + T - 1) / T) * (int64_t)B <= buf.hist_words;
   if (passes > 1 && sort_segmented(N, B, K) && seg_fits) {
@@ -700,7 +713,8 @@ hipError_t launch_argsort_labels(const int32_t* labels, int64_t N, int B, int K,
                       : wide_pass<11>(ls, n, buf, buf.kv[0], s, sj);
   }
   if (256 * sort_blocks(n) > buf.hist_words) return hipErrorInvalidValue;  // workspace laid out for fewer rows
-  if (passes == 2 && n < ((int64_t)1 << 24) && sort_blocks(n) > kScanFreeTiles) {
+  if (packed) {
+    if constexpr (MARK) ls.mark = *mark = 1u << 23;
     *sorted = buf.kv[1];
     const InertiaJob sj = side ? *side : InertiaJob{};
     return sort_tile(n) == kSortTileSmall ? packed_two_pass_t<kSortTileSmall>(ls, n, buf, buf.kv[1], s, sj)
@@ -716,6 +730,18 @@ hipError_t launch_argsort_labels(const int32_t* labels, int64_t N, int B, int K,
   }
   *sorted = buf.kv[cur];
   return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_argsort_labels(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf,
+                                 const uint2** sorted, hipStream_t s, const InertiaJob* side) {
+  return argsort_labels<false>(labels, N, B, K, buf, sorted, nullptr, s, side);
+}
+
+hipError_t launch_argsort_marked(const int32_t* labels, int64_t N, int B, int K, SortBuffers& buf,
+                                 const uint2** sorted, uint32_t* mark, hipStream_t s) {
+  return argsort_labels<true>(labels, N, B, K, buf, sorted, mark, s, nullptr);
 }
 
 }  // namespace fkm
