@@ -82,8 +82,8 @@ GradLayout grad_layout(int64_t N, int K, int D, int B) {
   const int64_t n = N * B;
   size_t o = 256;
   if (n > kGradDirect) {
-    L.kv0 = o;   o = al256(o + (size_t)n * 8);
-    L.kv1 = o;   o = al256(o + (size_t)n * 8);
+    L.kv0 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
+    L.kv1 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
     L.hist = o;  o = al256(o + (size_t)sort_hist_words(N, B, K) * 4);
     L.dtot = o;  o = al256(o + ((size_t)1 << kSortWideBits) * 4);
     for (int i = 0; i < 3; ++i) {

@@ -204,12 +204,13 @@ __global__ __launch_bounds__(256) void embed_grad_direct_kernel(const typename T
 
 // Level 1.  A group of LPR lanes, one vector each, takes a unit of U sorted
 // rows and a slab of LPR vectors, and adds the rows of each segment in order,
-// 8 row loads in flight.  A segment inside the unit is finished here; a piece
+// with 8 row loads in flight and their keys read a batch ahead of those.  A segment inside the unit is finished here; a piece
 // that continues from the left goes to the unit's fragment 0, one that starts
 // here and continues to the right to fragment 1.  Rows whose word carries the
 // mark leave nothing.  The workgroups past the sums zero the entries no row
 // has (not when accumulating), finding each by a binary search.
 constexpr int kAhead = 8;
+static_assert(3 * kAhead <= kSlack, "pairs read past the last row");
 template <class TI, class TO, int V, int LPR>
 __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::raw* __restrict__ dout,
                                                              const uint2* __restrict__ kv, int64_t n, uint32_t mark,
@@ -262,28 +263,37 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::
     }
     if (slab == 0 && threadIdx.x % LPR == 0) fany[unit * 2 + which] = any;
   };
-  const typename TI::raw* base = dout + (int64_t)c * V;
+  // Every row load is issued, so each ring slot keeps its registers: a marked
+  // row reads row 0 and a lane past the row its last vector, both left out
+  // below.
+  const typename TI::raw* base = dout + (int64_t)(on ? c : nv - 1) * V;
   const int64_t pitch = (int64_t)nv * V;
+  const uint32_t last = kv[j1 - 1].x;
+  // The batch at j, its rows past the unit as its last key, marked.  The loads
+  // are never skipped (the sorted pairs have kSlack readable ones behind them):
+  // a branch here would make the first wait of every batch wait for them all.
+  auto fetch = [&](uint2 (&e)[kAhead], int64_t j) {
+    const uint4* p = reinterpret_cast<const uint4*>(kv + j);  // units start at multiples of 16 rows
+    const int64_t have = j1 - j;
+#pragma unroll
+    for (int i = 0; i < kAhead / 2; ++i) {
+      const uint4 t = p[i];
+      e[2 * i] = 2 * i < have ? make_uint2(t.x, t.y) : make_uint2(last, mark);
+      e[2 * i + 1] = 2 * i + 1 < have ? make_uint2(t.z, t.w) : make_uint2(last, mark);
+    }
+  };
+  auto row = [&](Pack<TI, V>& p, const uint2& e) {
+    p.load_nt(base + (int64_t)(e.y & mark ? 0u : e.y) * pitch);
+  };
+  uint2 e[kAhead], en[kAhead];
+  Pack<TI, V> p[kAhead];
+  fetch(e, j0);
+  fetch(en, j0 + kAhead);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) row(p[i], e[i]);
   for (int64_t j = j0; j < j1; j += kAhead) {
-    uint2 e[kAhead];
-    if (j + kAhead <= j1) {
-      const uint4* p = reinterpret_cast<const uint4*>(kv + j);  // units start at multiples of 16 rows
-#pragma unroll
-      for (int i = 0; i < kAhead / 2; ++i) {
-        const uint4 t = p[i];
-        e[2 * i] = make_uint2(t.x, t.y), e[2 * i + 1] = make_uint2(t.z, t.w);
-      }
-    } else {
-      const uint32_t last = kv[j1 - 1].x;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) e[i] = j + i < j1 ? kv[j + i] : make_uint2(last, mark);
-    }
-    Pack<TI, V> p[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (on && !(e[i].y & mark)) p[i].load(base + (int64_t)e[i].y * pitch);
-      else p[i].zero();
-    }
+    uint2 e2[kAhead];
+    fetch(e2, j + 2 * kAhead);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       if (e[i].x != cur) {
@@ -294,11 +304,16 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::
 #pragma unroll
         for (int v = 0; v < V; ++v) a[v] = 0.f;
       }
-      float f[V];
-      p[i].unpack(f);
+      if (!(e[i].y & mark)) {
+        float f[V];
+        p[i].unpack(f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) a[v] += f[v];
-      any |= !(e[i].y & mark);
+        for (int v = 0; v < V; ++v) a[v] += f[v];
+        any = true;
+      }
+      row(p[i], en[i]);  // the same slot of the next batch
+      e[i] = en[i];
+      en[i] = e2[i];
     }
   }
   if (left) to_frag(0);
@@ -306,10 +321,11 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::
   else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, scale, acc, any);
 }
 
-// Joins the fragments of up to 64 consecutive units of W sorted rows from
+// Joins the fragments of up to kRange consecutive units of W sorted rows from
 // unit u0 (of `units`), one wave, V columns a lane.  Segments that end inside
 // are finished; what crosses the joined range's edges goes to its fragments
 // by the same rule.
+constexpr int kRange = kJoin / 16;
 template <class TO, int V>
 __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t n, int64_t W, int64_t u0,
                                            int64_t units, const float* frag, const uint32_t* fany, int64_t fbase,
@@ -318,95 +334,83 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
                                            int64_t obase, int oDp, int oc, bool flag_lane) {
   const int lane = lane_id();
   const int64_t u = u0 + lane;
-  bool from_left = false, to_right = false, one = false;
+  bool from_left = false, to_right = false, one = false, any0 = false, any1 = false;
   uint32_t kl = 0, kf = 0;
-  if (lane < 64 && u < units) {
+  if (lane < kRange && u < units) {
     const int64_t r0 = u * W, r1 = r0 + W < n ? r0 + W : n;
     kf = kv[r0].x, kl = kv[r1 - 1].x;
     from_left = r0 > 0 && kv[r0 - 1].x == kf;
     to_right = r1 < n && kv[r1].x == kl;
     one = kf == kl;
+    any0 = from_left && fany[(u - fbase) * 2];
+    any1 = to_right && !(from_left && one) && fany[(u - fbase) * 2 + 1];
   }
-  const uint64_t L = __ballot(from_left), R = __ballot(to_right), O = __ballot(one);
-  const int count = units - u0 < 64 ? (int)(units - u0) : 64;
-  float a[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) a[v] = 0.f;
-  bool any = false, left = true, open = (L & 1) != 0;  // a piece that comes from the left of the range is open at its start
-  constexpr int kB = 4;  // units whose fragments are loaded together
-  for (int i0 = 0; i0 < count; i0 += kB) {
-    if (((L | R) >> i0 & ((1ull << kB) - 1)) == 0) continue;
-    float f0[kB][V], f1[kB][V];
-    uint32_t n0[kB], n1[kB];
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int b = i0 + i;
-      const bool l = b < 64 && (L >> b & 1), r = b < 64 && (R >> b & 1) && !(l && (O >> b & 1));
-      n0[i] = n1[i] = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) f0[i][v] = f1[i][v] = 0.f;
-      const int64_t at = (u0 + b - fbase) * 2;
-      if (l) {
-        n0[i] = fany[at];
-        if (on) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) f0[i][v] = frag[at * Dp + c * V + v];
-        }
-      }
-      if (r) {
-        n1[i] = fany[at + 1];
-        if (on) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) f1[i][v] = frag[(at + 1) * Dp + c * V + v];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kB; ++i) {
-      const int b = i0 + i;
-      if (b >= count) break;
-      const bool l = L >> b & 1, r = R >> b & 1, whole = l && r && (O >> b & 1);
-      if (l) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] += f0[i][v];
-        any |= n0[i] != 0;
-        if (!whole) {  // the segment ends in this unit
-          const uint32_t k = __shfl(kf, b);
-          if (left) {
-            if (on) {
-#pragma unroll
-              for (int v = 0; v < V; ++v) ofrag[(obase * 2) * oDp + oc * V + v] = a[v];
-            }
-            if (flag_lane) oany[obase * 2] = any;
-          } else if (on) {
-            put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, any);
-          }
-          open = false;
-        }
-      }
-      if (r && !whole) {  // a segment starts here and goes on
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = f1[i][v];
-        any = n1[i] != 0;
-        left = false;
-        open = true;
-      } else if (!l) {
-        left = false;
-      }
-    }
-  }
-  if (open) {  // a piece continues to the right of the range
-    const int which = left ? 0 : 1;
+  // unit i continues a segment from the left / starts one that goes on to the right; passes one through
+  const uint32_t L = (uint32_t)__ballot(from_left), P = (uint32_t)__ballot(from_left && to_right && one);
+  const uint32_t S = (uint32_t)__ballot(to_right) & ~P;
+  const uint32_t A0 = (uint32_t)__ballot(any0), A1 = (uint32_t)__ballot(any1);
+  auto leave = [&](const float (&a)[V], int which, bool any) {
     if (on) {
 #pragma unroll
       for (int v = 0; v < V; ++v) ofrag[(obase * 2 + which) * oDp + oc * V + v] = a[v];
     }
     if (flag_lane) oany[obase * 2 + which] = any;
+  };
+  float a[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) a[v] = 0.f;
+  bool any = false, left = true, open = (L & 1) != 0;  // a piece from the left of the range is open at its start
+  constexpr int kB = 8;  // units whose fragments are loaded together
+#pragma unroll
+  for (int i0 = 0; i0 < kRange; i0 += kB) {
+    if (((L | S) >> i0 & ((1u << kB) - 1)) == 0) continue;
+    float f0[kB][V], f1[kB][V];
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int b = i0 + i;
+      const int64_t at = (u0 + b - fbase) * 2;
+#pragma unroll
+      for (int v = 0; v < V; ++v) f0[i][v] = f1[i][v] = 0.f;
+      if ((L >> b & 1) && on) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f0[i][v] = frag[at * Dp + c * V + v];
+      }
+      if ((S >> b & 1) && on) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) f1[i][v] = frag[(at + 1) * Dp + c * V + v];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kB; ++i) {
+      const int b = i0 + i;
+      if (L >> b & 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] += f0[i][v];
+        any |= A0 >> b & 1;
+        if (!(P >> b & 1)) {  // the segment ends in this unit
+          if (left) {
+            leave(a, 0, any);
+          } else if (on) {
+            const uint32_t k = __builtin_amdgcn_readlane(kf, b);
+            put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, any);
+          }
+          open = false;
+        }
+      }
+      if (S >> b & 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] = f1[i][v];
+        any = A1 >> b & 1;
+        left = false;
+        open = true;
+      }
+    }
   }
+  if (open) leave(a, left ? 0 : 1, any);  // a piece continues to the right of the range
 }
 
-// One workgroup joins kJoin units (16 waves of 64, then one wave joins the
-// 16) for a slab of 64 vectors of V columns.
+// One workgroup joins kJoin units (16 waves of kRange, then one wave joins
+// the 16) for a slab of 64 vectors of V columns.
 template <class TO, int V>
 __global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __restrict__ kv, int64_t n, int64_t W,
                                                                int64_t units, int nslab, const float* __restrict__ frag,
@@ -414,7 +418,7 @@ __global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __re
                                                                float scale, bool acc,
                                                                typename TO::raw* __restrict__ grad,
                                                                float* __restrict__ ofrag, uint32_t* __restrict__ oany) {
-  __shared__ float sfrag[16 * 2][64 * V];
+  __shared__ __align__(16) float sfrag[16 * 2][64 * V];
   __shared__ uint32_t sany[16 * 2];
   const int lane = lane_id();
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -422,17 +426,17 @@ __global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __re
   const int slab = (int)(blockIdx.x - g * nslab);
   const int c = slab * 64 + lane;
   const bool on = c < nv;
-  const int64_t u0 = g * kJoin + w * 64;
+  const int64_t u0 = g * kJoin + w * kRange;
   if (u0 < units)
     join_units<TO, V>(kv, n, W, u0, units, frag, fany, 0, Dp, nv, c, on, scale, acc, grad, &sfrag[0][0], sany, w,
                       64 * V, lane, lane == 0);
   __syncthreads();
   if (w == 0) {
-    const int64_t all = (units + 63) / 64, s0 = g * 16;
+    const int64_t all = (units + kRange - 1) / kRange, s0 = g * 16;
     const int64_t s1 = s0 + 16 < all ? s0 + 16 : all;
-    // the 16 joined ranges are units of 64 W rows; their fragments are in LDS
-    join_units<TO, V>(kv, n, 64 * W, s0, s1, &sfrag[0][0] + (lane - c) * V, sany, s0, 64 * V, nv, c, on, scale, acc,
-                      grad, ofrag, oany, g, Dp, c, lane == 0 && slab == 0);
+    // the 16 joined ranges are units of kRange * W rows; their fragments are in LDS
+    join_units<TO, V>(kv, n, kRange * W, s0, s1, &sfrag[0][0] + (lane - c) * V, sany, s0, 64 * V, nv, c, on, scale,
+                      acc, grad, ofrag, oany, g, Dp, c, lane == 0 && slab == 0);
   }
 }
 
@@ -486,7 +490,7 @@ hipError_t embed_grad_v(const void* dout, const int32_t* ids, int64_t N, int K, 
   int64_t W = U;
   for (int level = 0; units > 1; ++level) {
     const int64_t groups = (units + kJoin - 1) / kJoin;
-    const int waves = units < kJoin ? (int)((units + 63) / 64) : 16;
+    const int waves = units < kJoin ? (int)((units + kRange - 1) / kRange) : 16;
     embed_grad_join_kernel<TO, VJ><<<dim3((unsigned)(groups * nslab)), dim3(waves * 64), 0, s>>>(
         kv, n, W, units, nslab, buf.frag[level], buf.any[level], Dp, D / VJ, scale, acc,
         static_cast<typename TO::raw*>(grad), buf.frag[level + 1], buf.any[level + 1]);

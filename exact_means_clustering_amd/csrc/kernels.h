@@ -239,12 +239,19 @@ hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids,
 // The rows of the sorted order are summed by units of U rows and slabs of columns; pieces of an entry's segment that
 // cross a unit's edge go to fragments, two per unit, which are joined kJoin units at a time.
 constexpr int64_t kGradDirect = 256;  // up to this many rows the gradient needs no sort
-constexpr int kJoin = 1024;           // units joined by one workgroup (16 waves of 64)
+constexpr int kSlack = 32;             // readable pairs that the gradient's sort buffers have past the last row
+constexpr int kJoin = 256;            // units joined by one workgroup (16 waves of 16)
 // Rows per unit for n rows of D columns: 16 to 256, so that the waves (of 512 columns) number about 8,192.
+#ifndef FKM_GW
+#define FKM_GW 8192
+#endif
+#ifndef FKM_UMAX
+#define FKM_UMAX 256
+#endif
 inline int grad_unit(int64_t n, int D) {
   const int64_t slabs = (D + 511) / 512, per = D <= 256 ? 512 / (D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256) : 1;
   int u = 16;
-  while (u < 256 && n * slabs / per / u > 8192) u *= 2;
+  while (u < FKM_UMAX && n * slabs / per / u > FKM_GW) u *= 2;
   return u;
 }
 struct GradBuffers {

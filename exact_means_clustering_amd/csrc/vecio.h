@@ -36,6 +36,18 @@ template <class T, int V> struct Pack {
       w[0] = *reinterpret_cast<const uint16_t*>(p);
     }
   }
+  // the same, streamed past the caches (data read once)
+  __device__ __forceinline__ void load_nt(const typename T::raw* p) {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = fkm::load_nt(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    } else {
+      load(p);
+    }
+  }
   __device__ __forceinline__ void store(typename T::raw* p) const {
     if constexpr (BYTES >= 16) {
 #pragma unroll
