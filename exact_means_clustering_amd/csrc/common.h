@@ -322,6 +322,37 @@ __device__ __forceinline__ int64_t xcd_tile(int64_t b, int64_t n) {
   return x * q + (x < r ? x : r) + i;
 }
 
+// Mask of the active lanes of this wave whose RB-bit digit equals mine.
+// Per bit, t is all ones where this lane's bit is set, and the lanes whose
+// bit agrees are ~(ballot ^ t), applied to the two 32-bit halves of the mask
+// with one three-input bit operation each (truth table 0x90: src0 & ~(src1 ^
+// src2)): four vector instructions per bit, with every bit's extract and
+// ballot issued ahead of the mask updates.  The empty asm statement keeps
+// the compiler from re-deriving each ballot's condition with a shift.  (A
+// per-lane select between the ballot and its complement cost the compiler
+// nine instructions per bit; the scatter spends most of its issue cycles on
+// the vector ALU.)
+template <int RB>
+__device__ __forceinline__ uint64_t match_digit(uint32_t d, bool valid) {
+  const uint64_t v = __ballot(valid);
+  uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32);
+  uint32_t t[RB];
+  uint64_t bb[RB];
+#pragma unroll
+  for (int bit = 0; bit < RB; ++bit) {
+    t[bit] = (uint32_t)__builtin_amdgcn_sbfe((int)d, bit, 1);
+    asm volatile("" : "+v"(t[bit]));
+  }
+#pragma unroll
+  for (int bit = 0; bit < RB; ++bit) bb[bit] = __ballot(t[bit] != 0u);
+#pragma unroll
+  for (int bit = 0; bit < RB; ++bit) {
+    lo = __builtin_amdgcn_bitop3_b32(lo, (uint32_t)bb[bit], t[bit], 0x90);
+    hi = __builtin_amdgcn_bitop3_b32(hi, (uint32_t)(bb[bit] >> 32), t[bit], 0x90);
+  }
+  return ((uint64_t)hi << 32) | lo;
+}
+
 // Exclusive prefix sum over a 256-thread block (4 waves).  `tmp` must hold 4
 // words.  Returns the exclusive prefix of `v`; *total receives the block sum.
 __device__ __forceinline__ uint32_t block_exclusive_scan_256(uint32_t v, uint32_t* tmp, uint32_t* total) {

@@ -92,23 +92,28 @@ hipError_t embed_v(const void* table, const int32_t* ids, int64_t N, int K, int 
 // ---------------------------------------------------------------------------
 // backward
 // ---------------------------------------------------------------------------
-// Entry e of the gradient gets the sum `a` of its rows (V values at column
-// `col` of it); `any`: whether a row that counts was among them.  An entry
-// without such a row is zero, or stays as it is when accumulating.
+// How finished sums reach the gradient.
+struct PutMode {
+  float scale;
+  bool add;   // to the old value
+  bool keep;  // leave an entry without rows as it is (old values, or zeros written before)
+};
+// V values of an entry's sum `a` go to `at`; `any`: whether a row that counts
+// was among them (an entry without one is zero or stays as it is).
 template <class TO, int V>
-__device__ __forceinline__ void put_grad(typename TO::raw* grad, int64_t at, const float (&a)[V], float scale, bool acc,
+__device__ __forceinline__ void put_grad(typename TO::raw* grad, int64_t at, const float (&a)[V], const PutMode& m,
                                          bool any) {
-  if (acc && !any) return;
+  if (m.keep && !any) return;
   Pack<TO, V> o;
   float r[V];
-  if (acc) {
+  if (m.add) {
     o.load(grad + at);
     o.unpack(r);
 #pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = fmaf(scale, a[i], r[i]);
+    for (int i = 0; i < V; ++i) r[i] = fmaf(m.scale, a[i], r[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) r[i] = any ? scale * a[i] : 0.f;
+    for (int i = 0; i < V; ++i) r[i] = any ? m.scale * a[i] : 0.f;
   }
   o.pack(r);
   o.store(grad + at);
@@ -134,8 +139,8 @@ template <class TI, class TO, int V>
 __global__ __launch_bounds__(256) void embed_grad_direct_kernel(const typename TI::raw* __restrict__ dout,
                                                                 const int32_t* __restrict__ ids, int n, uint32_t N,
                                                                 uint32_t K, int64_t entries, int nv, int nslab,
-                                                                int64_t row_blocks, int64_t units, int per, float scale,
-                                                                bool acc, typename TO::raw* __restrict__ grad) {
+                                                                int64_t row_blocks, int64_t units, int per,
+                                                                PutMode mode, typename TO::raw* __restrict__ grad) {
   __shared__ uint32_t key[kGradDirect];  // entry of every row, ~0 for none
   __shared__ unsigned long long named[4];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
@@ -179,7 +184,7 @@ __global__ __launch_bounds__(256) void embed_grad_direct_kernel(const typename T
         for (int v = 0; v < V; ++v) a[v] += f[v];
       }
     }
-    put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, true);
+    put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, mode, true);
     return;
   }
   // zeros: a workgroup takes 4 waves of `per` (at most 64) entries at a time
@@ -202,141 +207,21 @@ __global__ __launch_bounds__(256) void embed_grad_direct_kernel(const typename T
   }
 }
 
-// Level 1.  A group of LPR lanes, one vector each, takes a unit of U sorted
-// rows and a slab of LPR vectors, and adds the rows of each segment in order,
-// with 8 row loads in flight and their keys read a batch ahead of those.  A segment inside the unit is finished here; a piece
-// that continues from the left goes to the unit's fragment 0, one that starts
-// here and continues to the right to fragment 1.  Rows whose word carries the
-// mark leave nothing.  The workgroups past the sums zero the entries no row
-// has (not when accumulating), finding each by a binary search.
-constexpr int kAhead = 8;
-static_assert(3 * kAhead <= kSlack, "pairs read past the last row");
-template <class TI, class TO, int V, int LPR>
-__global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::raw* __restrict__ dout,
-                                                             const uint2* __restrict__ kv, int64_t n, uint32_t mark,
-                                                             int U, int64_t units, int64_t sum_blocks, int nv,
-                                                             int nslab, int64_t entries, int per, float scale, bool acc,
-                                                             typename TO::raw* __restrict__ grad,
-                                                             float* __restrict__ frag, uint32_t* __restrict__ fany,
-                                                             int Dp) {
-  const int lane = lane_id();
-  const int w = threadIdx.x >> 6;
-  if ((int64_t)blockIdx.x >= sum_blocks) {
-    const int64_t zero_units = (entries + per - 1) / per;
-    for (int64_t u = ((int64_t)blockIdx.x - sum_blocks) * 4 + w; u < zero_units;
-         u += ((int64_t)gridDim.x - sum_blocks) * 4) {
-      const int64_t e = u * per + lane;
-      bool absent = false;
-      if (lane < per && e < entries) {
-        int64_t lo = 0, hi = n;  // first sorted position with a key of at least e
-        while (lo < hi) {
-          const int64_t m = (lo + hi) >> 1;
-          if ((int64_t)kv[m].x < e) lo = m + 1;
-          else hi = m;
-        }
-        absent = lo == n || (int64_t)kv[lo].x != e;
-      }
-      zero_entries<TO, V>(grad, u * per, __ballot(absent), nv, lane);
-    }
-    return;
-  }
-  constexpr int GPB = 256 / LPR;  // groups per workgroup
-  const int64_t q = (int64_t)blockIdx.x * GPB + threadIdx.x / LPR;
-  const int64_t unit = q / nslab;
-  if (unit >= units) return;
-  const int slab = (int)(q - unit * nslab);
-  const int c = slab * LPR + threadIdx.x % LPR;
-  const bool on = c < nv;
-  const int64_t j0 = unit * U, j1 = j0 + U < n ? j0 + U : n;
-  uint32_t cur = kv[j0].x;
-  bool left = j0 > 0 && kv[j0 - 1].x == cur;
-  const bool more = j1 < n && kv[j1].x == kv[j1 - 1].x;  // the last segment continues to the right
-  float a[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) a[v] = 0.f;
-  bool any = false;
-  auto to_frag = [&](int which) {
-    if (on) {
-      float* f = frag + (unit * 2 + which) * Dp + c * V;
-#pragma unroll
-      for (int v = 0; v < V; ++v) f[v] = a[v];
-    }
-    if (slab == 0 && threadIdx.x % LPR == 0) fany[unit * 2 + which] = any;
-  };
-  // Every row load is issued, so each ring slot keeps its registers: a marked
-  // row reads row 0 and a lane past the row its last vector, both left out
-  // below.
-  const typename TI::raw* base = dout + (int64_t)(on ? c : nv - 1) * V;
-  const int64_t pitch = (int64_t)nv * V;
-  const uint32_t last = kv[j1 - 1].x;
-  // The batch at j, its rows past the unit as its last key, marked.  The loads
-  // are never skipped (the sorted pairs have kSlack readable ones behind them):
-  // a branch here would make the first wait of every batch wait for them all.
-  auto fetch = [&](uint2 (&e)[kAhead], int64_t j) {
-    const uint4* p = reinterpret_cast<const uint4*>(kv + j);  // units start at multiples of 16 rows
-    const int64_t have = j1 - j;
-#pragma unroll
-    for (int i = 0; i < kAhead / 2; ++i) {
-      const uint4 t = p[i];
-      e[2 * i] = 2 * i < have ? make_uint2(t.x, t.y) : make_uint2(last, mark);
-      e[2 * i + 1] = 2 * i + 1 < have ? make_uint2(t.z, t.w) : make_uint2(last, mark);
-    }
-  };
-  auto row = [&](Pack<TI, V>& p, const uint2& e) {
-    p.load_nt(base + (int64_t)(e.y & mark ? 0u : e.y) * pitch);
-  };
-  uint2 e[kAhead], en[kAhead];
-  Pack<TI, V> p[kAhead];
-  fetch(e, j0);
-  fetch(en, j0 + kAhead);
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) row(p[i], e[i]);
-  for (int64_t j = j0; j < j1; j += kAhead) {
-    uint2 e2[kAhead];
-    fetch(e2, j + 2 * kAhead);
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (e[i].x != cur) {
-        if (left) to_frag(0);
-        else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, scale, acc, any);
-        cur = e[i].x;
-        left = any = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] = 0.f;
-      }
-      if (!(e[i].y & mark)) {
-        float f[V];
-        p[i].unpack(f);
-#pragma unroll
-        for (int v = 0; v < V; ++v) a[v] += f[v];
-        any = true;
-      }
-      row(p[i], en[i]);  // the same slot of the next batch
-      e[i] = en[i];
-      en[i] = e2[i];
-    }
-  }
-  if (left) to_frag(0);
-  else if (more) to_frag(1);
-  else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, scale, acc, any);
-}
-
-// Joins the fragments of up to kRange consecutive units of W sorted rows from
+// Joins the fragments of up to RANGE (64 at most) consecutive units of W sorted rows from
 // unit u0 (of `units`), one wave, V columns a lane.  Segments that end inside
 // are finished; what crosses the joined range's edges goes to its fragments
 // by the same rule.
-constexpr int kRange = kJoin / 16;
-template <class TO, int V>
+template <class TO, int V, int RANGE>
 __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t n, int64_t W, int64_t u0,
                                            int64_t units, const float* frag, const uint32_t* fany, int64_t fbase,
-                                           int Dp, int nv, int c, bool on, float scale, bool acc,
+                                           int Dp, int nv, int c, bool on, const PutMode& mode,
                                            typename TO::raw* __restrict__ grad, float* ofrag, uint32_t* oany,
                                            int64_t obase, int oDp, int oc, bool flag_lane) {
   const int lane = lane_id();
   const int64_t u = u0 + lane;
   bool from_left = false, to_right = false, one = false, any0 = false, any1 = false;
   uint32_t kl = 0, kf = 0;
-  if (lane < kRange && u < units) {
+  if (lane < RANGE && u < units) {
     const int64_t r0 = u * W, r1 = r0 + W < n ? r0 + W : n;
     kf = kv[r0].x, kl = kv[r1 - 1].x;
     from_left = r0 > 0 && kv[r0 - 1].x == kf;
@@ -346,9 +231,9 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
     any1 = to_right && !(from_left && one) && fany[(u - fbase) * 2 + 1];
   }
   // unit i continues a segment from the left / starts one that goes on to the right; passes one through
-  const uint32_t L = (uint32_t)__ballot(from_left), P = (uint32_t)__ballot(from_left && to_right && one);
-  const uint32_t S = (uint32_t)__ballot(to_right) & ~P;
-  const uint32_t A0 = (uint32_t)__ballot(any0), A1 = (uint32_t)__ballot(any1);
+  const uint64_t L = __ballot(from_left), P = __ballot(from_left && to_right && one);
+  const uint64_t S = __ballot(to_right) & ~P;
+  const uint64_t A0 = __ballot(any0), A1 = __ballot(any1);
   auto leave = [&](const float (&a)[V], int which, bool any) {
     if (on) {
 #pragma unroll
@@ -360,10 +245,9 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
 #pragma unroll
   for (int v = 0; v < V; ++v) a[v] = 0.f;
   bool any = false, left = true, open = (L & 1) != 0;  // a piece from the left of the range is open at its start
-  constexpr int kB = 8;  // units whose fragments are loaded together
-#pragma unroll
-  for (int i0 = 0; i0 < kRange; i0 += kB) {
-    if (((L | S) >> i0 & ((1u << kB) - 1)) == 0) continue;
+  constexpr int kB = RANGE < 8 ? RANGE : 8;  // units whose fragments are loaded together
+  for (int i0 = 0; i0 < RANGE; i0 += kB) {
+    if (((L | S) >> i0 & ((1ull << kB) - 1)) == 0) continue;
     float f0[kB][V], f1[kB][V];
 #pragma unroll
     for (int i = 0; i < kB; ++i) {
@@ -386,13 +270,13 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
       if (L >> b & 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) a[v] += f0[i][v];
-        any |= A0 >> b & 1;
+        any |= (A0 >> b & 1) != 0;
         if (!(P >> b & 1)) {  // the segment ends in this unit
           if (left) {
             leave(a, 0, any);
           } else if (on) {
             const uint32_t k = __builtin_amdgcn_readlane(kf, b);
-            put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, scale, acc, any);
+            put_grad<TO, V>(grad, ((int64_t)k * nv + c) * V, a, mode, any);
           }
           open = false;
         }
@@ -400,7 +284,7 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
       if (S >> b & 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) a[v] = f1[i][v];
-        any = A1 >> b & 1;
+        any = (A1 >> b & 1) != 0;
         left = false;
         open = true;
       }
@@ -409,14 +293,159 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
   if (open) leave(a, left ? 0 : 1, any);  // a piece continues to the right of the range
 }
 
+// Level 1.  A group of LPR lanes, one vector each, takes a unit of U sorted
+// rows and a slab of LPR vectors, and adds the rows of each segment in order,
+// with 8 row loads in flight and their keys read a batch ahead of those.  A
+// segment inside the unit is finished here; a piece that continues from the
+// left goes to the unit's fragment 0, one that starts here and continues to
+// the right to fragment 1; the workgroup joins its units' fragments in LDS
+// before any reaches memory.  Rows whose word carries the mark leave nothing.
+// The workgroups past the sums zero the entries no row has (not when they
+// keep what they hold), finding each by a binary search.
+constexpr int kAhead = 8;
+template <int LPR>
+constexpr int kGroups = 256 / LPR;
+static_assert(3 * kAhead <= kSlack, "pairs read past the last row");
+template <class TI, class TO, int V, int LPR>
+__global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::raw* __restrict__ dout,
+                                                             const uint2* __restrict__ kv, int64_t n, uint32_t mark,
+                                                             int U, int64_t units, int64_t sum_blocks, int nv,
+                                                             int nslab, int64_t entries, int per, PutMode mode,
+                                                             typename TO::raw* __restrict__ grad,
+                                                             float* __restrict__ frag, uint32_t* __restrict__ fany,
+                                                             int Dp) {
+  constexpr int GPB = kGroups<LPR>;              // units per workgroup
+  constexpr int VJ = V >= 4 ? 4 : 1;             // columns per lane in the join
+  __shared__ __align__(16) float sfrag[GPB * 2][LPR * V];
+  __shared__ uint32_t sany[GPB * 2];
+  const int lane = lane_id();
+  const int w = threadIdx.x >> 6;
+  if ((int64_t)blockIdx.x >= sum_blocks) {
+    const int64_t zero_units = (entries + per - 1) / per;
+    for (int64_t u = ((int64_t)blockIdx.x - sum_blocks) * 4 + w; u < zero_units;
+         u += ((int64_t)gridDim.x - sum_blocks) * 4) {
+      const int64_t e = u * per + lane;
+      bool absent = false;
+      if (lane < per && e < entries) {
+        int64_t lo = 0, hi = n;  // first sorted position with a key of at least e
+        while (lo < hi) {
+          const int64_t m = (lo + hi) >> 1;
+          if ((int64_t)kv[m].x < e) lo = m + 1;
+          else hi = m;
+        }
+        absent = lo == n || (int64_t)kv[lo].x != e;
+      }
+      zero_entries<TO, V>(grad, u * per, __ballot(absent), nv, lane);
+    }
+    return;
+  }
+  const int64_t ub = (int64_t)blockIdx.x / nslab;  // the workgroup's units: GPB from ub * GPB
+  const int slab = (int)((int64_t)blockIdx.x - ub * nslab);
+  const int grp = threadIdx.x / LPR, gl = threadIdx.x % LPR;
+  const int64_t unit = ub * GPB + grp;
+  if (unit < units) {
+    const int c = slab * LPR + gl;
+    const bool on = c < nv;
+    const int64_t j0 = unit * U, j1 = j0 + U < n ? j0 + U : n;
+    uint32_t cur = kv[j0].x;
+    bool left = j0 > 0 && kv[j0 - 1].x == cur;
+    const bool more = j1 < n && kv[j1].x == kv[j1 - 1].x;  // the last segment continues to the right
+    float a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = 0.f;
+    bool any = false;
+    auto to_frag = [&](int which) {
+      if (on) {
+        float* f = &sfrag[grp * 2 + which][gl * V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) f[v] = a[v];
+      }
+      if (gl == 0) sany[grp * 2 + which] = any;
+    };
+    // Every row load is issued, so each ring slot keeps its registers: a marked
+    // row reads row 0 and a lane past the row its last vector, both left out
+    // below.
+    const typename TI::raw* base = dout + (int64_t)(on ? c : nv - 1) * V;
+    const int64_t pitch = (int64_t)nv * V;
+    const uint32_t last = kv[j1 - 1].x;
+    // The batch at j, its rows past the unit as its last key, marked.  The loads
+    // are never skipped (the sorted pairs have kSlack readable ones behind them):
+    // a branch here would make the first wait of every batch wait for them all.
+    auto fetch = [&](uint2 (&e)[kAhead], int64_t j) {
+      const uint4* p = reinterpret_cast<const uint4*>(kv + j);  // units start at multiples of 16 rows
+      const int64_t have = j1 - j;
+#pragma unroll
+      for (int i = 0; i < kAhead / 2; ++i) {
+        const uint4 t = p[i];
+        e[2 * i] = 2 * i < have ? make_uint2(t.x, t.y) : make_uint2(last, mark);
+        e[2 * i + 1] = 2 * i + 1 < have ? make_uint2(t.z, t.w) : make_uint2(last, mark);
+      }
+    };
+    auto row = [&](Pack<TI, V>& p, const uint2& e) {
+      p.load_nt(base + (int64_t)(e.y & mark ? 0u : e.y) * pitch);
+    };
+    uint2 e[kAhead], en[kAhead];
+    Pack<TI, V> p[kAhead];
+    auto add = [&](const Pack<TI, V>& x, const uint2& e) {
+      if (e.x != cur) {
+        if (left) to_frag(0);
+        else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, mode, any);
+        cur = e.x;
+        left = any = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] = 0.f;
+      }
+      if (!(e.y & mark)) {
+        float f[V];
+        x.unpack(f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) a[v] += f[v];
+        any = true;
+      }
+    };
+    fetch(e, j0);
+    fetch(en, j0 + kAhead);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) row(p[i], e[i]);
+    int64_t j = j0;
+    for (; j + kAhead < j1; j += kAhead) {
+      uint2 e2[kAhead];
+      fetch(e2, j + 2 * kAhead);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        add(p[i], e[i]);
+        row(p[i], en[i]);  // the same slot of the next batch
+        e[i] = en[i];
+        en[i] = e2[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) add(p[i], e[i]);
+    if (left) to_frag(0);
+    else if (more) to_frag(1);
+    else if (on) put_grad<TO, V>(grad, ((int64_t)cur * nv + c) * V, a, mode, any);
+  }
+  __syncthreads();
+  // the units' fragments joined: 64 lanes of VJ columns a wave
+  constexpr int LJ = LPR * V / VJ;  // lanes that the slab takes
+  if (w * 64 < LJ) {
+    const int lj = w * 64 + lane, nj = nv * V / VJ;
+    const int cj = slab * LJ + lj;
+    const int64_t u0 = ub * GPB;
+    join_units<TO, VJ, GPB>(kv, n, U, u0, units < u0 + GPB ? units : u0 + GPB, &sfrag[0][0] + (lj - cj) * VJ, sany, u0,
+                            LPR * V, nj, cj, lj < LJ && cj < nj, mode, grad, frag, fany, ub, Dp, cj,
+                            lj == 0 && slab == 0);
+  }
+}
+
+constexpr int kRange = kJoin / 16;
 // One workgroup joins kJoin units (16 waves of kRange, then one wave joins
 // the 16) for a slab of 64 vectors of V columns.
 template <class TO, int V>
 __global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __restrict__ kv, int64_t n, int64_t W,
                                                                int64_t units, int nslab, const float* __restrict__ frag,
                                                                const uint32_t* __restrict__ fany, int Dp, int nv,
-                                                               float scale, bool acc,
-                                                               typename TO::raw* __restrict__ grad,
+                                                               PutMode mode, typename TO::raw* __restrict__ grad,
                                                                float* __restrict__ ofrag, uint32_t* __restrict__ oany) {
   __shared__ __align__(16) float sfrag[16 * 2][64 * V];
   __shared__ uint32_t sany[16 * 2];
@@ -428,30 +457,167 @@ __global__ __launch_bounds__(1024) void embed_grad_join_kernel(const uint2* __re
   const bool on = c < nv;
   const int64_t u0 = g * kJoin + w * kRange;
   if (u0 < units)
-    join_units<TO, V>(kv, n, W, u0, units, frag, fany, 0, Dp, nv, c, on, scale, acc, grad, &sfrag[0][0], sany, w,
+    join_units<TO, V, kRange>(kv, n, W, u0, units, frag, fany, 0, Dp, nv, c, on, mode, grad, &sfrag[0][0], sany, w,
                       64 * V, lane, lane == 0);
   __syncthreads();
   if (w == 0) {
     const int64_t all = (units + kRange - 1) / kRange, s0 = g * 16;
     const int64_t s1 = s0 + 16 < all ? s0 + 16 : all;
     // the 16 joined ranges are units of kRange * W rows; their fragments are in LDS
-    join_units<TO, V>(kv, n, kRange * W, s0, s1, &sfrag[0][0] + (lane - c) * V, sany, s0, 64 * V, nv, c, on, scale,
-                      acc, grad, ofrag, oany, g, Dp, c, lane == 0 && slab == 0);
+    join_units<TO, V, kRange>(kv, n, kRange * W, s0, s1, &sfrag[0][0] + (lane - c) * V, sany, s0, 64 * V, nv, c, on,
+                              mode, grad, ofrag, oany, g, Dp, c, lane == 0 && slab == 0);
   }
 }
 
+// Returns the units left to join.
 template <class TI, class TO, int V, int LPR>
-void sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, int U, int64_t units, int nv,
-                int64_t entries, float scale, bool acc, void* grad, float* frag, uint32_t* fany, int Dp,
-                hipStream_t s) {
+int64_t sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, int U, int nv, int64_t entries,
+                   const PutMode& mode, void* grad, float* frag, uint32_t* fany, int Dp, hipStream_t s) {
+  constexpr int GPB = kGroups<LPR>;
+  const int64_t units = (n + U - 1) / U, ublocks = (units + GPB - 1) / GPB;
   const int nslab = (nv + LPR - 1) / LPR;
-  const int64_t sum_blocks = (units * nslab + 256 / LPR - 1) / (256 / LPR);
+  const int64_t sum_blocks = ublocks * nslab;
   const int per = zero_per(nv * V * TO::SZ);
-  const int64_t zero_blocks = acc ? 0 : zero_grid((entries + 4 * per - 1) / (4 * per));
-  if (sum_blocks + zero_blocks == 0) return;
+  const int64_t zero_blocks = mode.keep ? 0 : zero_grid((entries + 4 * per - 1) / (4 * per));
   embed_grad_sum_kernel<TI, TO, V, LPR><<<dim3((unsigned)(sum_blocks + zero_blocks)), dim3(256), 0, s>>>(
-      static_cast<const typename TI::raw*>(dout), kv, n, mark, U, units, sum_blocks, nv, nslab, entries, per, scale,
-      acc, static_cast<typename TO::raw*>(grad), frag, fany, Dp);
+      static_cast<const typename TI::raw*>(dout), kv, n, mark, U, units, sum_blocks, nv, nslab, entries, per, mode,
+      static_cast<typename TO::raw*>(grad), frag, fany, Dp);
+  return ublocks;
+}
+
+// Up to kSortOne rows: one workgroup argsorts the ids in LDS (stable radix
+// passes of 8 bits over 32-bit words: key, out-of-range bit, row), and the
+// other workgroups of the launch meanwhile zero the gradient.  Ranks as in
+// the sort of many rows: digit matches inside a wave, a counter per wave and
+// digit, waves in row order.
+constexpr int kSortWaves = 16;
+// R: rounds of 64 keys per wave (the keys stay in registers).
+template <int R>
+__global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __restrict__ ids, int n, uint32_t N,
+                                                               uint32_t K, int row_bits, int passes,
+                                                               uint2* __restrict__ kv, uint8_t* __restrict__ zero,
+                                                               int head, size_t words, int tail) {
+  const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {
+    // `head` bytes, `words` 16-byte words, `tail` bytes
+    if (blockIdx.x == 1 && tid < 16) {
+      if (tid < head) zero[tid] = 0;
+      if (tid < tail) zero[head + words * 16 + tid] = 0;
+    }
+    uint4* body = reinterpret_cast<uint4*>(zero + head);
+    const size_t step = (size_t)(gridDim.x - 1) * 1024;
+    for (size_t i = (size_t)(blockIdx.x - 1) * 1024 + tid; i < words; i += step) body[i] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  __shared__ uint32_t word[kSortWaves * 64 * R];
+  __shared__ uint32_t cnt[kSortWaves][256];
+  __shared__ uint32_t tot[256];
+  const int lane = tid & 63, w = tid >> 6;
+  const int first = w * R * 64;
+  uint32_t x[R], rank[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = first + r * 64 + lane;
+    const int at = i < n ? i : n - 1;  // (unconditional, so the words stay in separate registers)
+    const uint32_t id = (uint32_t)ids[at];
+    const uint32_t key = (N < (uint32_t)n ? (uint32_t)at / N * K : 0u) + (id < K ? id : K - 1);
+    x[r] = (key << 1 | (id < K ? 0u : 1u)) << row_bits | (uint32_t)at;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = row_bits + 1 + 8 * p;
+    for (int i = tid; i < kSortWaves * 256; i += 1024) cnt[i >> 8][i & 255] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool valid = first + r * 64 + lane < n;
+      const uint32_t d = x[r] >> shift & 255u;
+      const uint64_t m = match_digit<8>(d, valid);
+      const uint32_t low = (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
+      const uint32_t before = cnt[w][d];
+      rank[r] = before + low;
+      if (valid && low == 0) cnt[w][d] = before + (uint32_t)__popcll(m);
+      // one round after the other: matching 16 rounds at once would not fit the registers
+      if constexpr (R > 8) __builtin_amdgcn_sched_barrier(0);
+    }
+    __syncthreads();
+    if (tid < 256) {
+      uint32_t run = 0;
+#pragma unroll
+      for (int q = 0; q < kSortWaves; ++q) {
+        const uint32_t c = cnt[q][tid];
+        cnt[q][tid] = run;
+        run += c;
+      }
+      tot[tid] = run;
+    }
+    __syncthreads();
+    if (w == 0) {  // exclusive scan of the 256 digit totals, four a lane
+      uint32_t t[4], s = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) t[q] = tot[4 * lane + q], s += t[q];
+      uint32_t inc = s;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t v = __shfl_up(inc, o);
+        if (lane >= o) inc += v;
+      }
+      uint32_t run = inc - s;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tot[4 * lane + q] = run, run += t[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t d = x[r] >> shift & 255u;
+      if (first + r * 64 + lane < n) word[tot[d] + cnt[w][d] + rank[r]] = x[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[r] = word[first + r * 64 + lane];  // (words past n are not used)
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = first + r * 64 + lane;
+    if (i < n)
+      kv[i] = make_uint2(x[r] >> (row_bits + 1),
+                         (x[r] & ((1u << row_bits) - 1)) | (x[r] >> row_bits & 1u) << 31);
+  }
+}
+
+int bits_for(int64_t values) {  // bits that hold 0 .. values - 1
+  int b = 1;
+  while (((int64_t)1 << b) < values) ++b;
+  return b;
+}
+bool grad_sorts_in_one(int64_t n, int64_t entries) {
+  return n <= kSortOne && bits_for(entries) + 1 + bits_for(n) <= 32;
+}
+// Zeroes `bytes` at `zero` too, if there are any.
+void sort_one_launch(const int32_t* ids, int64_t n, uint32_t N, uint32_t K, int64_t entries, uint2* kv, void* zero,
+                     size_t bytes, hipStream_t s) {
+  size_t head = 0, words = 0, tail = 0;
+  int64_t blocks = 0;
+  if (zero) {
+    head = (16 - (uintptr_t)zero % 16) % 16;
+    if (head > bytes) head = bytes;
+    words = (bytes - head) / 16;
+    tail = bytes - head - words * 16;
+    blocks = (int64_t)(words / 4096) + 1;  // four words a thread
+    if (blocks > 2048) blocks = 2048;
+  }
+  auto go = [&](auto kernel) {
+    kernel<<<dim3((unsigned)(1 + blocks)), dim3(1024), 0, s>>>(ids, (int)n, N, K, bits_for(n),
+                                                               (bits_for(entries) + 7) / 8, kv,
+                                                               static_cast<uint8_t*>(zero), (int)head, words, (int)tail);
+  };
+  static_assert(kSortOne == kSortWaves * 64 * 16, "the longest sort's rounds");
+  if (n <= 1024) go(embed_grad_sort_kernel<1>);
+  else if (n <= 2048) go(embed_grad_sort_kernel<2>);
+  else if (n <= 4096) go(embed_grad_sort_kernel<4>);
+  else if (n <= 8192) go(embed_grad_sort_kernel<8>);
+  else go(embed_grad_sort_kernel<16>);
 }
 
 template <class TI, class TO, int V>
@@ -467,18 +633,28 @@ hipError_t embed_grad_v(const void* dout, const int32_t* ids, int64_t N, int K, 
     const int64_t blocks = row_blocks + zero_grid(units);
     embed_grad_direct_kernel<TI, TO, V><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(
         static_cast<const typename TI::raw*>(dout), ids, (int)n, (uint32_t)N, (uint32_t)K, entries, nv, nslab,
-        row_blocks, units, per, scale, acc, static_cast<typename TO::raw*>(grad));
+        row_blocks, units, per, PutMode{scale, acc, acc}, static_cast<typename TO::raw*>(grad));
     return hipGetLastError();
   }
   const uint2* kv = nullptr;
   uint32_t mark = 0;
-  const hipError_t e = launch_argsort_marked(ids, N, B, K, buf.sort, &kv, &mark, s);
-  if (e != hipSuccess) return e;
+  PutMode mode{scale, acc, acc};
+  if (grad_sorts_in_one(n, entries)) {
+    kv = buf.sort.kv[0];
+    mark = 1u << 31;
+    sort_one_launch(ids, n, (uint32_t)N, (uint32_t)K, entries, buf.sort.kv[0], acc ? nullptr : grad,
+                    (size_t)entries * D * TO::SZ, s);
+    mode.keep = true;  // what is left of the zeros it wrote stays
+  } else {
+    const hipError_t e = launch_argsort_marked(ids, N, B, K, buf.sort, &kv, &mark, s);
+    if (e != hipSuccess) return e;
+  }
   const int U = grad_unit(n, D);
   const int Dp = (D + 3) / 4 * 4;
-  int64_t units = grad_units(n, D, 0);
-#define FKM_SUM(LPR) \
-  sum_launch<TI, TO, V, LPR>(dout, kv, n, mark, U, units, nv, entries, scale, acc, grad, buf.frag[0], buf.any[0], Dp, s)
+  int64_t units = 0, W = U;
+#define FKM_SUM(LPR)                                                                                                  \
+  units = sum_launch<TI, TO, V, LPR>(dout, kv, n, mark, U, nv, entries, mode, grad, buf.frag[0], buf.any[0], Dp, s), \
+  W *= kGroups<LPR>
   if (nv <= 4) FKM_SUM(4);
   else if (nv <= 8) FKM_SUM(8);
   else if (nv <= 16) FKM_SUM(16);
@@ -487,12 +663,11 @@ hipError_t embed_grad_v(const void* dout, const int32_t* ids, int64_t N, int K, 
 #undef FKM_SUM
   constexpr int VJ = V >= 4 ? 4 : 1;
   const int nslab = (D / VJ + 63) / 64;
-  int64_t W = U;
   for (int level = 0; units > 1; ++level) {
     const int64_t groups = (units + kJoin - 1) / kJoin;
     const int waves = units < kJoin ? (int)((units + kRange - 1) / kRange) : 16;
     embed_grad_join_kernel<TO, VJ><<<dim3((unsigned)(groups * nslab)), dim3(waves * 64), 0, s>>>(
-        kv, n, W, units, nslab, buf.frag[level], buf.any[level], Dp, D / VJ, scale, acc,
+        kv, n, W, units, nslab, buf.frag[level], buf.any[level], Dp, D / VJ, mode,
         static_cast<typename TO::raw*>(grad), buf.frag[level + 1], buf.any[level + 1]);
     W *= kJoin;
     units = groups;

@@ -239,19 +239,14 @@ hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids,
 // The rows of the sorted order are summed by units of U rows and slabs of columns; pieces of an entry's segment that
 // cross a unit's edge go to fragments, two per unit, which are joined kJoin units at a time.
 constexpr int64_t kGradDirect = 256;  // up to this many rows the gradient needs no sort
+constexpr int kSortOne = 16384;       // up to this many rows are sorted by one workgroup, where a word holds them
 constexpr int kSlack = 32;             // readable pairs that the gradient's sort buffers have past the last row
 constexpr int kJoin = 256;            // units joined by one workgroup (16 waves of 16)
 // Rows per unit for n rows of D columns: 16 to 256, so that the waves (of 512 columns) number about 8,192.
-#ifndef FKM_GW
-#define FKM_GW 8192
-#endif
-#ifndef FKM_UMAX
-#define FKM_UMAX 256
-#endif
 inline int grad_unit(int64_t n, int D) {
   const int64_t slabs = (D + 511) / 512, per = D <= 256 ? 512 / (D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256) : 1;
   int u = 16;
-  while (u < FKM_UMAX && n * slabs / per / u > FKM_GW) u *= 2;
+  while (u < 256 && n * slabs / per / u > 8192) u *= 2;
   return u;
 }
 struct GradBuffers {
@@ -261,8 +256,9 @@ struct GradBuffers {
   float* frag[4];
   uint32_t* any[4];
 };
+// Units with fragments per level, at most: a workgroup joins 4 units or more before the first level.
 inline int64_t grad_units(int64_t n, int D, int level) {
-  int64_t u = (n + grad_unit(n, D) - 1) / grad_unit(n, D);
+  int64_t u = (n + 4 * grad_unit(n, D) - 1) / (4 * grad_unit(n, D));
   for (int i = 0; i < level; ++i) u = (u + kJoin - 1) / kJoin;
   return u;
 }
