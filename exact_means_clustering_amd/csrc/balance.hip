@@ -26,23 +26,44 @@ namespace fkm {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kFold = 64;  // rows a column sum takes in fp32 before it is added in fp64
+constexpr int kFold = kBalanceFold;
 
 __device__ __forceinline__ float exp_diff(float x, float shift) {
   return __builtin_amdgcn_exp2f((x - shift) * kLog2e);
 }
 
-template <int LPR>
-__device__ __forceinline__ float team_max(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+// The value of the lane paired with this one: neighbours, pairs, then mirrored
+// halves of 8 and 16 lanes (within which every lane already holds the same).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int i = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(i, i, CTRL, 0xF, 0xF, true));
+}
+// op over the LPR lanes of a team (a power of two, aligned), in every lane.
+// All lanes of the wave take part.
+template <int LPR, class Op>
+__device__ __forceinline__ float team_op(float v, Op op) {
+  if constexpr (LPR >= 2) v = op(v, dpp<0xB1>(v));    // quad_perm 1,0,3,2
+  if constexpr (LPR >= 4) v = op(v, dpp<0x4E>(v));    // quad_perm 2,3,0,1
+  if constexpr (LPR >= 8) v = op(v, dpp<0x141>(v));   // row_half_mirror
+  if constexpr (LPR >= 16) v = op(v, dpp<0x140>(v));  // row_mirror
+  if constexpr (LPR >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
+  if constexpr (LPR >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+  }
   return v;
 }
 template <int LPR>
+__device__ __forceinline__ float team_max(float v) {
+  return team_op<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LPR>
 __device__ __forceinline__ float team_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  return team_op<LPR>(v, [](float a, float b) { return a + b; });
 }
 
 // What the forward pass writes for one instance.
@@ -94,25 +115,23 @@ struct Rows {
   static constexpr int STEP = TEAMS * SL;       // rows per workgroup and step
   static_assert(W == 1 || (LPR == 64 && TEAMS == 1), "a wide team is the workgroup");
   Pack<T, V> p[NV];
-  // the row's words of lane g of the team; zeros past it and for a row
-  // that is not live
+  // the row's words of lane g of the team; -inf past it and for a row that is
+  // not live
   __device__ __forceinline__ void load(const typename T::raw* row, int g, int K, bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int c = (j * LPR * W + g) * V;
       if (live && c < K) p[j].load(row + c);
-      else p[j].zero();
+      else p[j].fill_neg_inf();
     }
   }
-  // values as fp32, -inf past the row
-  __device__ __forceinline__ void values(float (&x)[E], int g, int K) const {
+  __device__ __forceinline__ void values(float (&x)[E]) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float f[V];
       p[j].unpack(f);
-      const bool in = (j * LPR * W + g) * V < K;
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[j * V + v] = in ? f[v] : -INFINITY;
+      for (int v = 0; v < V; ++v) x[j * V + v] = f[v];
     }
   }
 };
@@ -140,10 +159,16 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
   for (int k = tid; k < K; k += R::BLOCK) hist[k] = 0;
   if (tid == 0) nval = 0;
 
+  // (16-wave teams have no registers for fp64 sums: they take kFold steps at most)
+  constexpr bool FOLDS = W < 16;
   float acc[E];
-  double sum[E];
+  double sum[FOLDS ? E : 1];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f, sum[e] = 0.0;
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  if constexpr (FOLDS) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] = 0.0;
+  }
   int mine = 0;  // valid rows of this team
   auto is_live = [&](int64_t i) { return i < i1 && (!valid || valid[base + i]); };
   R next;
@@ -159,7 +184,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
     next_live = t + 1 < steps && is_live(i + R::STEP);
     next.load(logits + (base + i + R::STEP) * K, g, K, next_live);
     float x[E];
-    cur.values(x, g, K);
+    cur.values(x);
     float m = x[0];
 #pragma unroll
     for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
@@ -196,19 +221,26 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
       lse[base + i] = !live ? INFINITY : s == 0.f ? -INFINITY : m + logf(s);
       mine += live;
     }
-    // a row that leaves no probability adds nothing, whatever its words hold
-    const bool adds = live && s != 0.f;
-    const float q = adds ? scale / s : 0.f;
+    // a row that leaves no probability has exponentials of 0 only
+    const float q = s != 0.f ? scale / s : 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += adds ? x[e] * q : 0.f;
-    if (++fold == kFold) {
-      fold = 0;
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], q, acc[e]);
+    if constexpr (FOLDS) {
+      if (++fold == kFold) {
+        fold = 0;
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum[e] += (double)acc[e], acc[e] = 0.f;
+        for (int e = 0; e < E; ++e) sum[e] += (double)acc[e], acc[e] = 0.f;
+      }
     }
   }
+  if constexpr (FOLDS) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) sum[e] += (double)acc[e];
+    for (int e = 0; e < E; ++e) sum[e] += (double)acc[e];
+  }
+  auto total = [&](int e) -> double {
+    if constexpr (FOLDS) return sum[e];
+    else return (double)acc[e];
+  };
 
   // counts of the chunk's labels: integer LDS atomics, exact in any order
   const int64_t l0 = (base + i0) * S, l1 = (base + i1) * S;
@@ -255,9 +287,9 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
       const int k = ((e / V) * R::BLOCK + g) * V + e % V;
       if (k >= K) continue;
       if (chunks == 1) {
-        term += balance_entry(out, b * K + k, K, S, T_, sum[e], hist[k]);
+        term += balance_entry(out, b * K + k, K, S, T_, total(e), hist[k]);
       } else {
-        part[at + k] = (float)sum[e];
+        part[at + k] = (float)total(e);
         cpart[at + k] = hist[k];
       }
     }
@@ -362,7 +394,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
     next_z = t + 1 < steps ? z_of(i + R::STEP) : INFINITY;
     next.load(logits + (base + i + R::STEP) * K, g, K, is_live(next_z));
     float x[E];
-    cur.values(x, g, K);
+    cur.values(x);
     float s = 0.f, d = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {

@@ -11,6 +11,11 @@ template <> __device__ __forceinline__ float round_to<F32>(float f) { return f; 
 template <> __device__ __forceinline__ uint16_t round_to<F16>(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
 template <> __device__ __forceinline__ uint16_t round_to<BF16>(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
 
+// The 16-bit types' -infinity.
+template <class T> constexpr uint32_t neg_inf_bits() { return 0; }
+template <> constexpr uint32_t neg_inf_bits<F16>() { return 0xFC00u; }
+template <> constexpr uint32_t neg_inf_bits<BF16>() { return 0xFF80u; }
+
 // 16 * words bytes of V elements, moved with the widest accesses that the
 // V elements' own size allows (16 bytes for V = 8, or 4 of fp32).  The address
 // is aligned to the smaller of 16 bytes and the vector's size.
@@ -64,6 +69,11 @@ template <class T, int V> struct Pack {
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void fill_neg_inf() {
+    constexpr uint32_t h = T::SZ == 4 ? 0xFF800000u : neg_inf_bits<T>();
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = T::SZ == 4 ? h : h | h << 16;
   }
   __device__ __forceinline__ void unpack(float* o) const {
     if constexpr (T::SZ == 4) {
