@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void embed_kernel(const typename TI::raw* __re
       }
       Pack<TO, V> o;
       o.pack(f);
-      o.store(out + dst[u]);
+      o.store_nt(out + dst[u]);
     }
   }
 }
@@ -300,8 +300,8 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
 // left goes to the unit's fragment 0, one that starts here and continues to
 // the right to fragment 1; the workgroup joins its units' fragments in LDS
 // before any reaches memory.  Rows whose word carries the mark leave nothing.
-// The workgroups past the sums zero the entries no row has (not when they
-// keep what they hold), finding each by a binary search.
+// The first workgroups zero the entries no row has (unless those keep what
+// they hold), finding each by a binary search whose waits the sums fill.
 constexpr int kAhead = 8;
 template <int LPR>
 constexpr int kGroups = 256 / LPR;
@@ -309,7 +309,7 @@ static_assert(3 * kAhead <= kSlack, "pairs read past the last row");
 template <class TI, class TO, int V, int LPR>
 __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::raw* __restrict__ dout,
                                                              const uint2* __restrict__ kv, int64_t n, uint32_t mark,
-                                                             int U, int64_t units, int64_t sum_blocks, int nv,
+                                                             int U, int64_t units, int64_t zero_blocks, int nv,
                                                              int nslab, int64_t entries, int per, PutMode mode,
                                                              typename TO::raw* __restrict__ grad,
                                                              float* __restrict__ frag, uint32_t* __restrict__ fany,
@@ -320,10 +320,9 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::
   __shared__ uint32_t sany[GPB * 2];
   const int lane = lane_id();
   const int w = threadIdx.x >> 6;
-  if ((int64_t)blockIdx.x >= sum_blocks) {
+  if ((int64_t)blockIdx.x < zero_blocks) {
     const int64_t zero_units = (entries + per - 1) / per;
-    for (int64_t u = ((int64_t)blockIdx.x - sum_blocks) * 4 + w; u < zero_units;
-         u += ((int64_t)gridDim.x - sum_blocks) * 4) {
+    for (int64_t u = (int64_t)blockIdx.x * 4 + w; u < zero_units; u += zero_blocks * 4) {
       const int64_t e = u * per + lane;
       bool absent = false;
       if (lane < per && e < entries) {
@@ -339,8 +338,9 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(const typename TI::
     }
     return;
   }
-  const int64_t ub = (int64_t)blockIdx.x / nslab;  // the workgroup's units: GPB from ub * GPB
-  const int slab = (int)((int64_t)blockIdx.x - ub * nslab);
+  const int64_t sb = (int64_t)blockIdx.x - zero_blocks;
+  const int64_t ub = sb / nslab;  // the workgroup's units: GPB from ub * GPB
+  const int slab = (int)(sb - ub * nslab);
   const int grp = threadIdx.x / LPR, gl = threadIdx.x % LPR;
   const int64_t unit = ub * GPB + grp;
   if (unit < units) {
@@ -480,7 +480,7 @@ int64_t sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, 
   const int per = zero_per(nv * V * TO::SZ);
   const int64_t zero_blocks = mode.keep ? 0 : zero_grid((entries + 4 * per - 1) / (4 * per));
   embed_grad_sum_kernel<TI, TO, V, LPR><<<dim3((unsigned)(sum_blocks + zero_blocks)), dim3(256), 0, s>>>(
-      static_cast<const typename TI::raw*>(dout), kv, n, mark, U, units, sum_blocks, nv, nslab, entries, per, mode,
+      static_cast<const typename TI::raw*>(dout), kv, n, mark, U, units, zero_blocks, nv, nslab, entries, per, mode,
       static_cast<typename TO::raw*>(grad), frag, fany, Dp);
   return ublocks;
 }

@@ -268,7 +268,7 @@ hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* 
 // Balance loss and its gradient (see flashkm_codebook.h for the formulas).
 constexpr int kBalanceMaxK = 16384;   // longest rows kept in registers
 constexpr int kBalanceJoinCols = 32;  // fewest columns per workgroup that joins chunk sums
-constexpr int kBalanceFold = 64;      // rows a column sum takes in fp32 before it is added in fp64
+constexpr int kBalanceFold = 64;      // rows of a block of a column sum, and the most blocks of one
 constexpr int kBalanceRows = 256;     // rows per column-sum chunk of longer rows
 // Rows a workgroup takes at a time: 4 waves of 64 / LPR rows, LPR lanes of 8
 // elements a row, up to 512; then a wave (16 elements a lane), 4 or 16 waves a row.
@@ -288,7 +288,7 @@ inline BalanceSplit balance_split(int64_t N, int B, int K) {
   const int64_t all = (N + balance_step(K) - 1) / balance_step(K);
   int64_t steps = (all + want - 1) / want;
   if (steps < 4) steps = 4;
-  if (K > 4096 && steps > kBalanceFold) steps = kBalanceFold;
+  if (steps > kBalanceFold * kBalanceFold) steps = kBalanceFold * kBalanceFold;
   return BalanceSplit{(int)steps, all > 0 ? (all + steps - 1) / steps : 1};
 }
 inline int64_t balance_wide_chunks(int64_t N) { return N > 0 ? (N + kBalanceRows - 1) / kBalanceRows : 1; }

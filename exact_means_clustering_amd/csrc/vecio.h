@@ -66,6 +66,18 @@ template <class T, int V> struct Pack {
       *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
     }
   }
+  // the same, streamed past the caches (data written once and not read here)
+  __device__ __forceinline__ void store_nt(typename T::raw* p) const {
+    if constexpr (BYTES >= 16) {
+      typedef unsigned int v4u __attribute__((ext_vector_type(4)));
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i)
+        __builtin_nontemporal_store(v4u{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]},
+                                    reinterpret_cast<v4u*>(p) + i);
+    } else {
+      store(p);
+    }
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0u;
