@@ -448,19 +448,30 @@ def _on_stream(fn):
     belongs to the stream that uses it."""
     @functools.wraps(fn)
     def run(*args, stream=None, **kwargs):
-        t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
-        if t is None:
-            return fn(*args, **kwargs)
+        t = args[0] if args else None
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            t = next((a for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor) and a.is_cuda), None)
+            if t is None:
+                return fn(*args, **kwargs)
         if stream is not None:
             if stream.device != t.device:
                 raise KMeansError(KM_EINVAL, f"stream is on {stream.device}, the tensors on {t.device}")
             with torch.cuda.stream(stream):
                 return fn(*args, **kwargs)
-        if t.device.index == torch.cuda.current_device():
+        if t.get_device() == torch.cuda.current_device():
             return fn(*args, **kwargs)
         with torch.cuda.device(t.device):
             return fn(*args, **kwargs)
     return run
+
+
+# torch's own shortcut to the current stream's handle (2.7 us less per call than building a Stream object)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _current(t):
+    return _raw_stream(t.get_device())
 
 
 def _int32(v, name):
@@ -490,10 +501,17 @@ def _scratch(need, device, ws):
         msg = _lib.kmeans_last_error().decode(errors="replace")
         raise KMeansError(KM_EUNSUPPORTED if msg.startswith("unsupported") else KM_EINVAL, msg)
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        if need == 256:  # the shape needs none
+            return None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws, need
     if not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.device != device or not ws.is_contiguous():
         raise KMeansError(KM_EINVAL, f"ws must be a contiguous tensor on {device}")
     return ws, ws.numel() * ws.element_size()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 @_on_stream
@@ -514,8 +532,8 @@ def embed(table, ids, *, scale: float = 1.0, out_dtype=None, out=None):
         out = torch.empty((*ids.shape, D), dtype=out_dtype or table.dtype, device=table.device)
     else:
         _into(out, "out", (*ids.shape, D), out_dtype, table)
-    _check(_lib.kmeans_embed(_ptr(table), dt, ids.shape[-1], K, D, B, _ptr(ids), float(scale), _ptr(out), _dtype(out),
-                             _stream(None)))
+    _check(_lib.kmeans_embed(table.data_ptr(), dt, ids.shape[-1], K, D, B, ids.data_ptr(), float(scale),
+                             out.data_ptr(), _dtype(out), _current(table)))
     return out
 
 
@@ -545,8 +563,8 @@ def embed_grad(dout, ids, K: int, *, scale: float = 1.0, grad_dtype=None, out=No
         out = torch.empty(shape, dtype=grad_dtype or torch.float32, device=dout.device)
     else:
         _into(out, "out", shape, grad_dtype, dout)
-    _check(_lib.kmeans_embed_grad(_ptr(dout), dt, N, K, D, B, _ptr(ids), float(scale), int(bool(accumulate)), _ptr(out),
-                                  _dtype(out), _ptr(ws), ws_bytes, _stream(None)))
+    _check(_lib.kmeans_embed_grad(dout.data_ptr(), dt, N, K, D, B, ids.data_ptr(), float(scale), int(bool(accumulate)),
+                                  out.data_ptr(), _dtype(out), _at(ws), ws_bytes, _current(dout)))
     return out
 
 
@@ -582,8 +600,9 @@ def balance(logits, labels, *, valid=None, ws=None):
     prob = torch.empty(per, dtype=torch.float32, device=logits.device)
     coef = torch.empty(per, dtype=torch.float32, device=logits.device)
     lse = torch.empty(lead, dtype=torch.float32, device=logits.device)
-    _check(_lib.kmeans_balance(_ptr(logits), dt, N, K, B, _ptr(labels), S, _ptr(valid), _ptr(loss), _ptr(counts),
-                               _ptr(prob), _ptr(lse), _ptr(coef), _ptr(ws), ws_bytes, _stream(None)))
+    _check(_lib.kmeans_balance(logits.data_ptr(), dt, N, K, B, labels.data_ptr(), S, _at(valid), loss.data_ptr(),
+                               counts.data_ptr(), prob.data_ptr(), lse.data_ptr(), coef.data_ptr(), _at(ws), ws_bytes,
+                               _current(logits)))
     return loss, counts, prob, (lse, coef)
 
 
@@ -600,6 +619,6 @@ def balance_grad(logits, saved, dloss, *, out=None):
         out = torch.empty_like(logits)
     else:
         _into(out, "out", logits.shape, logits.dtype, logits)
-    _check(_lib.kmeans_balance_grad(_ptr(logits), dt, N, K, B, _ptr(lse), _ptr(coef), _ptr(dloss), _ptr(out),
-                                    _stream(None)))
+    _check(_lib.kmeans_balance_grad(logits.data_ptr(), dt, N, K, B, lse.data_ptr(), coef.data_ptr(), dloss.data_ptr(),
+                                    out.data_ptr(), _current(logits)))
     return out

@@ -66,7 +66,11 @@ int check_arrays(const Arr (&a)[M]) {
   return KM_OK;
 }
 
+// The smallest workspace size: what a shape without need of one is given.
+constexpr size_t kNoWorkspace = 256;
+
 int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == kNoWorkspace) return KM_OK;
   if (ws_bytes < need) return fail(KM_EWORKSPACE, "workspace too small: %zu bytes given, %zu needed", ws_bytes, need);
   if (!ws) return fail(KM_EINVAL, "workspace pointer is null");
   if (((uintptr_t)ws & 255) != 0) return fail(KM_EINVAL, "workspace must be 256-byte aligned");
@@ -80,17 +84,19 @@ struct GradLayout {
 GradLayout grad_layout(int64_t N, int K, int D, int B) {
   GradLayout L{};
   const int64_t n = N * B;
-  size_t o = 256;
-  if (n > kGradDirect) {
-    L.kv0 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
-    L.kv1 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
-    L.hist = o;  o = al256(o + (size_t)sort_hist_words(N, B, K) * 4);
-    L.dtot = o;  o = al256(o + ((size_t)1 << kSortWideBits) * 4);
-    for (int i = 0; i < 3; ++i) {
-      const size_t units = (size_t)grad_units(n, D, i);
-      L.frag[i] = o;  o = al256(o + units * 2 * ((D + 3) / 4 * 4) * 4);
-      L.any[i] = o;   o = al256(o + units * 2 * 4);
-    }
+  if (n <= kGradDirect) {
+    L.total = kNoWorkspace;
+    return L;
+  }
+  size_t o = kNoWorkspace;
+  L.kv0 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
+  L.kv1 = o;   o = al256(o + (size_t)(n + kSlack) * 8);
+  L.hist = o;  o = al256(o + (size_t)sort_hist_words(N, B, K) * 4);
+  L.dtot = o;  o = al256(o + ((size_t)1 << kSortWideBits) * 4);
+  for (int i = 0; i < 3; ++i) {
+    const size_t units = (size_t)grad_units(n, D, i);
+    L.frag[i] = o;  o = al256(o + units * 2 * ((D + 3) / 4 * 4) * 4);
+    L.any[i] = o;   o = al256(o + units * 2 * 4);
   }
   L.total = o;
   return L;
@@ -104,7 +110,11 @@ BalanceLayout balance_layout(int64_t N, int K, int B) {
   const bool wide = K > kBalanceMaxK;
   const int64_t chunks = wide ? balance_wide_chunks(N) : balance_split(N, B, K).chunks;
   const size_t cells = wide || chunks > 1 ? (size_t)B * chunks * K : 0;  // one chunk is finished where it is summed
-  size_t o = 256;
+  if (!cells) {
+    L.total = kNoWorkspace;
+    return L;
+  }
+  size_t o = kNoWorkspace;
   L.part = o;   o = al256(o + cells * 4);
   L.cpart = o;  o = al256(o + (wide ? 0 : cells * 4));
   L.vpart = o;  o = al256(o + (wide ? (size_t)B : (size_t)B * chunks) * 4);
@@ -172,7 +182,7 @@ int kmeans_embed_grad(const void* dout, int32_t dout_dtype, int64_t N, int32_t K
   const Arr arrs[] = {{"dout", dout, n * D * isz, (unsigned)isz, false},
                       {"ids", ids, n * 4, 4, false},
                       {"grad", grad, (uint64_t)B * K * D * gsz, (unsigned)gsz, true},
-                      {"workspace", ws, L.total, 1, true}};
+                      {"workspace", ws, L.total == kNoWorkspace ? 0 : L.total, 1, true}};
   if (int rc = check_arrays(arrs)) return rc;
   if (n == 0 && accumulate) return KM_OK;
   char* base = static_cast<char*>(ws);
@@ -214,7 +224,7 @@ int kmeans_balance(const void* logits, int32_t dtype, int64_t N, int32_t K, int3
                       {"prob", prob, e * 4, 4, true},
                       {"lse", lse, n * 4, 4, true},
                       {"coef", coef, e * 4, 4, true},
-                      {"workspace", ws, L.total, 1, true}};
+                      {"workspace", ws, L.total == kNoWorkspace ? 0 : L.total, 1, true}};
   if (int rc = check_arrays(arrs)) return rc;
   char* base = static_cast<char*>(ws);
   BalanceBuffers buf{};

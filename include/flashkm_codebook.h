@@ -42,7 +42,8 @@ KM_API int kmeans_embed(const void* table, int32_t table_dtype, int64_t N, int32
                         const int32_t* ids, float scale, void* out, int32_t out_dtype, void* stream);
 
 /* Bytes of device workspace kmeans_embed_grad needs for this shape (0 for an
- * invalid shape; the same for every type). */
+ * invalid shape; 256 where none is needed: `ws` may then be null; the same for
+ * every type). */
 KM_API size_t kmeans_embed_grad_workspace_bytes(int64_t N, int32_t K, int32_t D, int32_t B);
 
 /* Gradient of the lookup with respect to the table:
@@ -58,7 +59,8 @@ KM_API int kmeans_embed_grad(const void* dout, int32_t dout_dtype, int64_t N, in
                              void* ws, size_t ws_bytes, void* stream);
 
 /* Bytes of device workspace kmeans_balance needs for this shape (0 for an
- * invalid shape; the same for every type). */
+ * invalid shape; 256 where none is needed: `ws` may then be null; the same for
+ * every type). */
 KM_API size_t kmeans_balance_workspace_bytes(int64_t N, int32_t K, int32_t B, int32_t S);
 
 /* Balance loss of the use of K choices by N rows, with counts:

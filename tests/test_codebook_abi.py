@@ -74,7 +74,7 @@ def test_embed_of_no_rows_is_nothing(lib):
     assert embed(lib, N=0, ids=None, out=None) == 0
 
 
-def grad(lib, dout=at(0), idt=BF16, N=10, K=20, D=64, B=1, ids=at(1), acc=0, g=at(2), gdt=F32, ws=at(3), wb=1 << 30):
+def grad(lib, dout=at(0), idt=BF16, N=1000, K=20, D=64, B=1, ids=at(1), acc=0, g=at(2), gdt=F32, ws=at(3), wb=1 << 30):
     return lib.kmeans_embed_grad(dout, idt, N, K, D, B, ids, 1.0, acc, g, gdt, ws, wb, None)
 
 
@@ -102,6 +102,16 @@ def test_embed_grad_refusals(lib, kw, code, word):
 
 def test_embed_grad_of_no_rows_accumulated_is_nothing(lib):
     assert grad(lib, N=0, dout=None, ids=None, acc=1) == 0
+    assert grad(lib, N=0, dout=None, ids=None, acc=1, ws=None, wb=0) == 0
+
+
+def test_few_rows_need_no_workspace(lib):
+    # 256 bytes stand for none; a misaligned or overlapping one is then of no consequence, other faults still are
+    assert lib.kmeans_embed_grad_workspace_bytes(256, 20, 64, 1) == 256
+    assert lib.kmeans_embed_grad_workspace_bytes(257, 20, 64, 1) > 256
+    assert lib.kmeans_balance_workspace_bytes(32, 8, 1, 2) == 256
+    assert grad(lib, N=10, ws=None, wb=0, dout=None) == EINVAL and "dout" in err(lib)
+    assert balance(lib, N=10, ws=None, wb=0, labels=None) == EINVAL and "labels" in err(lib)
 
 
 def test_workspace_sizes(lib):
@@ -116,7 +126,7 @@ def test_workspace_sizes(lib):
     assert g(1 << 20, 1024, 1, 1) < (1 << 20) * 1024 // 8
 
 
-def balance(lib, x=at(0), dt=F16, N=10, K=20, B=1, labels=at(1), S=2, valid=at(2), loss=at(3), counts=at(4), prob=at(5),
+def balance(lib, x=at(0), dt=F16, N=10000, K=20, B=1, labels=at(1), S=2, valid=at(2), loss=at(3), counts=at(4), prob=at(5),
             lse=at(6), coef=at(7), ws=at(8), wb=1 << 30):
     return lib.kmeans_balance(x, dt, N, K, B, labels, S, valid, loss, counts, prob, lse, coef, ws, wb, None)
 
@@ -125,6 +135,7 @@ def balance(lib, x=at(0), dt=F16, N=10, K=20, B=1, labels=at(1), S=2, valid=at(2
     (dict(dt=3), EUNSUPPORTED, "dtype"),
     (dict(K=0), EINVAL, "K=0"),
     (dict(B=-1), EINVAL, "B=-1"),
+    (dict(B=(1 << 22) + 1, N=1), EINVAL, "B=4194305"),
     (dict(S=0), EINVAL, "S=0"),
     (dict(N=1 << 28, S=8), EINVAL, "B*N*S"),
     (dict(N=-7), EINVAL, "N=-7"),
