@@ -6,7 +6,7 @@
 // whole waves, holds one row, E elements a lane, as 16-byte words where the
 // row allows it.  Forward, a lane owns its columns: after the row's maximum
 // and sum it adds its probabilities to its own column sums (fp32, by blocks of
-// kFold rows, then fp64 from the lanes' sums on), so the probabilities are
+// kFold rows and over the lanes of a wave, then fp64), so the probabilities are
 // never written and the logits are read once.  A workgroup covers a chunk of rows of one
 // instance and leaves one partial sum per column (and its counts, from an LDS
 // histogram of integers); a second launch adds the chunks in a fixed order.
@@ -31,6 +31,7 @@ constexpr int kFold = kBalanceFold;
 // forward 463 us with 1, 443 with 2, 444 with 4; backward with the caches'
 // streaming hints 871 us with 2, 807 with 4).
 constexpr int kAheadF = 2, kAheadB = 4;
+constexpr int kEarly = 2;  // labels a thread reads ahead of the rows
 
 __device__ __forceinline__ float exp_diff(float x, float shift) {
   return __builtin_amdgcn_exp2f((x - shift) * kLog2e);
@@ -68,6 +69,25 @@ __device__ __forceinline__ float team_max(float v) {
 template <int LPR>
 __device__ __forceinline__ float team_sum(float v) {
   return team_op<LPR>(v, [](float a, float b) { return a + b; });
+}
+
+// v summed over the 64 / LPR lanes of a wave that are LPR apart, in every one of
+// them (rotations within 16 lanes, then swaps of 16 and 32).
+template <int LPR>
+__device__ __forceinline__ float slot_sum(float v) {
+  if constexpr (LPR <= 1) v += dpp<0xB1>(v);   // quad_perm 1,0,3,2
+  if constexpr (LPR <= 2) v += dpp<0x4E>(v);   // quad_perm 2,3,0,1
+  if constexpr (LPR <= 4) v += dpp<0x124>(v);  // row_ror 4
+  if constexpr (LPR <= 8) v += dpp<0x128>(v);  // row_ror 8
+  if constexpr (LPR <= 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (LPR <= 32) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return v;
 }
 
 // What the forward pass writes for one instance.
@@ -140,15 +160,18 @@ struct Rows {
   }
 };
 
+// (Waves of 16 values a lane: five per SIMD instead of four, 423 against 432 us
+// for 1,048,576 x 1,024 bf16.)
 template <class T, int V, int NV, int LPR, int W>
-__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_kernel(
+__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK), (W == 1 && V * NV == 16 && V > 1 ? 5 : 1))
+void balance_rows_kernel(
     const typename T::raw* __restrict__ logits, int64_t N, int K, const int32_t* __restrict__ labels, int S,
     const uint8_t* __restrict__ valid, float* __restrict__ lse, int64_t chunks, int steps, float* __restrict__ part,
     int32_t* __restrict__ cpart, int32_t* __restrict__ vpart, BalanceOut out) {
   using R = Rows<T, V, NV, LPR, W>;
   constexpr int E = R::E, WAVES = R::WAVES;
   __shared__ int hist[R::MAXK];
-  __shared__ double col[W == 1 ? R::MAXK : 1];
+  __shared__ float col[W == 1 ? WAVES * R::MAXK : 1];
   __shared__ float2 xch[2][W == 1 ? 1 : W];
   __shared__ double tmp[WAVES];
   __shared__ int nval;
@@ -178,6 +201,15 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
   };
 #pragma unroll
   for (int h = 0; h < kAheadF; ++h) refill(h, h);
+  // the first labels are read now and counted after the rows
+  const int64_t l0 = (base + i0) * S, l1 = (base + i1) * S;
+  auto label_at = [&](int64_t l) -> uint32_t {  // ~0 if it names nothing
+    if (l >= l1 || (valid && !valid[(uint32_t)l / (uint32_t)S])) return ~0u;
+    return (uint32_t)labels[l];
+  };
+  uint32_t early[kEarly];
+#pragma unroll
+  for (int q = 0; q < kEarly; ++q) early[q] = label_at(l0 + tid + q * R::BLOCK);
   __syncthreads();  // the histogram is clear
   int fold = 0;
   auto step = [&](int t, int h) {
@@ -241,44 +273,40 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_rows_
   for (int e = 0; e < E; ++e) sum[e] += acc[e];
 
   // counts of the chunk's labels: integer LDS atomics, exact in any order
-  const int64_t l0 = (base + i0) * S, l1 = (base + i1) * S;
-  for (int64_t l = l0 + tid; l < l1; l += R::BLOCK) {
-    const uint32_t k = (uint32_t)labels[l];
-    if (k < (uint32_t)K && (!valid || valid[(uint32_t)l / (uint32_t)S])) atomicAdd(&hist[k], 1);
+#pragma unroll
+  for (int q = 0; q < kEarly; ++q)
+    if (early[q] < (uint32_t)K) atomicAdd(&hist[early[q]], 1);
+  for (int64_t l = l0 + tid + kEarly * R::BLOCK; l < l1; l += R::BLOCK) {
+    const uint32_t k = label_at(l);
+    if (k < (uint32_t)K) atomicAdd(&hist[k], 1);
   }
   if (mine) atomicAdd(&nval, mine);
 
-  // column sums: lanes of one column add in a fixed order, then the waves
+  // column sums: lanes of one column, then (below) the waves, in fixed orders
   if constexpr (W == 1) {
-    double total[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      total[e] = sum[e];
-#pragma unroll
-      for (int o = LPR; o < 64; o <<= 1) total[e] += __shfl_xor(total[e], o);
+      const float total = slot_sum<LPR>(sum[e]);
+      const int k = ((e / V) * LPR + g) * V + e % V;
+      if (lane < LPR && k < K) col[w * R::MAXK + k] = total;
     }
-    for (int q = 0; q < WAVES; ++q) {
-      if (w == q && lane < LPR) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int k = ((e / V) * LPR + g) * V + e % V;
-          if (k < K) col[k] = q ? col[k] + total[e] : total[e];
-        }
-      }
-      __syncthreads();
-    }
-  } else {
-    __syncthreads();
   }
+  __syncthreads();
+  auto column = [&](int k) {
+    double s = 0.0;
+#pragma unroll
+    for (int q = 0; q < WAVES; ++q) s += (double)col[q * R::MAXK + k];
+    return s;
+  };
   const double T_ = nval;
   const int64_t at = (b * chunks + c) * K;
   double term = 0.0;
   if constexpr (W == 1) {
     for (int k = tid; k < K; k += R::BLOCK) {
       if (chunks == 1) {
-        term += balance_entry(out, b * K + k, K, S, T_, col[k], hist[k]);
+        term += balance_entry(out, b * K + k, K, S, T_, column(k), hist[k]);
       } else {
-        part[at + k] = (float)col[k];
+        part[at + k] = (float)column(k);
         cpart[at + k] = hist[k];
       }
     }

@@ -8,7 +8,9 @@ Tolerances count roundings (u = 2^-24, half a step of fp32; half a step of the o
   balance       with R the largest |logit - maximum| that still leaves a probability (exp of less than -104 is 0 in fp32),
                 an exponential is off by (R + 4) u relative (the difference's rounding, its scaling, exp itself), a row's sum by
                 another (K / 64 + 24) u (lanes add at most K / 64 + 16 values one after another, then 6 levels of pairs), a
-                column's by ROWS u more, ROWS the rows summed one after another in fp32.
+                column's by ROWS u more (blocks of 64 rows added one after another), by one u a block (4 at most here) and by 6
+                over a wave's lanes, which the 24 of the row's sum and the 8 leave room for (the row's own sums of at most 16
+                values and 6 levels take 22 of them only where a lane has 16 values, and then a wave holds one row).
   balance_grad  p is off by an exponential and a row's sum as above; the mean of coef under p by that and a sum's depth; the
                 difference, the products and the output's type add 4 u and half a step.
 """
@@ -181,7 +183,10 @@ def check_grad(got, dout, ids, K, scale, old=None):
 GRAD_SHAPES = [(1, 1, 1, 1, "mixed"), (1, 37, 1000, 80, "mixed"), (1, 1000, 77, 128, "mixed"), (3, 129, 50, 12, "mixed"),
                (2, 333, 70, 1027, "zipf"), (1, 70, 11, 8200, "mixed"), (5, 1, 9, 16, "mixed"), (1, 5000, 300, 64, "zipf"),
                (1, 2049, 40, 256, "one"), (1, 65, 3, 24, "none"), (1, 500, 700, 32, "once"), (7, 300, 256, 16, "zipf"),
-               (2, 20000, 3, 8, "one"), (1, 70001, 5000, 20, "zipf"), (1, 17000, 70000, 8, "zipf"), (64, 40, 256, 32, "mixed")]
+               (2, 20000, 3, 8, "one"), (1, 70001, 5000, 20, "zipf"), (1, 17000, 70000, 8, "zipf"), (64, 40, 256, 32, "mixed"),
+               # one word cannot hold key and row (sorted by launches); just past each limit of the one-workgroup sorts
+               (1, 9000, 300000, 8, "zipf"), (1, 257, 33, 40, "zipf"), (2, 513, 40, 136, "mixed"), (1, 4097, 131072, 4, "mixed"),
+               (1, 8193, 1, 8, "one"), (1, 16385, 600, 8, "mixed")]
 
 
 @pytest.mark.parametrize("of, to", [(F32, F32), (BF16, F32), (F16, F32), (BF16, BF16), (F16, F16), (F32, BF16)])
@@ -533,6 +538,7 @@ def test_balance_offsets_past_32_bits(km):
 def test_refusals_on_the_gpu(km):
     t = torch.zeros(6, 8, device="cuda")
     i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    many, at = torch.zeros(300, 8, device="cuda"), torch.zeros(300, dtype=torch.int32, device="cuda")
     E = km.KMeansError
     for call in (lambda: km.embed(t, i.long()), lambda: km.embed(t, i[None]), lambda: km.embed(t[:, ::2], i),
                  lambda: km.embed(t.double(), i), lambda: km.embed(t, i, out=torch.zeros(3, 9, device="cuda")),
@@ -540,10 +546,12 @@ def test_refusals_on_the_gpu(km):
                  lambda: km.embed_grad(t, i, 4), lambda: km.embed_grad(t[:3], i, 0),
                  lambda: km.embed_grad(t[:3], i, 4, accumulate=True),
                  lambda: km.embed_grad(t[:3], i, 6, out=t), lambda: km.embed_grad(t[:3], i, 1 << 40),
-                 lambda: km.embed_grad(t[:3], i, 6, ws=torch.empty(8, device="cuda")),
+                 lambda: km.embed_grad(many, at, 6, ws=torch.empty(8, device="cuda")),
+                 lambda: km.embed_grad(many, at, 6, ws=torch.empty(1 << 20)),
                  lambda: km.balance(t, i), lambda: km.balance(t[:3], i.long()),
-                 lambda: km.balance(t[:3], i, valid=i), lambda: km.balance(t[:3], torch.empty(3, 0, dtype=torch.int32, device="cuda")),
-                 lambda: km.balance_grad(t, (i, i), i), lambda: km.balance_grad(t, (torch.zeros(6, device="cuda"),) * 2, i),
+                 lambda: km.balance(t[:3], i, valid=i), lambda: km.balance(t[:3], i.new_empty(3, 0)),
+                 lambda: km.balance_grad(t, (i, i), i),
+                 lambda: km.balance_grad(t, (torch.zeros(6, device="cuda"),) * 2, i),
                  lambda: km.balance_grad(t[:3], (torch.zeros(3, device="cuda"), torch.zeros(8, device="cuda")),
                                          torch.zeros(1, device="cuda"), out=t[:3])):
         with pytest.raises(E):
