@@ -132,7 +132,7 @@ template <class T, int V, int NV, int LPR, int W>
 struct Rows {
   static constexpr int E = V * NV;
   static constexpr int MAXK = LPR * W * E;
-  static constexpr int BLOCK = W == 16 ? 1024 : 256;
+  static constexpr int BLOCK = W > 4 ? 64 * W : 256;
   static constexpr int WAVES = BLOCK / 64;
   static constexpr int TEAMS = WAVES / W;       // teams of whole waves per workgroup
   static constexpr int SL = 64 / LPR;           // rows per wave and step
@@ -470,54 +470,100 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
 // ---------------------------------------------------------------------------
 // rows longer than the registers hold
 // ---------------------------------------------------------------------------
+// One workgroup per row, V elements per load; f(values, first column) over the
+// row's elements that thread tid takes, in order.
+template <class T, int V, class F>
+__device__ __forceinline__ void over_row(const typename T::raw* __restrict__ row, int K, F&& f) {
+#pragma unroll 4
+  for (int k = threadIdx.x * V; k < K; k += 256 * V) {
+    Pack<T, V> p;
+    float x[V];
+    p.load(row + k);
+    p.unpack(x);
+    f(x, k);
+  }
+}
+// (a, b) summed over the workgroup's 4 waves, in every thread.
+__device__ __forceinline__ float2 block_sum2(float a, float b, float2* tmp) {
+  a = team_sum<64>(a);
+  b = team_sum<64>(b);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = make_float2(a, b);
+  __syncthreads();
+  return make_float2((tmp[0].x + tmp[1].x) + (tmp[2].x + tmp[3].x), (tmp[0].y + tmp[1].y) + (tmp[2].y + tmp[3].y));
+}
+
 // lse of every row (+inf for an invalid one) and its (maximum, 1 / sum of
 // exponentials), (0, 0) for a row that leaves no probability: the
 // probabilities come from these, since a large lse has lost the sum's low
-// bits.  One wave per row.
-template <class T>
+// bits.  One read: a thread keeps a running maximum and the sum relative to it.
+template <class T, int V>
 __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw* __restrict__ logits, int64_t n, int K,
                                                           const uint8_t* __restrict__ valid, float* __restrict__ lse,
                                                           float2* __restrict__ ms) {
-  const int lane = lane_id();
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
-    if (valid && !valid[i]) {
-      if (lane == 0) lse[i] = INFINITY, ms[i] = make_float2(0.f, 0.f);
+  __shared__ float2 tmp[4];
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
+    if (valid && !valid[i]) {  // uniform over the workgroup
+      if (threadIdx.x == 0) lse[i] = INFINITY, ms[i] = make_float2(0.f, 0.f);
       continue;
     }
-    const typename T::raw* row = logits + i * K;
-    float m = -INFINITY;
-    for (int k = lane; k < K; k += 64) m = fmaxf(m, T::to_f32(row[k]));
-    m = team_max<64>(m);
-    const float shift = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-    for (int k = lane; k < K; k += 64) sum += exp_diff(T::to_f32(row[k]), shift);
-    sum = team_sum<64>(sum);
-    if (lane == 0) {
-      lse[i] = sum == 0.f ? -INFINITY : m + logf(sum);
+    float m = -INFINITY, s = 0.f;
+    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int) {
+      float top = x[0];
+#pragma unroll
+      for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
+      if (top > m) {  // the sum moves to the new maximum (from nothing, if that was -inf)
+        s *= exp_diff(m, top);
+        m = top;
+      }
+      const float shift = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int v = 0; v < V; ++v) s += exp_diff(x[v], shift);
+    });
+    // the workgroup's maximum, then the sums relative to it
+    const float wm = team_max<64>(m);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6].x = wm;
+    __syncthreads();
+    const float top = fmaxf(fmaxf(tmp[0].x, tmp[1].x), fmaxf(tmp[2].x, tmp[3].x));
+    const float shift = top == -INFINITY ? 0.f : top;
+    // a thread without a maximum holds 0 (or NaN), relative to 0
+    const float sum = block_sum2(m == -INFINITY ? s : s * exp_diff(m, shift), 0.f, tmp).x;
+    if (threadIdx.x == 0) {
+      lse[i] = sum == 0.f ? -INFINITY : top + logf(sum);
       ms[i] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(shift, 1.f / sum);
     }
   }
 }
 
-// part[b, chunk, k] = sum of p[b, i, k] over the chunk's valid rows; one
-// thread per column.
-template <class T>
+// part[b, chunk, k] = sum of p[b, i, k] over the chunk's valid rows; V columns
+// per thread.
+template <class T, int V>
 __global__ __launch_bounds__(256) void balance_cols_kernel(const typename T::raw* __restrict__ logits, int64_t N,
                                                            int K, int64_t chunks, int kblocks, int64_t units,
                                                            const float2* __restrict__ ms, float* __restrict__ part) {
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t bc = u / kblocks;
-    const int k = (int)(u - bc * kblocks) * 256 + threadIdx.x;
+    const int k = ((int)(u - bc * kblocks) * 256 + threadIdx.x) * V;
     if (k >= K) continue;
     const int64_t b = bc / chunks, c = bc - b * chunks;
     const int64_t i0 = c * kBalanceRows, i1 = i0 + kBalanceRows < N ? i0 + kBalanceRows : N;
-    double sum = 0.0;
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = 0.f;
+#pragma unroll 4
     for (int64_t i = i0; i < i1; ++i) {
       const float2 z = ms[b * N + i];
-      if (z.y == 0.f) continue;
-      sum += (double)(exp_diff(T::to_f32(logits[(b * N + i) * K + k]), z.x) * z.y);
+      Pack<T, V> p;
+      float x[V];
+      p.load_nt(logits + (b * N + i) * K + k);
+      p.unpack(x);
+      // (a row that leaves nothing may hold anything)
+#pragma unroll
+      for (int v = 0; v < V; ++v) sum[v] += z.y == 0.f ? 0.f : exp_diff(x[v], z.x) * z.y;
     }
-    part[bc * K + k] = (float)sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[bc * K + k + v] = sum[v];
   }
 }
 
@@ -545,31 +591,42 @@ __global__ __launch_bounds__(256) void balance_count_kernel(const int32_t* __res
   }
 }
 
-template <class T>
+template <class T, int V>
 __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T::raw* __restrict__ logits, int64_t n,
                                                                 uint32_t N, int K, const float* __restrict__ lse,
                                                                 const float* __restrict__ coef,
                                                                 const float* __restrict__ dloss,
                                                                 typename T::raw* __restrict__ dlogits) {
-  const int lane = lane_id();
-  for (int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); i < n; i += (int64_t)gridDim.x * 4) {
+  __shared__ float2 tmp[4];
+  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
     const int64_t b = (uint32_t)i / N;
     const float z = lse[i];
-    const bool none = z == INFINITY || z == -INFINITY;
+    const bool none = z == INFINITY || z == -INFINITY;  // uniform over the workgroup
     const float* cf = coef + b * K;
-    float s = 0.f, d = 0.f;
-    if (!none)
-      for (int k = lane; k < K; k += 64) {
-        const float e = exp_diff(T::to_f32(logits[i * K + k]), z);
-        s += e;
-        d = fmaf(e, cf[k], d);
-      }
-    s = team_sum<64>(s);
-    d = team_sum<64>(d);
-    const float inv = 1.f / s, mean = d * inv, scale = dloss[b] * inv;
-    for (int k = lane; k < K; k += 64)
-      dlogits[i * K + k] =
-          round_to<T>(none ? 0.f : scale * exp_diff(T::to_f32(logits[i * K + k]), z) * (cf[k] - mean));
+    float mean = 0.f, scale = 0.f;
+    if (!none) {
+      float s = 0.f, d = 0.f;
+      over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float e = exp_diff(x[v], z);
+          s += e;
+          d = fmaf(e, cf[k + v], d);
+        }
+      });
+      const float2 t = block_sum2(s, d, tmp);
+      const float inv = 1.f / t.x;
+      mean = t.y * inv, scale = dloss[b] * inv;
+    }
+    // the row again (from the cache) for the gradient
+    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] = none ? 0.f : scale * exp_diff(x[v], z) * (cf[k + v] - mean);
+      Pack<T, V> q;
+      q.pack(o);
+      q.store_nt(dlogits + i * K + k);
+    });
   }
 }
 
@@ -650,8 +707,33 @@ hipError_t with_team(int K, F&& f) {
   if (K <= 256) return f(Team<V, A, 32, 1>{});
   if (K <= 512) return f(Team<V, A, 64, 1>{});
   if (K <= 1024) return f(Team<V, C, 64, 1>{});
+  // (a barrier a row: the fewer waves share one, the more rows a CU works on)
+  if (K <= 2048) return f(Team<V, A, 64, 4>{});
   if (K <= 4096) return f(Team<V, C, 64, 4>{});
+  if (K <= 8192) return f(Team<V, C, 64, 8>{});
   return f(Team<V, C, 64, 16>{});
+}
+
+template <class T, int V>
+hipError_t wide_forward(const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
+                        const uint8_t* valid, float* lse, const BalanceOut& out, const BalanceBuffers& buf,
+                        hipStream_t s) {
+  const int64_t n = N * B;
+  const auto* x = static_cast<const typename T::raw*>(logits);
+  const int64_t entries = (int64_t)B * K;
+  balance_zero_kernel<<<dim3((unsigned)capped((entries + 255) / 256)), dim3(256), 0, s>>>(out.counts, entries,
+                                                                                           buf.vpart, B);
+  if (n) {
+    balance_lse_kernel<T, V><<<dim3((unsigned)capped(n)), dim3(256), 0, s>>>(x, n, K, valid, lse, buf.ms);
+    balance_count_kernel<<<dim3((unsigned)capped((n + 255) / 256)), dim3(256), 0, s>>>(
+        labels, n, (uint32_t)N, (uint32_t)K, S, valid, out.counts, buf.vpart);
+  }
+  const int64_t chunks = balance_wide_chunks(N);
+  const int kblocks = (K + 256 * V - 1) / (256 * V);
+  const int64_t units = B * chunks * kblocks;
+  balance_cols_kernel<T, V><<<dim3((unsigned)capped(units)), dim3(256), 0, s>>>(x, N, K, chunks, kblocks, units,
+                                                                                 buf.ms, buf.part);
+  return join(JoinIn{buf.part, chunks, out.counts, 1, buf.vpart, 1}, K, S, B, out, buf.terms, s);
 }
 
 template <class T>
@@ -663,24 +745,11 @@ hipError_t balance_t(const void* logits, int64_t N, int K, int B, const int32_t*
       using P = decltype(team);
       return rows_forward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
     };
-    return vec_width(K, logits, T::SZ, logits, T::SZ) >= VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
   }
-  const int64_t n = N * B;
-  const auto* x = static_cast<const typename T::raw*>(logits);
-  const int64_t entries = (int64_t)B * K;
-  balance_zero_kernel<<<dim3((unsigned)capped((entries + 255) / 256)), dim3(256), 0, s>>>(out.counts, entries,
-                                                                                           buf.vpart, B);
-  if (n) {
-    balance_lse_kernel<T><<<dim3((unsigned)capped((n + 3) / 4)), dim3(256), 0, s>>>(x, n, K, valid, lse, buf.ms);
-    balance_count_kernel<<<dim3((unsigned)capped((n + 255) / 256)), dim3(256), 0, s>>>(
-        labels, n, (uint32_t)N, (uint32_t)K, S, valid, out.counts, buf.vpart);
-  }
-  const int64_t chunks = balance_wide_chunks(N);
-  const int kblocks = (K + 255) / 256;
-  const int64_t units = B * chunks * kblocks;
-  balance_cols_kernel<T><<<dim3((unsigned)capped(units)), dim3(256), 0, s>>>(x, N, K, chunks, kblocks, units, buf.ms,
-                                                                              buf.part);
-  return join(JoinIn{buf.part, chunks, out.counts, 1, buf.vpart, 1}, K, S, B, out, buf.terms, s);
+  return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC
+             ? wide_forward<T, VEC>(logits, N, K, B, labels, S, valid, lse, out, buf, s)
+             : wide_forward<T, 1>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
 }
 
 template <class T>
@@ -692,12 +761,16 @@ hipError_t balance_grad_t(const void* logits, int64_t N, int K, int B, const flo
       using P = decltype(team);
       return rows_backward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, lse, coef, dloss, dlogits, s);
     };
-    return vec_width(K, logits, T::SZ, dlogits, T::SZ) >= VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
   }
   const int64_t n = N * B;
-  balance_grad_wide_kernel<T><<<dim3((unsigned)capped((n + 3) / 4)), dim3(256), 0, s>>>(
-      static_cast<const typename T::raw*>(logits), n, (uint32_t)N, K, lse, coef, dloss,
-      static_cast<typename T::raw*>(dlogits));
+  const dim3 grid((unsigned)capped(n));
+  const auto* x = static_cast<const typename T::raw*>(logits);
+  auto* dx = static_cast<typename T::raw*>(dlogits);
+  if (vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC)
+    balance_grad_wide_kernel<T, VEC><<<grid, dim3(256), 0, s>>>(x, n, (uint32_t)N, K, lse, coef, dloss, dx);
+  else
+    balance_grad_wide_kernel<T, 1><<<grid, dim3(256), 0, s>>>(x, n, (uint32_t)N, K, lse, coef, dloss, dx);
   return hipGetLastError();
 }
 

@@ -697,7 +697,7 @@ static hipError_t with_type(int dt, F&& f) {
 
 hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids, int64_t N, int K, int D, int B,
                         float scale, void* out, hipStream_t s) {
-  const int w = vec_width(D, table, dtype_size(tdt), out, dtype_size(odt));
+  const int w = vec_width(D, 16 / dtype_size(odt), table, dtype_size(tdt), out, dtype_size(odt));
   return with_type(tdt, [&](auto ti) {
     return with_type(odt, [&](auto to) {
       using TI = decltype(ti);
@@ -709,7 +709,7 @@ hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids,
 
 hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* ids, int64_t N, int K, int D, int B,
                              float scale, bool acc, void* grad, GradBuffers& buf, hipStream_t s) {
-  const int w = vec_width(D, dout, dtype_size(idt), grad, dtype_size(gdt));
+  const int w = vec_width(D, 16 / dtype_size(idt), dout, dtype_size(idt), grad, dtype_size(gdt));
   return with_type(idt, [&](auto ti) {
     return with_type(gdt, [&](auto to) {
       using TI = decltype(ti);

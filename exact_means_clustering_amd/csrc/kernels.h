@@ -269,9 +269,9 @@ hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* 
 constexpr int kBalanceMaxK = 16384;   // longest rows kept in registers
 constexpr int kBalanceJoinCols = 32;  // fewest columns per workgroup that joins chunk sums
 constexpr int kBalanceFold = 64;      // rows of a block of a column sum, and the most blocks of one
-constexpr int kBalanceRows = 256;     // rows per column-sum chunk of longer rows
+constexpr int kBalanceRows = 64;      // rows per column-sum chunk of longer rows
 // Rows a workgroup takes at a time: 4 waves of 64 / LPR rows, LPR lanes of 8
-// elements a row, up to 512; then a wave (16 elements a lane), 4 or 16 waves a row.
+// elements a row, up to 512; then a wave (16 elements a lane), 4, 8 or 16 waves a row.
 constexpr int balance_step(int K) {
   int lpr = 1;
   while (lpr < 64 && lpr * 8 < K) lpr *= 2;
@@ -283,7 +283,7 @@ struct BalanceSplit {
   int64_t chunks;
 };
 inline BalanceSplit balance_split(int64_t N, int B, int K) {
-  const int64_t blocks = K > 4096 ? 512 : 2048;  // 1,024 or 256 threads each
+  const int64_t blocks = K > 8192 ? 512 : K > 4096 ? 1024 : 2048;  // of 1,024, 512 and 256 threads
   const int64_t want = blocks / B > 1 ? blocks / B : 1;
   const int64_t all = (N + balance_step(K) - 1) / balance_step(K);
   int64_t steps = (all + want - 1) / want;

@@ -5,14 +5,15 @@ Tolerances count roundings (u = 2^-24, half a step of fp32; half a step of the o
   embed_grad    a sum of m values in any order is off by at most (m - 1) u times the sum of their magnitudes; the scale
                 and the addition to the old value add u each, the output's type half a step (and, for fp16, half of its
                 smallest step 2^-24).
-  balance       with R the largest |logit - maximum| that still leaves a probability (exp of less than -104 is 0 in fp32),
-                an exponential is off by (R + 4) u relative (the difference's rounding, its scaling, exp itself), a row's sum by
-                another (K / 64 + 24) u (lanes add at most K / 64 + 16 values one after another, then 6 levels of pairs), a
-                column's by ROWS u more (blocks of 64 rows added one after another), by one u a block (4 at most here) and by 6
-                over a wave's lanes, which the 24 of the row's sum and the 8 leave room for (the row's own sums of at most 16
-                values and 6 levels take 22 of them only where a lane has 16 values, and then a wave holds one row).
-  balance_grad  p is off by an exponential and a row's sum as above; the mean of coef under p by that and a sum's depth; the
-                difference, the products and the output's type add 4 u and half a step.
+  balance       with R the largest |logit - maximum| that still leaves a probability (exp of less than -104 is 0 in
+                fp32), an exponential is off by (R + 4) u relative (the difference's rounding, its scaling, exp itself), a
+                row's sum by another (K / 64 + 24) u (lanes add at most K / 64 + 16 values one after another, then 6 levels
+                of pairs), a column's by ROWS u more (blocks of 64 rows added one after another), by one u a block (4 at
+                most here) and by 6 over a wave's lanes, which the 24 of the row's sum and the 8 leave room for (the row's
+                own sums of at most 16 values and 6 levels take 22 of them only where a lane has 16 values, and then a
+                wave holds one row).
+  balance_grad  p is off by an exponential and a row's sum as above; the mean of coef under p by that and a sum's depth;
+                the difference, the products and the output's type add 4 u and half a step.
 """
 
 import math
@@ -94,8 +95,9 @@ def same(a, b):
 
 @pytest.mark.parametrize("to", TYPES)
 @pytest.mark.parametrize("of", TYPES)
-@pytest.mark.parametrize("B, N, K, D", [(1, 1, 1, 1), (1, 5, 3, 80), (1, 1000, 77, 128), (3, 129, 50, 12), (2, 33, 700, 1027),
-                                        (1, 7, 11, 8200), (1, 3, 5, 1026), (5, 1, 9, 16), (1, 4097, 2, 4)])
+@pytest.mark.parametrize("B, N, K, D", [(1, 1, 1, 1), (1, 5, 3, 80), (1, 1000, 77, 128), (3, 129, 50, 12),
+                                        (2, 33, 700, 1027), (1, 7, 11, 8200), (1, 3, 5, 1026), (5, 1, 9, 16),
+                                        (1, 4097, 2, 4)])
 def test_embed(km, of, to, B, N, K, D):
     table = torch.randn(B, K, D, generator=gen(D)).to(of)
     ids = some_ids(B, N, K, N)
@@ -336,7 +338,8 @@ def check_balance(got, logits, labels, valid):
 
 BALANCE_SHAPES = [(1, 1, 1, 1), (1, 32, 8, 2), (1, 1000, 7, 1), (3, 257, 64, 4), (2, 300, 128, 8), (1, 129, 100, 3),
                   (1, 70, 1000, 1), (2, 65, 1024, 2), (1, 40, 3001, 5), (1, 9, 20000, 1), (1, 5, 70000, 2), (4, 1, 16, 6),
-                  (70, 3, 12, 2), (1, 5000, 256, 2), (1, 3, 2, 9), (2, 900, 33, 2), (1, 515, 520, 1), (1, 66, 4104, 1)]
+                  (70, 3, 12, 2), (1, 5000, 256, 2), (1, 3, 2, 9), (2, 900, 33, 2), (1, 515, 520, 1), (1, 66, 4104, 1),
+                  (1, 300, 2048, 2), (1, 33, 8191, 3), (2, 70, 8200, 1), (1, 37, 12345, 2), (1, 21, 16384, 1)]
 
 
 def balance_case(B, N, K, S, dtype, seed, spread=2.0):
