@@ -33,8 +33,22 @@ constexpr int kFold = kBalanceFold;
 constexpr int kAheadF = 2, kAheadB = 4;
 constexpr int kEarly = 2;  // labels a thread reads ahead of the rows
 
+// exp(x - shift).  The product with log2(e) rounds to |x - shift| 2^-24 of the
+// result, which is lost in a 16-bit gradient; for fp32 logits the product's
+// rounding and log2(e)'s own are put back to first order.
+template <class T>
 __device__ __forceinline__ float exp_diff(float x, float shift) {
-  return __builtin_amdgcn_exp2f((x - shift) * kLog2e);
+  const float t = x - shift;
+  if constexpr (T::SZ == 4) {
+    constexpr float kLog2eLow = 1.925963033500757e-8f, kLn2 = 0.6931471805599453f;
+    const float c = t < -150.f ? -150.f : t;  // exp is 0 there; NaN stays
+    const float y = c * kLog2e;
+    const float r = fmaf(c, kLog2eLow, fmaf(c, kLog2e, -y));
+    const float e = __builtin_amdgcn_exp2f(y);
+    return fmaf(e, r * kLn2, e);
+  } else {
+    return __builtin_amdgcn_exp2f(t * kLog2e);
+  }
 }
 
 // The value of the lane paired with this one: neighbours, pairs, then mirrored
@@ -228,7 +242,7 @@ void balance_rows_kernel(
     float s = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      x[e] = exp_diff(x[e], shift);
+      x[e] = exp_diff<T>(x[e], shift);
       s += x[e];
     }
     s = team_sum<LPR>(s);
@@ -245,9 +259,9 @@ void balance_rows_kernel(
       for (int q = 0; q < W; ++q) {
         const float2 o = xch[t & 1][q];
         // a wave's sum is relative to its own shift (0 if it had none)
-        ss += o.y * exp_diff(o.x == -INFINITY ? (o.y == 0.f ? sh : 0.f) : o.x, sh);
+        ss += o.y * exp_diff<T>(o.x == -INFINITY ? (o.y == 0.f ? sh : 0.f) : o.x, sh);
       }
-      scale = exp_diff(m == -INFINITY ? sh : m, sh);
+      scale = exp_diff<T>(m == -INFINITY ? sh : m, sh);
       m = mm, s = ss;
     }
     if (g == 0 && i < i1) {
@@ -430,7 +444,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
     float s = 0.f, d = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      x[e] = exp_diff(x[e], z);
+      x[e] = exp_diff<T>(x[e], z);
       s += x[e];
       d = fmaf(x[e], cf[e], d);
     }
@@ -513,12 +527,12 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
 #pragma unroll
       for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
       if (top > m) {  // the sum moves to the new maximum (from nothing, if that was -inf)
-        s *= exp_diff(m, top);
+        s *= exp_diff<T>(m, top);
         m = top;
       }
       const float shift = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s += exp_diff(x[v], shift);
+      for (int v = 0; v < V; ++v) s += exp_diff<T>(x[v], shift);
     });
     // the workgroup's maximum, then the sums relative to it
     const float wm = team_max<64>(m);
@@ -528,7 +542,7 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
     const float top = fmaxf(fmaxf(tmp[0].x, tmp[1].x), fmaxf(tmp[2].x, tmp[3].x));
     const float shift = top == -INFINITY ? 0.f : top;
     // a thread without a maximum holds 0 (or NaN), relative to 0
-    const float sum = block_sum2(m == -INFINITY ? s : s * exp_diff(m, shift), 0.f, tmp).x;
+    const float sum = block_sum2(m == -INFINITY ? s : s * exp_diff<T>(m, shift), 0.f, tmp).x;
     if (threadIdx.x == 0) {
       lse[i] = sum == 0.f ? -INFINITY : top + logf(sum);
       ms[i] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(shift, 1.f / sum);
@@ -560,7 +574,7 @@ __global__ __launch_bounds__(256) void balance_cols_kernel(const typename T::raw
       p.unpack(x);
       // (a row that leaves nothing may hold anything)
 #pragma unroll
-      for (int v = 0; v < V; ++v) sum[v] += z.y == 0.f ? 0.f : exp_diff(x[v], z.x) * z.y;
+      for (int v = 0; v < V; ++v) sum[v] += z.y == 0.f ? 0.f : exp_diff<T>(x[v], z.x) * z.y;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) part[bc * K + k + v] = sum[v];
@@ -609,7 +623,7 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
       over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          const float e = exp_diff(x[v], z);
+          const float e = exp_diff<T>(x[v], z);
           s += e;
           d = fmaf(e, cf[k + v], d);
         }
@@ -622,7 +636,7 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
     over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
       float o[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v] = none ? 0.f : scale * exp_diff(x[v], z) * (cf[k + v] - mean);
+      for (int v = 0; v < V; ++v) o[v] = none ? 0.f : scale * exp_diff<T>(x[v], z) * (cf[k + v] - mean);
       Pack<T, V> q;
       q.pack(o);
       q.store_nt(dlogits + i * K + k);
