@@ -25,7 +25,7 @@ namespace fkm {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kFold = kBalanceFold;
 // Rows in flight per team, forward and backward (1,048,576 x 1,024 bf16:
 // forward 463 us with 1, 443 with 2, 444 with 4; backward with the caches'
@@ -40,7 +40,7 @@ template <class T>
 __device__ __forceinline__ float exp_diff(float x, float shift) {
   const float t = x - shift;
   if constexpr (T::SZ == 4) {
-    constexpr float kLog2eLow = 1.925963033500757e-8f, kLn2 = 0.6931471805599453f;
+    constexpr float kLog2eLow = 1.925963033500757e-8f;
     const float c = t < -150.f ? -150.f : t;  // exp is 0 there; NaN stays
     const float y = c * kLog2e;
     const float r = fmaf(c, kLog2eLow, fmaf(c, kLog2e, -y));
@@ -75,6 +75,18 @@ __device__ __forceinline__ float team_op(float v, Op op) {
     v = op(__uint_as_float(p[0]), __uint_as_float(p[1]));
   }
   return v;
+}
+// Maximum of E values, two at a time (fmaxf would first canonicalise each value
+// unpacked from a word: one instruction more per value).  A NaN may win or lose:
+// the row's exponentials are NaN either way.
+template <int E>
+__device__ __forceinline__ float max_of(const float (&x)[E]) {
+  static_assert(E % 2 == 0, "pairs");
+  float m = x[0];
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(x[0]), "v"(x[1]));
+#pragma unroll
+  for (int e = 2; e < E; e += 2) asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(m), "v"(x[e]), "v"(x[e + 1]));
+  return m;
 }
 template <int LPR>
 __device__ __forceinline__ float team_max(float v) {
@@ -232,10 +244,7 @@ void balance_rows_kernel(
     float x[E];
     ring[h].values(x);
     refill(h, t + kAheadF);
-    float m = x[0];
-#pragma unroll
-    for (int e = 1; e < E; ++e) m = fmaxf(m, x[e]);
-    m = team_max<LPR>(m);
+    float m = team_max<LPR>(max_of(x));
     // a wave (or team) without a finite maximum: shift by 0, so that -inf
     // gives 0 (and NaN and +inf stay what they are)
     float shift = m == -INFINITY ? 0.f : m;
@@ -265,11 +274,11 @@ void balance_rows_kernel(
       m = mm, s = ss;
     }
     if (g == 0 && i < i1) {
-      lse[base + i] = !live ? INFINITY : s == 0.f ? -INFINITY : m + logf(s);
+      lse[base + i] = !live ? INFINITY : s == 0.f ? -INFINITY : fmaf(__builtin_amdgcn_logf(s), kLn2, m);
       mine += live;
     }
     // a row that leaves no probability has exponentials of 0 only
-    const float q = s != 0.f ? scale / s : 0.f;
+    const float q = s != 0.f ? scale * __builtin_amdgcn_rcpf(s) : 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(x[e], q, acc[e]);
     if (++fold == kFold) {
@@ -457,7 +466,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
 #pragma unroll
       for (int q = 0; q < W; ++q) s += xch[t & 1][q].x, d += xch[t & 1][q].y;
     }
-    const float inv = 1.f / s;
+    const float inv = __builtin_amdgcn_rcpf(s);
     const float mean = d * inv, scale = dl * inv;
     const bool live = is_live(z);
     if (i < i1) {
