@@ -143,7 +143,9 @@ __device__ __forceinline__ void zero_entries(typename TO::raw* __restrict__ grad
   }
 }
 
-// Few rows (n <= kGradDirect): no sort.  A wave takes row i and a slab of 64
+// Few rows (n <= kGradDirect, 256): no sort (256 rows of 1,024 bf16 into
+// 32,000 fp32: 29 us either way, bound by the zeros; accumulated, without
+// zeros: 8.3 us so, 16.3 us sorted by one workgroup).  A wave takes row i and a slab of 64
 // vectors; if no earlier row has its id, it adds every row of that id in
 // order.  Further workgroups zero the entries that no row names, each
 // looking for its own range of entries among the ids.
@@ -314,6 +316,10 @@ __device__ __forceinline__ void join_units(const uint2* __restrict__ kv, int64_t
 // before any reaches memory.  Rows whose word carries the mark leave nothing.
 // The first workgroups zero the entries no row has (unless those keep what
 // they hold), finding each by a binary search whose waits the sums fill.
+// Bound by the rows' bytes: 2^23 rows of 256 bytes in 0.41 ms, 5.2 TB/s (the
+// whole gradient into 65,536 x 128 fp32 0.543 ms, of it 0.104 the sort).  With
+// 4 loads in flight 0.557 ms, with loads that stay in the caches 0.580 ms;
+// units of at most 128 or 512 rows 0.545 and 0.550 ms.
 constexpr int kAhead = 8;
 template <int LPR>
 constexpr int kGroups = 256 / LPR;
@@ -497,7 +503,10 @@ int64_t sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, 
   return ublocks;
 }
 
-// Up to kSortOne rows: one workgroup argsorts the ids in LDS (stable radix
+// Up to kSortOne rows, where a word holds key and row: 16,384 rows of 2,048
+// bf16 into 32,000 fp32 in 73 us against 106 us with the sort's own launches
+// and zeros by binary search; 4,099 rows accumulated into 131,072 in 36.5
+// against 52 us.  One workgroup argsorts the ids in LDS (stable radix
 // passes of 8 bits over 32-bit words: key, out-of-range bit, row), and the
 // other workgroups of the launch meanwhile zero the gradient.  Ranks as in
 // the sort of many rows: digit matches inside a wave, a counter per wave and
