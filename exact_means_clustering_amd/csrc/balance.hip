@@ -152,10 +152,16 @@ __device__ __forceinline__ double block_sum_f64(double v, double* tmp) {
 // ---------------------------------------------------------------------------
 // rows in registers
 // ---------------------------------------------------------------------------
-// T type, V elements per load, NV loads per lane, LPR lanes per row (W = 1)
-// or W whole waves per row (LPR = 64).
-template <class T, int V, int NV, int LPR, int W>
+// T type, V elements (16 bytes) per load, NV loads per lane, LPR lanes per row
+// (W = 1) or W whole waves per row (LPR = 64).  LOOSE: rows that are no multiple
+// of 16 bytes or start anywhere: loads at element alignment, the last one of a
+// row ending with it, its elements that the load before has too left out
+// (65,536 x 5,001 bf16 forward 295 us, 1,048,576 x 100 90 us; with loads of
+// single elements 425 and 95 us; with single elements at a row's end only, whose
+// branches break the ring, 304 and 162 us).
+template <class T, int NV, int LPR, int W, bool LOOSE>
 struct Rows {
+  static constexpr int V = 16 / T::SZ;
   static constexpr int E = V * NV;
   static constexpr int MAXK = LPR * W * E;
   static constexpr int BLOCK = W > 4 ? 64 * W : 256;
@@ -164,24 +170,56 @@ struct Rows {
   static constexpr int SL = 64 / LPR;           // rows per wave and step
   static constexpr int STEP = TEAMS * SL;       // rows per workgroup and step
   static_assert(W == 1 || (LPR == 64 && TEAMS == 1), "a wide team is the workgroup");
+  // The columns of lane g of a team: load j takes V from first[j], of which
+  // those from skip[j] to before end are the lane's own.
+  struct Cols {
+    int first[NV], skip[NV], end, K;
+    __device__ __forceinline__ Cols(int g, int K_) : K(K_) {
+      end = LOOSE && K < V ? K : V;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * LPR * W + g) * V;
+        first[j] = c, skip[j] = c < K ? 0 : V;
+        if (LOOSE && c + V > K && K >= V) {
+          first[j] = K - V;
+          skip[j] = c + V - K < V ? c + V - K : V;
+        }
+      }
+    }
+    // column of the lane's element e, or -1
+    __device__ __forceinline__ int at(int e) const {
+      const int v = e % V;
+      return v >= skip[e / V] && v < end ? first[e / V] + v : -1;
+    }
+  };
   Pack<T, V> p[NV];
-  // the row's words of lane g of the team; -inf past it and for a row that is
-  // not live
-  __device__ __forceinline__ void load(const typename T::raw* row, int g, int K, bool live) {
+  // the row's words; -inf for columns that are not the lane's (where a whole
+  // load has none) and for a row that is not live
+  __device__ __forceinline__ void load(const typename T::raw* row, const Cols& c, bool live) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * LPR * W + g) * V;
-            if (live && c < K) p[j].load_nt(row + c);
-      else p[j].fill_neg_inf();
+      if constexpr (LOOSE) {
+        if (c.end == V) {  // uniform over the launch
+          if (live) p[j].load_loose(row + c.first[j]);
+          else p[j].fill_neg_inf();
+        } else {
+          p[j].fill_neg_inf();
+          if (live && c.skip[j] == 0) p[j].load_head(row + c.first[j], c.K);
+        }
+      } else {
+        if (live && c.skip[j] == 0) p[j].load_nt(row + c.first[j]);
+        else p[j].fill_neg_inf();
+      }
     }
   }
-  __device__ __forceinline__ void values(float (&x)[E]) const {
+  // values as fp32, -inf for columns that are not the lane's
+  __device__ __forceinline__ void values(float (&x)[E], const Cols& c) const {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       float f[V];
       p[j].unpack(f);
 #pragma unroll
-      for (int v = 0; v < V; ++v) x[j * V + v] = f[v];
+      for (int v = 0; v < V; ++v) x[j * V + v] = LOOSE && v < c.skip[j] ? -INFINITY : f[v];
     }
   }
 };
@@ -190,14 +228,15 @@ struct Rows {
 // GB in 0.41 ms, 5.2 TB/s) and by the vector instructions, about 9 a value,
 // where they are short (8,388,608 x 8: 68 us, 3.5 TB/s).  Waves of 16 values a
 // lane: five per SIMD instead of four, 412 against 432 us.
-template <class T, int V, int NV, int LPR, int W>
-__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK), (W == 1 && V * NV == 16 && V > 1 ? 5 : 1))
+template <class T, int NV, int LPR, int W, bool LOOSE>
+__global__ __launch_bounds__((Rows<T, NV, LPR, W, LOOSE>::BLOCK),
+                             (W == 1 && Rows<T, NV, LPR, W, LOOSE>::E == 16 && !LOOSE ? 5 : 1))
 void balance_rows_kernel(
     const typename T::raw* __restrict__ logits, int64_t N, int K, const int32_t* __restrict__ labels, int S,
     const uint8_t* __restrict__ valid, float* __restrict__ lse, int64_t chunks, int steps, float* __restrict__ part,
     int32_t* __restrict__ cpart, int32_t* __restrict__ vpart, BalanceOut out) {
-  using R = Rows<T, V, NV, LPR, W>;
-  constexpr int E = R::E, WAVES = R::WAVES;
+  using R = Rows<T, NV, LPR, W, LOOSE>;
+  constexpr int V = R::V, E = R::E, WAVES = R::WAVES;
   __shared__ int hist[R::MAXK];
   __shared__ float col[W == 1 ? WAVES * R::MAXK : 1];
   __shared__ float2 xch[2][W == 1 ? 1 : W];
@@ -205,6 +244,7 @@ void balance_rows_kernel(
   __shared__ int nval;
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int g = W == 1 ? lane % LPR : tid;          // lane of the team
+  const typename R::Cols cols(g, K);
   const int slot = W == 1 ? w * R::SL + lane / LPR : 0;
   const int64_t b = blockIdx.x / chunks, c = blockIdx.x - b * chunks;
   const int64_t i0 = c * steps * R::STEP;
@@ -225,7 +265,7 @@ void balance_rows_kernel(
   auto refill = [&](int h, int t) {
     const int64_t i = i0 + (int64_t)t * R::STEP + slot;
     live_at[h] = t < steps && is_live(i);
-    ring[h].load(logits + (base + i) * K, g, K, live_at[h]);
+    ring[h].load(logits + (base + i) * K, cols, live_at[h]);
   };
 #pragma unroll
   for (int h = 0; h < kAheadF; ++h) refill(h, h);
@@ -244,7 +284,7 @@ void balance_rows_kernel(
     const int64_t i = i0 + (int64_t)t * R::STEP + slot;
     const bool live = live_at[h];
     float x[E];
-    ring[h].values(x);
+    ring[h].values(x, cols);
     refill(h, t + kAheadF);
     float m = team_max<LPR>(max_of(x));
     // a wave (or team) without a finite maximum: shift by 0, so that -inf
@@ -312,8 +352,8 @@ void balance_rows_kernel(
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float total = slot_sum<LPR>(sum[e]);
-      const int k = ((e / V) * LPR + g) * V + e % V;
-      if (lane < LPR && k < K) col[w * R::MAXK + k] = total;
+      const int k = cols.at(e);
+      if (lane < LPR && k >= 0) col[w * R::MAXK + k] = total;
     }
   }
   __syncthreads();
@@ -338,8 +378,8 @@ void balance_rows_kernel(
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const int k = ((e / V) * R::BLOCK + g) * V + e % V;
-      if (k >= K) continue;
+      const int k = cols.at(e);
+      if (k < 0) continue;
       if (chunks == 1) {
         term += balance_entry(out, b * K + k, K, S, T_, (double)sum[e], hist[k]);
       } else {
@@ -415,16 +455,17 @@ __global__ __launch_bounds__(256) void balance_loss_kernel(const double* __restr
 
 // Bound by the bytes read and written: 1,048,576 x 1,024 bf16 4.3 GB in 0.81 ms,
 // 5.3 TB/s.
-template <class T, int V, int NV, int LPR, int W>
-__global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_rows_kernel(
+template <class T, int NV, int LPR, int W, bool LOOSE>
+__global__ __launch_bounds__((Rows<T, NV, LPR, W, LOOSE>::BLOCK)) void balance_grad_rows_kernel(
     const typename T::raw* __restrict__ logits, int64_t N, int K, const float* __restrict__ lse,
     const float* __restrict__ coef, const float* __restrict__ dloss, int64_t chunks, int steps,
     typename T::raw* __restrict__ dlogits) {
-  using R = Rows<T, V, NV, LPR, W>;
-  constexpr int E = R::E;
+  using R = Rows<T, NV, LPR, W, LOOSE>;
+  constexpr int V = R::V, E = R::E;
   __shared__ float2 xch[2][W == 1 ? 1 : W];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int g = W == 1 ? lane % LPR : tid;
+  const typename R::Cols cols(g, K);
   const int slot = W == 1 ? w * R::SL + lane / LPR : 0;
   const int64_t b = blockIdx.x / chunks, c = blockIdx.x - b * chunks;
   const int64_t i0 = c * steps * R::STEP;
@@ -434,8 +475,8 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
   float cf[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int k = ((e / V) * LPR * W + g) * V + e % V;
-    cf[e] = k < K ? coef[b * K + k] : 0.f;
+    const int k = cols.at(e);
+    cf[e] = k >= 0 ? coef[b * K + k] : 0.f;
   }
   auto z_of = [&](int64_t i) { return i < i1 ? lse[base + i] : INFINITY; };
   auto is_live = [](float z) { return z != INFINITY && z != -INFINITY; };
@@ -444,7 +485,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
   auto refill = [&](int h, int t) {
     const int64_t i = i0 + (int64_t)t * R::STEP + slot;
     z_at[h] = t < steps ? z_of(i) : INFINITY;
-    ring[h].load(logits + (base + i) * K, g, K, is_live(z_at[h]));
+    ring[h].load(logits + (base + i) * K, cols, is_live(z_at[h]));
   };
 #pragma unroll
   for (int h = 0; h < kAheadB; ++h) refill(h, h);
@@ -452,7 +493,7 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
     const int64_t i = i0 + (int64_t)t * R::STEP + slot;
     const float z = z_at[h];
     float x[E];
-    ring[h].values(x);
+    ring[h].values(x, cols);
     refill(h, t + kAheadB);
     float s = 0.f, d = 0.f;
 #pragma unroll
@@ -476,14 +517,19 @@ __global__ __launch_bounds__((Rows<T, V, NV, LPR, W>::BLOCK)) void balance_grad_
     if (i < i1) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int k = (j * LPR * W + g) * V;
-        if (k >= K) continue;
+        if (cols.skip[j] == V) continue;
         float o[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = live ? scale * x[j * V + v] * (cf[j * V + v] - mean) : 0.f;
         Pack<T, V> q;
         q.pack(o);
-        q.store_nt(dlogits + (base + i) * K + k);
+        typename T::raw* at = dlogits + (base + i) * K + cols.first[j];
+        if constexpr (LOOSE) {
+          if (cols.skip[j] == 0 && cols.end == V) q.store_loose(at);
+          else q.store_range(at, cols.skip[j], cols.end);
+        } else {
+          q.store_nt(at);
+        }
       }
     }
   };
@@ -694,53 +740,54 @@ hipError_t join(const JoinIn& in, int K, int S, int B, const BalanceOut& out, do
   return hipGetLastError();
 }
 
-template <class T, int V, int NV, int LPR, int W>
+template <class T, int NV, int LPR, int W, bool LOOSE>
 hipError_t rows_forward(const void* logits, int64_t N, int K, int B, const int32_t* labels, int S,
                         const uint8_t* valid, float* lse, const BalanceOut& out, const BalanceBuffers& buf,
                         hipStream_t s) {
-  using R = Rows<T, V, NV, LPR, W>;
+  using R = Rows<T, NV, LPR, W, LOOSE>;
   static_assert(R::STEP == balance_step(R::MAXK), "the workspace's chunks are these");
   const BalanceSplit sp = balance_split(N, B, K);
-  balance_rows_kernel<T, V, NV, LPR, W><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
+  balance_rows_kernel<T, NV, LPR, W, LOOSE><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
       static_cast<const typename T::raw*>(logits), N, K, labels, S, valid, lse, sp.chunks, sp.steps, buf.part,
       buf.cpart, buf.vpart, out);
   if (sp.chunks == 1) return hipGetLastError();
   return join(JoinIn{buf.part, sp.chunks, buf.cpart, sp.chunks, buf.vpart, sp.chunks}, K, S, B, out, buf.terms, s);
 }
 
-template <class T, int V, int NV, int LPR, int W>
+template <class T, int NV, int LPR, int W, bool LOOSE>
 hipError_t rows_backward(const void* logits, int64_t N, int K, int B, const float* lse, const float* coef,
                          const float* dloss, void* dlogits, hipStream_t s) {
-  using R = Rows<T, V, NV, LPR, W>;
+  using R = Rows<T, NV, LPR, W, LOOSE>;
   static_assert(R::STEP == balance_step(R::MAXK), "the workspace's chunks are these");
   const BalanceSplit sp = balance_split(N, B, K);
-  balance_grad_rows_kernel<T, V, NV, LPR, W><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
+  balance_grad_rows_kernel<T, NV, LPR, W, LOOSE><<<dim3((unsigned)(B * sp.chunks)), dim3(R::BLOCK), 0, s>>>(
       static_cast<const typename T::raw*>(logits), N, K, lse, coef, dloss, sp.chunks, sp.steps,
       static_cast<typename T::raw*>(dlogits));
   return hipGetLastError();
 }
 
-// f(Team) with the smallest team that holds a row of K elements.
-template <int V_, int NV_, int LPR_, int W_>
+// f(Team) with the smallest team that holds a row of K elements, A loads of
+// 16 bytes making 8 elements.
+template <int NV_, int LPR_, int W_, bool LOOSE_>
 struct Team {
-  static constexpr int V = V_, NV = NV_, LPR = LPR_, W = W_;
+  static constexpr int NV = NV_, LPR = LPR_, W = W_;
+  static constexpr bool LOOSE = LOOSE_;
 };
-template <int V, class F>
+template <int A, bool LOOSE, class F>
 hipError_t with_team(int K, F&& f) {
-  constexpr int A = 8 / V, C = 16 / V;  // loads for 8 and 16 elements
-  if (K <= 8) return f(Team<V, A, 1, 1>{});
-  if (K <= 16) return f(Team<V, A, 2, 1>{});
-  if (K <= 32) return f(Team<V, A, 4, 1>{});
-  if (K <= 64) return f(Team<V, A, 8, 1>{});
-  if (K <= 128) return f(Team<V, A, 16, 1>{});
-  if (K <= 256) return f(Team<V, A, 32, 1>{});
-  if (K <= 512) return f(Team<V, A, 64, 1>{});
-  if (K <= 1024) return f(Team<V, C, 64, 1>{});
+  if (K <= 8) return f(Team<A, 1, 1, LOOSE>{});
+  if (K <= 16) return f(Team<A, 2, 1, LOOSE>{});
+  if (K <= 32) return f(Team<A, 4, 1, LOOSE>{});
+  if (K <= 64) return f(Team<A, 8, 1, LOOSE>{});
+  if (K <= 128) return f(Team<A, 16, 1, LOOSE>{});
+  if (K <= 256) return f(Team<A, 32, 1, LOOSE>{});
+  if (K <= 512) return f(Team<A, 64, 1, LOOSE>{});
+  if (K <= 1024) return f(Team<2 * A, 64, 1, LOOSE>{});
   // (a barrier a row: the fewer waves share one, the more rows a CU works on)
-  if (K <= 2048) return f(Team<V, A, 64, 4>{});
-  if (K <= 4096) return f(Team<V, C, 64, 4>{});
-  if (K <= 8192) return f(Team<V, C, 64, 8>{});
-  return f(Team<V, C, 64, 16>{});
+  if (K <= 2048) return f(Team<A, 64, 4, LOOSE>{});
+  if (K <= 4096) return f(Team<2 * A, 64, 4, LOOSE>{});
+  if (K <= 8192) return f(Team<2 * A, 64, 8, LOOSE>{});
+  return f(Team<2 * A, 64, 16, LOOSE>{});
 }
 
 template <class T, int V>
@@ -772,9 +819,9 @@ hipError_t balance_t(const void* logits, int64_t N, int K, int B, const int32_t*
   if (K <= kBalanceMaxK) {
     auto go = [&](auto team) {
       using P = decltype(team);
-      return rows_forward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
+      return rows_forward<T, P::NV, P::LPR, P::W, P::LOOSE>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
     };
-    return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go) : with_team<8 / VEC, true>(K, go);
   }
   return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC
              ? wide_forward<T, VEC>(logits, N, K, B, labels, S, valid, lse, out, buf, s)
@@ -788,9 +835,9 @@ hipError_t balance_grad_t(const void* logits, int64_t N, int K, int B, const flo
   if (K <= kBalanceMaxK) {
     auto go = [&](auto team) {
       using P = decltype(team);
-      return rows_backward<T, P::V, P::NV, P::LPR, P::W>(logits, N, K, B, lse, coef, dloss, dlogits, s);
+      return rows_backward<T, P::NV, P::LPR, P::W, P::LOOSE>(logits, N, K, B, lse, coef, dloss, dlogits, s);
     };
-    return vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC ? with_team<VEC>(K, go) : with_team<1>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go) : with_team<8 / VEC, true>(K, go);
   }
   const int64_t n = N * B;
   const dim3 grid((unsigned)capped(n));

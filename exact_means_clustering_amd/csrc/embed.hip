@@ -31,28 +31,36 @@ constexpr int kTileVecs = 256 * kVecs;    // vectors per workgroup tile
 // kernel spent 91 vector instructions per 8 elements and was bound by them
 // (2^23 rows of 128 fp32 to bf16: 404 us; 392 so).  The output is streamed
 // past the caches, which then keep the table (680 us without).
-template <class TI, class TO, int V>
+// LOOSE: rows that are no multiple of 16 bytes or start anywhere.  Vectors have
+// element alignment, a row's last one ends with it, and of that one only the
+// elements that the one before does not have are stored (65,536 rows of 2,049
+// bf16: 102 us; element by element 288 us).
+template <class TI, class TO, int V, bool LOOSE>
 __global__ __launch_bounds__(256) void embed_kernel(const typename TI::raw* __restrict__ table,
                                                     const int32_t* __restrict__ ids, int64_t n, uint32_t N, uint32_t K,
-                                                    int nv, uint32_t magic, int rpt, int nslab, int64_t tiles,
-                                                    float scale, typename TO::raw* __restrict__ out) {
+                                                    int nv, int D, uint32_t magic, int rpt, int nslab,
+                                                    int64_t tiles, float scale, typename TO::raw* __restrict__ out) {
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
     const int64_t row0 = nslab == 1 ? t * rpt : t / nslab;
     const int c0 = nslab == 1 ? 0 : (int)(t - row0 * nslab) * kTileVecs;
     const int64_t left = n - row0;
     const int limit = nslab == 1 ? (int)(left < rpt ? left : rpt) * nv : nv - c0 < kTileVecs ? nv - c0 : kTileVecs;
-    typename TO::raw* dst = out + (row0 * nv + c0) * V;
+    typename TO::raw* dst = out + row0 * D;
     const int32_t* id0 = ids + row0;
     // instance of the tile's first row and the rows it has left in it
     const uint32_t b0 = N < n ? (uint32_t)row0 / N : 0u;
     const uint32_t in_b0 = N < n ? N - ((uint32_t)row0 - b0 * N) : ~0u;
     bool live[kVecs];
+    uint32_t at[kVecs], row[kVecs];  // column of the vector's first element, and its row in the tile
     Pack<TI, V> v[kVecs];
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint32_t l = threadIdx.x + 256 * u;
       const uint32_t r = nslab != 1 ? 0u : nv == 1 ? l : __umulhi(l, magic);
       const uint32_t c = c0 + l - r * (uint32_t)nv;
+      row[u] = r;
+      at[u] = c * V;
+      if constexpr (LOOSE) at[u] = at[u] + V > (uint32_t)D ? (uint32_t)(D - V) : at[u];
       live[u] = false;
       v[u].zero();
       if ((int)l < limit) {
@@ -61,7 +69,9 @@ __global__ __launch_bounds__(256) void embed_kernel(const typename TI::raw* __re
         if (live[u]) {
           uint64_t e = id;
           if (N < n) e += (uint64_t)(r < in_b0 ? b0 : b0 + 1 + (r - in_b0) / N) * K;
-          v[u].load(table + (e * (uint32_t)nv + c) * V);
+          const typename TI::raw* from = table + (e * (uint32_t)D + at[u]);
+          if constexpr (LOOSE) v[u].load_loose(from);
+          else v[u].load(from);
         }
       }
     }
@@ -80,23 +90,30 @@ __global__ __launch_bounds__(256) void embed_kernel(const typename TI::raw* __re
       }
       Pack<TO, V> o;
       o.pack(f);
-      o.store_nt(dst + (int64_t)l * V);
+      if constexpr (LOOSE) {
+        typename TO::raw* to = dst + (row[u] * (uint32_t)D + at[u]);
+        const uint32_t c = c0 + l - row[u] * (uint32_t)nv;
+        if (at[u] == c * V) o.store_loose(to);
+        else o.store_range(to, (int)(c * V - at[u]), V);
+      } else {
+        o.store_nt(dst + (int64_t)(c0 + l) * V);
+      }
     }
   }
 }
 
-template <class TI, class TO, int V>
+template <class TI, class TO, int V, bool LOOSE>
 hipError_t embed_v(const void* table, const int32_t* ids, int64_t N, int K, int D, int B, float scale, void* out,
                    hipStream_t s) {
   const int64_t n = N * B;
-  const int nv = D / V;
+  const int nv = (D + V - 1) / V;
   const int nslab = (nv + kTileVecs - 1) / kTileVecs;
   const int rpt = nslab == 1 ? kTileVecs / nv : 1;
   const int64_t tiles = nslab == 1 ? (n + rpt - 1) / rpt : n * nslab;
   const int64_t grid = tiles < (1 << 22) ? tiles : (1 << 22);
   const uint32_t magic = (uint32_t)((((uint64_t)1 << 32) + nv - 1) / nv);  // (nv = 1 does without)
-  embed_kernel<TI, TO, V><<<dim3((unsigned)grid), dim3(256), 0, s>>>(
-      static_cast<const typename TI::raw*>(table), ids, n, (uint32_t)N, (uint32_t)K, nv, magic, rpt, nslab, tiles,
+  embed_kernel<TI, TO, V, LOOSE><<<dim3((unsigned)grid), dim3(256), 0, s>>>(
+      static_cast<const typename TI::raw*>(table), ids, n, (uint32_t)N, (uint32_t)K, nv, D, magic, rpt, nslab, tiles,
       scale, static_cast<typename TO::raw*>(out));
   return hipGetLastError();
 }
@@ -718,12 +735,15 @@ static hipError_t with_type(int dt, F&& f) {
 
 hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids, int64_t N, int K, int D, int B,
                         float scale, void* out, hipStream_t s) {
-  const int w = vec_width(D, 16 / dtype_size(odt), table, dtype_size(tdt), out, dtype_size(odt));
   return with_type(tdt, [&](auto ti) {
     return with_type(odt, [&](auto to) {
       using TI = decltype(ti);
       using TO = decltype(to);
-      FKM_PAIR(embed_v, w, table, ids, N, K, D, B, scale, out, s)
+      constexpr int V = 16 / TO::SZ;
+      if (vec_width(D, V, table, TI::SZ, out, TO::SZ) == V)
+        return embed_v<TI, TO, V, false>(table, ids, N, K, D, B, scale, out, s);
+      if (D >= V) return embed_v<TI, TO, V, true>(table, ids, N, K, D, B, scale, out, s);
+      return embed_v<TI, TO, 1, false>(table, ids, N, K, D, B, scale, out, s);
     });
   });
 }

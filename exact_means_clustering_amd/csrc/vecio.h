@@ -78,6 +78,45 @@ template <class T, int V> struct Pack {
       store(p);
     }
   }
+  // The same at an address aligned to its elements only (the hardware takes
+  // unaligned global accesses; the compiler is told the alignment it has).
+  struct __attribute__((packed, aligned(T::SZ))) Loose {
+    uint32_t w[W];
+  };
+  __device__ __forceinline__ void load_loose(const typename T::raw* p) {
+    static_assert(BYTES >= 4, "whole words");
+    const Loose v = *reinterpret_cast<const Loose*>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = v.w[i];
+  }
+  __device__ __forceinline__ void store_loose(typename T::raw* p) const {
+    Loose v;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v.w[i] = w[i];
+    *reinterpret_cast<Loose*>(p) = v;
+  }
+  // The first n < V elements only; the others keep what they hold.
+  __device__ __forceinline__ void load_head(const typename T::raw* p, int n) {
+#pragma unroll
+    for (int i = 0; i < V - 1; ++i) {
+      if (i >= n) continue;
+      if constexpr (T::SZ == 4) {
+        w[i] = __float_as_uint(p[i]);
+      } else {
+        const uint32_t h = p[i];
+        w[i / 2] = (i & 1) ? (w[i / 2] & 0xFFFFu) | h << 16 : (w[i / 2] & 0xFFFF0000u) | h;
+      }
+    }
+  }
+  // Elements from `from` to before `to` only.
+  __device__ __forceinline__ void store_range(typename T::raw* p, int from, int to) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i < from || i >= to) continue;
+      if constexpr (T::SZ == 4) p[i] = __uint_as_float(w[i]);
+      else p[i] = (uint16_t)((i & 1) ? w[i / 2] >> 16 : w[i / 2]);
+    }
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < W; ++i) w[i] = 0u;
