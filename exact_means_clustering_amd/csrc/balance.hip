@@ -3,8 +3,7 @@
 // logits (and writing the gradient) once.
 //
 // Rows up to kMaxK choices stay in registers.  A team of LPR lanes, or of W
-// whole waves, holds one row, E elements a lane, as 16-byte words where the
-// row allows it.  Forward, a lane owns its columns: after the row's maximum
+// whole waves, holds one row, E elements a lane, loaded 16 bytes at a time.  Forward, a lane owns its columns: after the row's maximum
 // and sum it adds its probabilities to its own column sums (fp32, by blocks of
 // kFold rows and over the lanes of a wave, then fp64), so the probabilities are
 // never written and the logits are read once.  A workgroup covers a chunk of rows of one

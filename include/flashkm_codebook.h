@@ -16,9 +16,8 @@
  *   Shapes: B instances (B = 1 is the plain problem) of N rows.  N may be 0
  *     and may be below or above K; pointers to arrays without elements may be
  *     null.  B >= 1, K >= 1, 1 <= D <= 2^20, B*N < 2^31, B*K < 2^31.
- *   Any D and K: rows whose length and address allow it move in 16-byte
- *     words, others element by element.  Pointers need their element type's
- *     alignment only.
+ *   Any D and K; pointers need their element type's alignment only (rows of
+ *     whole 16-byte words at 16-byte addresses move fastest).
  *   Outputs must not overlap inputs (KM_EINVAL).
  *   NaN and infinities in the data propagate as IEEE arithmetic has it; what
  *     an id outside [0,K) or an invalid row hides is never read into a result.
