@@ -524,13 +524,15 @@ int64_t sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, 
 // bf16 into 32,000 fp32 in 73 us against 106 us with the sort's own launches
 // and zeros by binary search; 4,099 rows accumulated into 131,072 in 36.5
 // against 52 us.  One workgroup argsorts the ids in LDS (stable radix
-// passes of 8 bits over 32-bit words: key, out-of-range bit, row), and the
+// passes of 8 or 9 bits over 32-bit words: key, out-of-range bit, row), and the
 // other workgroups of the launch meanwhile zero the gradient.  Ranks as in
 // the sort of many rows: digit matches inside a wave, a counter per wave and
 // digit, waves in row order.
 constexpr int kSortWaves = 16;
-// R: rounds of 64 keys per wave (the keys stay in registers).
-template <int R>
+// R: rounds of 64 keys per wave (the keys stay in registers); RB: digit bits
+// (9 where that saves a pass, as for keys of 17 and 18 bits: 36.5 to 33.4 us for
+// the 4,099 rows above, 52.3 to 46.2 us for 15,333 rows of 16 into 92,338).
+template <int R, int RB>
 __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __restrict__ ids, int n, uint32_t N,
                                                                uint32_t K, int row_bits, int passes,
                                                                uint2* __restrict__ kv, uint8_t* __restrict__ zero,
@@ -548,8 +550,9 @@ __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __
     return;
   }
   __shared__ uint32_t word[kSortWaves * 64 * R];
-  __shared__ uint32_t cnt[kSortWaves][256];
-  __shared__ uint32_t tot[256];
+  constexpr uint32_t DIG = 1u << RB;
+  __shared__ uint32_t cnt[kSortWaves][DIG];
+  __shared__ __align__(16) uint32_t tot[DIG];
   const int lane = tid & 63, w = tid >> 6;
   const int first = w * R * 64;
   uint32_t x[R], rank[R];
@@ -562,14 +565,14 @@ __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __
     x[r] = (key << 1 | (id < K ? 0u : 1u)) << row_bits | (uint32_t)at;
   }
   for (int p = 0; p < passes; ++p) {
-    const int shift = row_bits + 1 + 8 * p;
-    for (int i = tid; i < kSortWaves * 256; i += 1024) cnt[i >> 8][i & 255] = 0;
+    const int shift = row_bits + 1 + RB * p;
+    for (int i = tid; i < kSortWaves * (int)DIG; i += 1024) cnt[i >> RB][i & (DIG - 1)] = 0;
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const bool valid = first + r * 64 + lane < n;
-      const uint32_t d = x[r] >> shift & 255u;
-      const uint64_t m = match_digit<8>(d, valid);
+      const uint32_t d = x[r] >> shift & (DIG - 1);
+      const uint64_t m = match_digit<RB>(d, valid);
       const uint32_t low = (uint32_t)__popcll(m & ((1ull << lane) - 1ull));
       const uint32_t before = cnt[w][d];
       rank[r] = before + low;
@@ -578,7 +581,7 @@ __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __
       if constexpr (R > 8) __builtin_amdgcn_sched_barrier(0);
     }
     __syncthreads();
-    if (tid < 256) {
+    if (tid < (int)DIG) {
       uint32_t run = 0;
 #pragma unroll
       for (int q = 0; q < kSortWaves; ++q) {
@@ -589,10 +592,11 @@ __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __
       tot[tid] = run;
     }
     __syncthreads();
-    if (w == 0) {  // exclusive scan of the 256 digit totals, four a lane
-      uint32_t t[4], s = 0;
+    if (w == 0) {  // exclusive scan of the digit totals, PER a lane
+      constexpr int PER = (int)DIG / 64;
+      uint32_t t[PER], s = 0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) t[q] = tot[4 * lane + q], s += t[q];
+      for (int q = 0; q < PER; ++q) t[q] = tot[PER * lane + q], s += t[q];
       uint32_t inc = s;
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
@@ -601,12 +605,12 @@ __global__ __launch_bounds__(1024) void embed_grad_sort_kernel(const int32_t* __
       }
       uint32_t run = inc - s;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tot[4 * lane + q] = run, run += t[q];
+      for (int q = 0; q < PER; ++q) tot[PER * lane + q] = run, run += t[q];
     }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint32_t d = x[r] >> shift & 255u;
+      const uint32_t d = x[r] >> shift & (DIG - 1);
       if (first + r * 64 + lane < n) word[tot[d] + cnt[w][d] + rank[r]] = x[r];
     }
     __syncthreads();
@@ -645,17 +649,19 @@ void sort_one_launch(const int32_t* ids, int64_t n, uint32_t N, uint32_t K, int6
     blocks = (int64_t)(words / 4096) + 1;  // four words a thread
     if (blocks > 2048) blocks = 2048;
   }
-  auto go = [&](auto kernel) {
-    kernel<<<dim3((unsigned)(1 + blocks)), dim3(1024), 0, s>>>(ids, (int)n, N, K, bits_for(n),
-                                                               (bits_for(entries) + 7) / 8, kv,
-                                                               static_cast<uint8_t*>(zero), (int)head, words, (int)tail);
+  const int bits = bits_for(entries);
+  const bool nine = (bits + 8) / 9 < (bits + 7) / 8;
+  const int passes = nine ? (bits + 8) / 9 : (bits + 7) / 8;
+  auto go = [&](auto eight_bits, auto nine_bits) {
+    (nine ? nine_bits : eight_bits)<<<dim3((unsigned)(1 + blocks)), dim3(1024), 0, s>>>(
+        ids, (int)n, N, K, bits_for(n), passes, kv, static_cast<uint8_t*>(zero), (int)head, words, (int)tail);
   };
   static_assert(kSortOne == kSortWaves * 64 * 16, "the longest sort's rounds");
-  if (n <= 1024) go(embed_grad_sort_kernel<1>);
-  else if (n <= 2048) go(embed_grad_sort_kernel<2>);
-  else if (n <= 4096) go(embed_grad_sort_kernel<4>);
-  else if (n <= 8192) go(embed_grad_sort_kernel<8>);
-  else go(embed_grad_sort_kernel<16>);
+  if (n <= 1024) go(embed_grad_sort_kernel<1, 8>, embed_grad_sort_kernel<1, 9>);
+  else if (n <= 2048) go(embed_grad_sort_kernel<2, 8>, embed_grad_sort_kernel<2, 9>);
+  else if (n <= 4096) go(embed_grad_sort_kernel<4, 8>, embed_grad_sort_kernel<4, 9>);
+  else if (n <= 8192) go(embed_grad_sort_kernel<8, 8>, embed_grad_sort_kernel<8, 9>);
+  else go(embed_grad_sort_kernel<16, 8>, embed_grad_sort_kernel<16, 9>);
 }
 
 template <class TI, class TO, int V>

@@ -188,7 +188,8 @@ GRAD_SHAPES = [(1, 1, 1, 1, "mixed"), (1, 37, 1000, 80, "mixed"), (1, 1000, 77, 
                (2, 20000, 3, 8, "one"), (1, 70001, 5000, 20, "zipf"), (1, 17000, 70000, 8, "zipf"), (64, 40, 256, 32, "mixed"),
                # one word cannot hold key and row (sorted by launches); just past each limit of the one-workgroup sorts
                (1, 9000, 300000, 8, "zipf"), (1, 257, 33, 40, "zipf"), (2, 513, 40, 136, "mixed"), (1, 4097, 131072, 4, "mixed"),
-               (1, 8193, 1, 8, "one"), (1, 16385, 600, 8, "mixed"),
+               (1, 8193, 1, 8, "one"), (1, 16385, 600, 8, "mixed"), (1, 15333, 92338, 4, "mixed"),
+               (1, 900, 200000, 4, "mixed"), (1, 2000, 300, 4, "mixed"), (3, 1000, 90000, 4, "mixed"),
                # ids outside the table on every path of the sort by launches: two packed passes, three passes, one
                # segmented pass, large tiles
                (1, 70003, 5000, 20, "mixed"), (1, 70003, 300000, 4, "mixed"), (40, 2000, 200, 8, "mixed"),
