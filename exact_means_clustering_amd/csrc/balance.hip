@@ -401,8 +401,8 @@ void balance_rows_kernel(
 template <int CB>
 __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part, int64_t chunks,
                                                             const int32_t* cpart, int64_t cchunks,
-                                                            const int32_t* __restrict__ vpart, int64_t vchunks, int K,
-                                                            int S, int kblocks, int64_t units, BalanceOut out,
+                                                            const int32_t* __restrict__ vpart, int64_t vchunks,
+                                                            uint32_t K, int S, int kblocks, int64_t units, BalanceOut out,
                                                             double* __restrict__ terms) {
   constexpr int G = 1024 / CB;
   __shared__ double sp[1024];
@@ -412,7 +412,8 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restr
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t b = u / kblocks;
     const int kb = (int)(u - b * kblocks);
-    const int k = kb * CB + tid % CB, g = tid / CB;
+    const uint32_t k = (uint32_t)kb * CB + tid % CB;
+    const int g = tid / CB;
     int64_t nv = 0;
     for (int64_t c = tid; c < vchunks; c += 1024) nv += vpart[b * vchunks + c];
     double p = 0.0;
@@ -431,7 +432,7 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restr
       if (tid < h) sp[tid] += sp[tid + h], sc[tid] += sc[tid + h];
     }
     double term = 0.0;
-    if (tid < CB && k < K) term = balance_entry(out, b * K + k, K, S, T_, sp[tid], sc[tid]);
+    if (tid < CB && k < K) term = balance_entry(out, b * K + k, (int)K, S, T_, sp[tid], sc[tid]);
     term = block_sum_f64<16>(term, tmp);  // its barriers also end this unit's use of sp and sc
     if (tid == 0) {
       if (kblocks == 1) out.loss[b] = (float)term;
@@ -542,12 +543,13 @@ __global__ __launch_bounds__((Rows<T, NV, LPR, W, LOOSE>::BLOCK)) void balance_g
 // ---------------------------------------------------------------------------
 // rows longer than the registers hold
 // ---------------------------------------------------------------------------
+// Columns are unsigned: K may be 2^31 - 1, and a step past it must not wrap.
 // One workgroup per row, V elements per load; f(values, first column) over the
 // row's elements that thread tid takes, in order.
 template <class T, int V, class F>
-__device__ __forceinline__ void over_row(const typename T::raw* __restrict__ row, int K, F&& f) {
+__device__ __forceinline__ void over_row(const typename T::raw* __restrict__ row, uint32_t K, F&& f) {
 #pragma unroll 4
-  for (int k = threadIdx.x * V; k < K; k += 256 * V) {
+  for (uint32_t k = threadIdx.x * V; k < K; k += 256 * V) {
     Pack<T, V> p;
     float x[V];
     p.load(row + k);
@@ -580,7 +582,7 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
       continue;
     }
     float m = -INFINITY, s = 0.f;
-    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int) {
+    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t) {
       float top = x[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
@@ -612,11 +614,11 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
 // per thread.
 template <class T, int V>
 __global__ __launch_bounds__(256) void balance_cols_kernel(const typename T::raw* __restrict__ logits, int64_t N,
-                                                           int K, int64_t chunks, int kblocks, int64_t units,
+                                                           uint32_t K, int64_t chunks, uint32_t kblocks, int64_t units,
                                                            const float2* __restrict__ ms, float* __restrict__ part) {
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t bc = u / kblocks;
-    const int k = ((int)(u - bc * kblocks) * 256 + threadIdx.x) * V;
+    const uint32_t k = ((uint32_t)(u - bc * kblocks) * 256 + threadIdx.x) * V;
     if (k >= K) continue;
     const int64_t b = bc / chunks, c = bc - b * chunks;
     const int64_t i0 = c * kBalanceRows, i1 = i0 + kBalanceRows < N ? i0 + kBalanceRows : N;
@@ -678,7 +680,7 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
     float mean = 0.f, scale = 0.f;
     if (!none) {
       float s = 0.f, d = 0.f;
-      over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
+      over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t k) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float e = exp_diff<T>(x[v], z);
@@ -691,7 +693,7 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
       mean = t.y * inv, scale = dloss[b] * inv;
     }
     // the row again (from the cache) for the gradient
-    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], int k) {
+    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t k) {
       float o[V];
 #pragma unroll
       for (int v = 0; v < V; ++v) o[v] = none ? 0.f : scale * exp_diff<T>(x[v], z) * (cf[k + v] - mean);
@@ -716,7 +718,7 @@ struct JoinIn {
 };
 template <int CB>
 void join_launch(const JoinIn& in, int K, int S, int B, const BalanceOut& out, double* terms, hipStream_t s) {
-  const int kblocks = (K + CB - 1) / CB;
+  const int kblocks = (int)(((uint32_t)K + CB - 1) / CB);
   const int64_t units = (int64_t)B * kblocks;
   const int64_t grid = units < (1 << 20) ? units : (1 << 20);
   balance_join_kernel<CB><<<dim3((unsigned)grid), dim3(1024), 0, s>>>(in.part, in.chunks, in.cpart, in.cchunks,
@@ -804,7 +806,7 @@ hipError_t wide_forward(const void* logits, int64_t N, int K, int B, const int32
         labels, n, (uint32_t)N, (uint32_t)K, S, valid, out.counts, buf.vpart);
   }
   const int64_t chunks = balance_wide_chunks(N);
-  const int kblocks = (K + 256 * V - 1) / (256 * V);
+  const uint32_t kblocks = ((uint32_t)K + 256 * V - 1) / (256 * V);
   const int64_t units = B * chunks * kblocks;
   balance_cols_kernel<T, V><<<dim3((unsigned)capped(units)), dim3(256), 0, s>>>(x, N, K, chunks, kblocks, units,
                                                                                  buf.ms, buf.part);

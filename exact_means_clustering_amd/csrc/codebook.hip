@@ -118,7 +118,7 @@ BalanceLayout balance_layout(int64_t N, int K, int B) {
   L.part = o;   o = al256(o + cells * 4);
   L.cpart = o;  o = al256(o + (wide ? 0 : cells * 4));
   L.vpart = o;  o = al256(o + (wide ? (size_t)B : (size_t)B * chunks) * 4);
-  L.terms = o;  o = al256(o + (size_t)B * ((K + kBalanceJoinCols - 1) / kBalanceJoinCols) * 8);
+  L.terms = o;  o = al256(o + (size_t)B * (((size_t)K + kBalanceJoinCols - 1) / kBalanceJoinCols) * 8);
   L.ms = o;     o = al256(o + (wide ? (size_t)B * N * 8 : 0));
   L.total = o;
   return L;

@@ -195,3 +195,11 @@ def test_binding_refuses_what_is_not_on_the_gpu():
             call()
     with pytest.raises(km.KMeansError, match="32 bits"):
         km.embed_grad_workspace_bytes(10, 1 << 32, 64)
+
+
+@pytest.mark.parametrize("N, K", [(1, (1 << 31) - 1), (1, (1 << 31) - 8), (1, (1 << 31) - 31), (100, (1 << 31) - 2),
+                                  (129, (1 << 31) - 2049), (64, 20001)])
+def test_balance_workspace_at_the_largest_k(lib, N, K):
+    # longer rows: column sums of every chunk of 64 rows, a term of the loss for every 32 columns, two values a row
+    need = -(-N // 64) * K * 4 + -(-K // 32) * 8 + N * 8
+    assert need <= lib.kmeans_balance_workspace_bytes(N, K, 1, 1) <= need + 8 * 256

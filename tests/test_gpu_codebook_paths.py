@@ -1,0 +1,49 @@
+"""The codebook operators on the paths that tests/test_gpu_codebook.py does not reach (definitions and tolerances there;
+u = 2^-24)."""
+
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_codebook import BF16, U, half_step, km  # noqa: F401  (km is the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def pieces(n, size=1 << 28):
+    for at in range(0, n, size):
+        yield at, min(n, at + size)
+
+
+def test_balance_at_the_largest_k(km):  # noqa: F811
+    # Column counts next to 2^31.  With logits of 0 (and, for the gradient, which takes nothing but the live rows from
+    # it, an lse of 0) a thread adds fewer than 2^24 ones, exactly; 8 levels of joins then round both sums.
+    K = (1 << 31) - 8
+    x = torch.zeros(1, K, dtype=BF16, device="cuda")
+    out = [0, 7, 1 << 30, K - 2049, K - 3]
+    named = [5, K - 1]
+    x[0, out] = -math.inf
+    left = K - len(out)
+    loss, counts, prob, (lse, coef) = km.balance(x, torch.tensor([named], dtype=torch.int32, device="cuda"))
+    assert int(counts.sum(dtype=torch.int64)) == 2 and counts[named].tolist() == [1, 1]
+    assert abs(float(lse[0]) - math.log(left)) <= 20 * U * math.log(left)
+    assert abs(float(loss) - K / left) <= 16 * U * K / left
+    assert not prob[out].any()
+    # K / 2 has 28 bits, the fp32 coef 24: one rounding
+    assert all(abs(c - K / 2) <= U * K / 2 for c in coef[named].tolist()) and int((coef != 0).sum()) == 2
+    near = sum(int(((prob[a:b].double() * left - 1).abs() <= 16 * U).sum()) for a, b in pieces(K))
+    assert near == left
+    del prob, counts
+    dl = 1024.0
+    dx = km.balance_grad(x, (torch.zeros_like(lse), coef), torch.full((1,), dl, device="cuda"))[0]
+    assert not dx[out].any()
+    mean = K / left                                      # of coef under p
+    tol = 64 * U + half_step(BF16) * (1 + 64 * U)
+    want = dl / left * (K / 2 - mean)
+    assert all(abs(float(v) - want) <= tol * want for v in dx[named])
+    want = dl / left * mean
+    near = sum(int(((dx[a:b].float() + want).abs() <= tol * want).sum()) for a, b in pieces(K))
+    assert near == left - 2
+    del dx, coef, x
+    torch.cuda.empty_cache()
