@@ -570,30 +570,49 @@ __device__ __forceinline__ float2 block_sum2(float a, float b, float2* tmp) {
 // lse of every row (+inf for an invalid one) and its (maximum, 1 / sum of
 // exponentials), (0, 0) for a row that leaves no probability: the
 // probabilities come from these, since a large lse has lost the sum's low
-// bits.  One read: a thread keeps a running maximum and the sum relative to it.
+// bits.  One read: a thread keeps a running maximum and the sum relative to it,
+// fp32 over a load's elements and fp64 over its loads (in fp32 alone a row of
+// 2^24 equal values rounds the same way 65,536 times: lse off by 1.6e-4).
+// Loads of single elements go in groups of G, to share one step in fp64.
 template <class T, int V>
 __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw* __restrict__ logits, int64_t n, int K,
                                                           const uint8_t* __restrict__ valid, float* __restrict__ lse,
                                                           float2* __restrict__ ms) {
+  constexpr int G = V == 1 ? 4 : 1;
   __shared__ float2 tmp[4];
+  const uint32_t tid = threadIdx.x, Ku = K;
   for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
     if (valid && !valid[i]) {  // uniform over the workgroup
       if (threadIdx.x == 0) lse[i] = INFINITY, ms[i] = make_float2(0.f, 0.f);
       continue;
     }
-    float m = -INFINITY, s = 0.f;
-    over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t) {
+    float m = -INFINITY;
+    double s = 0.0;
+    const typename T::raw* row = logits + i * K;
+#pragma unroll G == 1 ? 4 : 2
+    for (uint32_t k = tid * V; k < Ku; k += 256 * V * G) {
+      float x[V * G];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const uint32_t at = k + 256 * V * g;
+        Pack<T, V> p;
+        p.load(row + (G == 1 || at < Ku ? at : k));  // (no branch: the loads of a group are in flight together)
+        p.unpack(x + g * V);
+        if (G > 1 && at >= Ku) x[g] = -INFINITY;
+      }
       float top = x[0];
 #pragma unroll
-      for (int v = 1; v < V; ++v) top = fmaxf(top, x[v]);
+      for (int v = 1; v < V * G; ++v) top = fmaxf(top, x[v]);
       if (top > m) {  // the sum moves to the new maximum (from nothing, if that was -inf)
-        s *= exp_diff<T>(m, top);
+        s *= (double)exp_diff<T>(m, top);
         m = top;
       }
       const float shift = m == -INFINITY ? 0.f : m;
+      float e = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s += exp_diff<T>(x[v], shift);
-    });
+      for (int v = 0; v < V * G; ++v) e += exp_diff<T>(x[v], shift);
+      s += (double)e;
+    }
     // the workgroup's maximum, then the sums relative to it
     const float wm = team_max<64>(m);
     __syncthreads();
@@ -602,7 +621,7 @@ __global__ __launch_bounds__(256) void balance_lse_kernel(const typename T::raw*
     const float top = fmaxf(fmaxf(tmp[0].x, tmp[1].x), fmaxf(tmp[2].x, tmp[3].x));
     const float shift = top == -INFINITY ? 0.f : top;
     // a thread without a maximum holds 0 (or NaN), relative to 0
-    const float sum = block_sum2(m == -INFINITY ? s : s * exp_diff<T>(m, shift), 0.f, tmp).x;
+    const float sum = block_sum2(m == -INFINITY ? (float)s : (float)s * exp_diff<T>(m, shift), 0.f, tmp).x;
     if (threadIdx.x == 0) {
       lse[i] = sum == 0.f ? -INFINITY : top + logf(sum);
       ms[i] = sum == 0.f ? make_float2(0.f, 0.f) : make_float2(shift, 1.f / sum);
@@ -679,16 +698,18 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
     const float* cf = coef + b * K;
     float mean = 0.f, scale = 0.f;
     if (!none) {
-      float s = 0.f, d = 0.f;
+      double s = 0.0, d = 0.0;  // as in the forward pass
       over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t k) {
+        float es = 0.f, ds = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const float e = exp_diff<T>(x[v], z);
-          s += e;
-          d = fmaf(e, cf[k + v], d);
+          es += e;
+          ds = fmaf(e, cf[k + v], ds);
         }
+        s += (double)es, d += (double)ds;
       });
-      const float2 t = block_sum2(s, d, tmp);
+      const float2 t = block_sum2((float)s, (float)d, tmp);
       const float inv = 1.f / t.x;
       mean = t.y * inv, scale = dloss[b] * inv;
     }

@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_codebook import BF16, U, half_step, km  # noqa: F401  (km is the fixture)
+from tests.test_gpu_codebook import BF16, F16, F32, U, half_step, km, tiny  # noqa: F401  (km is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,39 @@ def test_balance_at_the_largest_k(km):  # noqa: F811
     assert near == left - 2
     del dx, coef, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype, K", [(BF16, 1 << 24), (F16, (1 << 22) + 5), (F32, (1 << 23) + 4)])
+def test_balance_sums_of_very_long_rows(km, dtype, K):  # noqa: F811
+    # rows of equal logits but for one and for the first 2,048 (below a thread's own maximum every addition of a long
+    # sum rounds the same way), and a random row
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    x = torch.full((3, K), -2.0, dtype=dtype, device="cuda")
+    x[0, 3] = 0
+    x[2, :2048] = 0
+    x[1] = torch.randn(K, generator=g, device="cuda") * 2
+    labels = torch.randint(0, K, (3, 3), generator=g, device="cuda", dtype=torch.int32)
+    dl = torch.full((1,), float(K), device="cuda")
+    loss, counts, prob, (lse, coef) = km.balance(x, labels)
+    dx = km.balance_grad(x, (lse, coef), dl)
+    z = x.double()
+    p = torch.softmax(z, -1)
+    R = z.amax(-1, keepdim=True) - z.amin(-1, keepdim=True)
+    # an exponential (R + 4) u; a thread's sum of up to 256 fp32 values before 64 bits take it over, then 10 roundings
+    row = (R + 4 + 256 + 10) * U
+    want = torch.logsumexp(z, -1)
+    assert bool(((lse.double() - want).abs() <= row[:, 0] + 3 * U * want.abs()).all())
+    rel = (row + (R + 8) * U).max()
+    want = p.mean(0)
+    assert bool(((prob.double() - want).abs() <= rel * want).all())
+    want = K / 3 * (counts.double() / 3 * want).sum()
+    assert float((loss.double() - want).abs()) <= float((rel + U) * want)
+    c = coef.double()
+    dot = (p * c).sum(-1, keepdim=True)
+    want = float(dl) * p * (c - dot)
+    tol = float(dl) * p * ((rel + 4 * U) * (c + dot) + rel * dot + 266 * U * dot)
+    tol = tol * 1.01 + half_step(dtype) * (want.abs() + tol) + tiny(dtype) + 2.0 ** -126 * float(dl) * (c + dot)
+    # (a labelled column's gradient may be past the type's range)
+    over = torch.isinf(dx) & (want.abs() + tol >= torch.finfo(dtype).max)
+    assert bool((((dx.double() - want).abs() <= tol) | over).all())
