@@ -78,7 +78,10 @@ KM_API size_t kmeans_balance_workspace_bytes(int64_t N, int32_t K, int32_t B, in
  * At most 2^22 instances.
  * T = 0 gives loss, prob and coef 0.  A valid row whose logits are all -inf
  * has lse -inf and leaves no probability (it still counts in T).  A choice with
- * logit -inf has probability 0.  Balanced use gives loss 1. */
+ * logit -inf has probability 0.  A valid row with a NaN or a +inf has no
+ * softmax (inf - inf): its lse is NaN, never the +inf of an invalid row, and
+ * prob and loss of its instance are NaN; counts, coef and the other rows' lse
+ * are not touched by it.  Balanced use gives loss 1. */
 KM_API int kmeans_balance(const void* logits, int32_t dtype, int64_t N, int32_t K, int32_t B,
                           const int32_t* labels, int32_t S, const uint8_t* valid, float* loss, int32_t* counts,
                           float* prob, float* lse, float* coef, void* ws, size_t ws_bytes, void* stream);
@@ -89,7 +92,7 @@ KM_API int kmeans_balance(const void* logits, int32_t dtype, int64_t N, int32_t 
  *   dlogits[b,i,:] = dloss[b] * p * (coef[b,:] - sum_k p_k coef[b,k])
  * rounded once into dtype.  lse only says which rows have probabilities: rows
  * with lse +inf (invalid) or -inf (nothing left) get zeros, whatever their
- * logits hold.  (p is taken from the logits again, since an fp32 lse of large
+ * logits hold; a row with lse NaN gets NaN.  (p is taken from the logits again, since an fp32 lse of large
  * magnitude does not hold the logarithm of the sum.) */
 KM_API int kmeans_balance_grad(const void* logits, int32_t dtype, int64_t N, int32_t K, int32_t B,
                                const float* lse, const float* coef, const float* dloss, void* dlogits, void* stream);

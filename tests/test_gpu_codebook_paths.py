@@ -6,7 +6,7 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_codebook import BF16, F16, F32, U, half_step, km, tiny  # noqa: F401  (km is the fixture)
+from tests.test_gpu_codebook import BF16, F16, F32, TYPES, U, half_step, km, tiny  # noqa: F401  (km is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,30 @@ def test_balance_sums_of_very_long_rows(km, dtype, K):  # noqa: F811
     # (a labelled column's gradient may be past the type's range)
     over = torch.isinf(dx) & (want.abs() + tol >= torch.finfo(dtype).max)
     assert bool((((dx.double() - want).abs() <= tol) | over).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [3, 64, 189, 1500, 9000, 16500, 20001])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_balance_rows_without_a_softmax(km, dtype, K, bad):  # noqa: F811
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    x = torch.randn(2, 9, K, generator=g, device="cuda").to(dtype)
+    labels = torch.randint(0, K, (2, 9), generator=g, device="cuda", dtype=torch.int32)
+    valid = torch.ones(2, 9, dtype=torch.bool, device="cuda")
+    valid[0, 2] = False
+    x[0, 2, K // 2] = bad                                # of an invalid row: no consequence
+    plain = x.clone()
+    x[1, 4, K - 1] = bad
+    want = km.balance(plain, labels, valid=valid)
+    got = km.balance(x, labels, valid=valid)
+    assert torch.equal(got[1], want[1]) and torch.equal(got[3][1], want[3][1])
+    assert torch.equal(got[0][0], want[0][0]) and bool(torch.isnan(got[0][1]))
+    assert torch.equal(got[2][0], want[2][0]) and bool(torch.isnan(got[2][1]).all())
+    rest = torch.ones(2, 9, dtype=torch.bool, device="cuda")
+    rest[1, 4] = False
+    assert bool(torch.isnan(got[3][0][1, 4])) and torch.equal(got[3][0][rest], want[3][0][rest])
+    assert bool(torch.isinf(got[3][0][0, 2]))
+    dl = torch.full((2,), 9.0, device="cuda")
+    dx, dw = km.balance_grad(x, got[3], dl), km.balance_grad(plain, want[3], dl)
+    assert bool(torch.isnan(dx[1, 4]).all()) and torch.equal(dx[rest], dw[rest]) and not dx[0, 2].any()
