@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 
 import torch
@@ -444,8 +445,8 @@ def fit_streamed(X_host, C0, iters: int, device_x_budget: int, *, history: bool 
 
 
 def _on_stream(fn):
-    """Run fn with its first CUDA tensor's device, and ``stream`` if one is given, current: what it allocates then
-    belongs to the stream that uses it."""
+    """Give fn a keyword ``stream``: it runs with its first CUDA tensor's device, and ``stream`` if one is given,
+    current, so what it allocates belongs to the stream that uses it."""
     @functools.wraps(fn)
     def run(*args, stream=None, **kwargs):
         t = args[0] if args else None
@@ -462,6 +463,9 @@ def _on_stream(fn):
             return fn(*args, **kwargs)
         with torch.cuda.device(t.device):
             return fn(*args, **kwargs)
+    sig = inspect.signature(fn)
+    run.__signature__ = sig.replace(parameters=[
+        *sig.parameters.values(), inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return run
 
 
@@ -517,7 +521,8 @@ def _at(t):
 @_on_stream
 def embed(table, ids, *, scale: float = 1.0, out_dtype=None, out=None):
     """Table lookup with scaling: out[.., i, :] = scale * table[.., ids[.., i], :], rounded once; zeros for ids outside
-    [0, K).  table [K, D] with ids [N], or [B, K, D] with ids [B, N] int32; out_dtype defaults to the table's."""
+    [0, K).  table [K, D] with ids [N], or [B, K, D] with ids [B, N] int32; out_dtype defaults to the table's.  Runs on
+    ``stream`` (default: the current one)."""
     _need(table, "table")
     dt = _dtype(table)
     if table.dim() not in (2, 3):
@@ -545,7 +550,7 @@ def embed_grad_workspace_bytes(N: int, K: int, D: int, B: int = 1) -> int:
 def embed_grad(dout, ids, K: int, *, scale: float = 1.0, grad_dtype=None, out=None, accumulate: bool = False, ws=None):
     """Gradient of embed with respect to the table: [.., K, D], the sum of scale * dout[.., i, :] over the rows i with
     ids[.., i] = k (deterministic, fp32 sums rounded once into grad_dtype, fp32 by default).  accumulate adds to ``out``
-    and leaves the entries that no row names untouched."""
+    and leaves the entries that no row names untouched.  Runs on ``stream`` (default: the current one)."""
     _need(dout, "dout")
     dt = _dtype(dout)
     if dout.dim() not in (2, 3):
@@ -584,7 +589,8 @@ def _logits(logits):
 def balance(logits, labels, *, valid=None, ws=None):
     """Balance loss of the use of K choices: logits [.., N, K], labels [.., N] or [.., N, S] int32 (the selections, for
     instance from assign or assign_top2), valid [.., N] bool or None.  Returns (loss fp32 [B], counts int32 [.., K],
-    mean probabilities fp32 [.., K], (lse fp32 [.., N], coef fp32 [.., K])); the last pair is what balance_grad needs."""
+    mean probabilities fp32 [.., K], (lse fp32 [.., N], coef fp32 [.., K])); the last pair is what balance_grad needs.
+    Runs on ``stream`` (default: the current one)."""
     dt, B, N, K = _logits(logits)
     _need(labels, "labels", torch.int32, like=logits)
     lead = tuple(logits.shape[:-1])
@@ -609,7 +615,8 @@ def balance(logits, labels, *, valid=None, ws=None):
 @_on_stream
 def balance_grad(logits, saved, dloss, *, out=None):
     """Gradient of the balance loss with respect to the logits: ``saved`` = the (lse, coef) of balance, dloss fp32 [B]
-    the derivative of what follows with respect to the loss.  Returns dlogits, of the logits' shape and type."""
+    the derivative of what follows with respect to the loss.  Returns dlogits, of the logits' shape and type.  Runs on
+    ``stream`` (default: the current one)."""
     dt, B, N, K = _logits(logits)
     lse, coef = saved
     _into(lse, "lse", logits.shape[:-1], torch.float32, logits)

@@ -203,3 +203,14 @@ def test_balance_workspace_at_the_largest_k(lib, N, K):
     # longer rows: column sums of every chunk of 64 rows, a term of the loss for every 32 columns, two values a row
     need = -(-N // 64) * K * 4 + -(-K // 32) * 8 + N * 8
     assert need <= lib.kmeans_balance_workspace_bytes(N, K, 1, 1) <= need + 8 * 256
+
+
+@pytest.mark.parametrize("name", ["embed", "embed_grad", "balance", "balance_grad"])
+def test_binding_shows_its_stream_argument(name):
+    import inspect
+
+    import exact_means_clustering_amd as km
+    fn = getattr(km, name)
+    p = inspect.signature(fn).parameters["stream"]
+    assert p.kind is inspect.Parameter.KEYWORD_ONLY and p.default is None
+    assert "stream" in fn.__doc__
