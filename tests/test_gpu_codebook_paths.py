@@ -110,3 +110,93 @@ def test_balance_rows_without_a_softmax(km, dtype, K, bad):  # noqa: F811
     dl = torch.full((2,), 9.0, device="cuda")
     dx, dw = km.balance_grad(x, got[3], dl), km.balance_grad(plain, want[3], dl)
     assert bool(torch.isnan(dx[1, 4]).all()) and torch.equal(dx[rest], dw[rest]) and not dx[0, 2].any()
+
+
+# ---- gradient of the lookup ------------------------------------------------------------------------------------------
+
+def ids_on_gpu(n, K, kind, g):
+    r = torch.rand(n, generator=g, device="cuda", dtype=torch.float64)
+    if kind == "one":
+        ids = torch.full((n,), K // 2, device="cuda")
+    elif kind == "hot":                                  # half of the rows on a few entries, a tenth on none
+        ids = (r ** 6 * K).long()
+        ids[torch.rand(n, generator=g, device="cuda") < 0.1] = -1
+    elif kind == "runs":                                 # 15 to 17 rows an entry: segments that end at and around a unit's edge
+        ids = torch.arange(n, device="cuda") // 16 % K
+        ids[::31] = (ids[::31] + 1) % K
+        ids = ids[torch.randperm(n, generator=g, device="cuda")]
+    else:                                                # ids outside the table among them
+        ids = (r * 1.1 * K).long()
+        ids[::97] = -(1 << 31)
+    return ids.to(torch.int32)
+
+
+def check_grad_on_gpu(got, dout, ids, K, scale, old=None):
+    """got [K, D] against the definition in 64 bits, with the tolerance of test_gpu_codebook.check_grad."""
+    D = dout.shape[1]
+    hit = ((ids >= 0) & (ids < K)).nonzero()[:, 0]
+    key, order = torch.sort(ids[hit].long(), stable=True)
+    rows = hit[order]
+    ends = torch.searchsorted(key, torch.arange(K + 1, device="cuda"))
+    m = ends[1:] - ends[:-1]
+    s32 = float(torch.tensor(scale, dtype=F32))
+    for a in range(0, D, 256):                           # columns in pieces
+        x = dout[:, a:a + 256][rows].double()
+        total, mag = (torch.segment_reduce(v, "sum", lengths=m, axis=0, initial=0.0) for v in (x, x.abs()))
+        y = got[:, a:a + 256]
+        want = s32 * total
+        tol = (m + 1).double()[:, None] * U * abs(s32) * mag * 1.01
+        bare = m == 0
+        if old is None:
+            assert not y[bare].any()
+        else:
+            o = old[:, a:a + 256]
+            assert torch.equal(y[bare], o[bare])
+            want = want + o.double()
+            tol = tol + 2 * U * (want.abs() + abs(s32) * mag)
+        tol = tol + half_step(got.dtype) * (want.abs() + tol) + tiny(got.dtype)
+        bad = (y.double() - want).abs() > tol
+        assert not bool(bad.any()), (a, int(bad.sum()))
+
+
+def run_grad(km, n, K, D, kind, of, to):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n * 7 + D)
+    dout = torch.randn(n, D, generator=g, device="cuda").to(of)
+    ids = ids_on_gpu(n, K, kind, g)
+    got = km.embed_grad(dout, ids, K, scale=0.3, grad_dtype=to)
+    check_grad_on_gpu(got, dout, ids, K, 0.3)
+    old = torch.randn(K, D, generator=g, device="cuda").to(to)
+    buf = old.clone()
+    km.embed_grad(dout, ids, K, scale=1.5, out=buf, accumulate=True)
+    check_grad_on_gpu(buf, dout, ids, K, 1.5, old)
+
+
+@pytest.mark.parametrize("of, to", [(BF16, F32), (F16, F16), (F32, F32), (BF16, BF16), (F32, BF16)])
+@pytest.mark.parametrize("n, K, D, kind", [
+    # rows of whole vectors wider than a wave: one slab, a second one of a single vector, several; rows of 4 elements at
+    # a time and of single ones; joins inside the workgroup and of one and two levels behind it
+    (300, 40, 512, "mixed"), (300, 9, 520, "hot"), (2000, 100, 1024, "runs"), (4099, 700, 1024, "hot"),
+    (5000, 3, 2048, "mixed"), (6000, 1, 1024, "one"), (9001, 500, 1028, "runs"), (16384, 900, 1024, "runs"),
+    (20011, 60000, 520, "hot"), (20011, 1300, 1536, "runs"), (70001, 1000, 1024, "hot"), (70001, 2, 1024, "one"),
+    (70001, 90, 1029, "hot")])
+def test_embed_grad_of_wide_rows(km, of, to, n, K, D, kind):  # noqa: F811
+    run_grad(km, n, K, D, kind, of, to)
+
+
+@pytest.mark.parametrize("n", [256, 257, 1024, 1025, 2048, 2049, 4096, 4097, 8192, 8193, 16384, 16385])
+@pytest.mark.parametrize("K", [600, 200000])
+def test_embed_grad_at_its_limits(km, n, K):  # noqa: F811
+    run_grad(km, n, K, 1024 if K == 600 else 136, "hot", BF16, F32)
+
+
+@pytest.mark.parametrize("n", [1 << 23, (1 << 23) + 1, (1 << 23) + 4099])
+@pytest.mark.parametrize("K", [5000, 65536, 90000])
+def test_embed_grad_of_more_rows_than_a_packed_word_holds(km, n, K):  # noqa: F811
+    run_grad(km, n, K, 8, "mixed", BF16, F32)
+
+
+@pytest.mark.parametrize("of, to", [(BF16, F32), (F32, F32), (F16, F16)])
+@pytest.mark.parametrize("D", [1, 16, 40, 100, 264])
+def test_embed_grad_of_narrow_rows_at_a_large_n(km, of, to, D):  # noqa: F811
+    run_grad(km, 700003, 30000, D, "hot", of, to)
