@@ -200,3 +200,102 @@ def test_embed_grad_of_more_rows_than_a_packed_word_holds(km, n, K):  # noqa: F8
 @pytest.mark.parametrize("D", [1, 16, 40, 100, 264])
 def test_embed_grad_of_narrow_rows_at_a_large_n(km, of, to, D):  # noqa: F811
     run_grad(km, 700003, 30000, D, "hot", of, to)
+
+
+# ---- balance: rings that turn, blocks that fold, chunks that join --------------------------------------------------------
+
+def balance_depths(K, steps):
+    """(row, column): roundings of a row's sum and of a column's.  K <= 16,384: a lane adds K / 64 + 16 values at most,
+    then 6 levels and up to 16 waves; a column has blocks of 64 rows, then the blocks, 6 levels and one rounding of a
+    chunk.  Longer rows: a load's 8 values, fp64, 10 roundings; a column has the 64 rows of a chunk and its rounding."""
+    if K > 16384:
+        return 20, 66
+    return K / 64 + 40, 64 + -(-steps // 64) + 8
+
+
+def check_balance_on_gpu(km, B, N, K, S, dtype, steps, spread=3.0, masked=True):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(N + K)
+    x = torch.empty(B, N, K, dtype=dtype, device="cuda")
+    flat = x.view(-1, K)
+    rows = max(1, (1 << 25) // K)
+    for a, b in pieces(B * N, rows):
+        flat[a:b] = torch.randn(b - a, K, generator=g, device="cuda") * spread
+    labels = torch.randint(-1, K, (B, N, S), generator=g, device="cuda", dtype=torch.int32)
+    valid = torch.rand(B, N, generator=g, device="cuda") < 0.85
+    one = B == 1
+    if masked:
+        x[~valid] = math.nan
+    else:
+        valid[:] = True
+    got = km.balance(x[0] if one else x, labels[0] if one else labels, valid=(valid[0] if one else valid) if masked else None)
+    loss, counts, prob, (lse, coef) = got
+    dl = torch.rand(B, generator=g, device="cuda") + N
+    dx = km.balance_grad(x[0] if one else x, (lse, coef), dl).view(-1, K)
+    counts, prob, coef, lse = counts.view(B, K), prob.view(B, K), coef.view(B, K), lse.view(-1)
+    row, col = balance_depths(K, steps)
+    T = valid.sum(1).double()
+    named = torch.where(valid[..., None] & (labels >= 0), labels.long() + torch.arange(B, device="cuda")[:, None, None] * K, B * K)
+    want = torch.bincount(named.view(-1), minlength=B * K + 1)[:-1].view(B, K)
+    assert torch.equal(counts.long(), want)
+    share = want.double() * (K / S) / T[:, None]
+    assert bool(((coef.double() - share / T[:, None]).abs() <= 2 * U * share / T[:, None]).all())
+    total = torch.zeros(B, K, dtype=torch.float64, device="cuda")
+    at = torch.arange(B * N, device="cuda") // N
+    live = valid.view(-1)
+    most = torch.zeros((), dtype=torch.float64, device="cuda")
+    c64 = coef.double()
+    for a, b in pieces(B * N, rows):
+        on = live[a:b]
+        z = torch.where(on[:, None], flat[a:b].double(), 0.0)
+        R = z.amax(-1, keepdim=True) - z.amin(-1, keepdim=True)
+        most = torch.maximum(most, R.max())
+        p = torch.softmax(z, -1) * on[:, None]
+        r = torch.logsumexp(z, -1)
+        assert bool(torch.isposinf(lse[a:b][~on]).all())
+        tol = (R[:, 0] + 4 + row) * U + 3 * U * (r.abs() + math.log(K) + 1)
+        assert bool(((lse[a:b].double() - r).abs() <= tol)[on].all())
+        for q in range(int(at[a]), int(at[b - 1]) + 1):
+            total[q] += p[max(0, q * N - a):(q + 1) * N - a].sum(0)
+        c = c64[at[a:b]]
+        d = dl.double()[at[a:b], None]
+        dot = (p * c).sum(-1, keepdim=True)
+        want = d * p * (c - dot)
+        rel = (2 * R + 8 + row) * U
+        tol = d * p * ((rel + 4 * U) * (c + dot) + (rel + row * U) * dot)
+        tol = tol * 1.01 + half_step(dtype) * (want.abs() + tol) + tiny(dtype) + 2.0 ** -126 * d * (c + dot)
+        out = dx[a:b].double()
+        bad = ~((out - want).abs() <= tol)
+        assert not bool(bad.any()), (a, int(bad.sum()))
+        assert not out[~on].any()
+    prob64 = total / T[:, None]
+    rel = (2 * most + 8 + row + col) * U
+    assert bool(((prob.double() - prob64).abs() <= rel * prob64).all())
+    want = (share * prob64).sum(1)
+    assert bool(((loss.double() - want).abs() <= (rel + U) * want).all())
+
+
+# steps: rows a team takes one after another (chosen so that a ring of 4 turns, a block of 64 folds, several chunks join)
+@pytest.mark.parametrize("masked", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B, N, K, S, steps", [
+    (1, 50003, 1024, 1, 7), (1, 50003, 520, 2, 7), (1, 50003, 1001, 1, 7), (3, 20001, 700, 3, 8), (2, 140001, 250, 2, 18),
+    (1, 1000003, 8, 2, 4), (1, 300007, 100, 2, 10), (1, 9001, 2048, 1, 5), (1, 20001, 3999, 2, 10), (1, 9001, 8192, 1, 9),
+    (1, 5003, 8200, 2, 10), (1, 4001, 12345, 1, 8), (2100, 23, 200, 2, 4), (2100, 131, 129, 1, 17)])
+def test_balance_of_many_steps(km, dtype, B, N, K, S, steps, masked):  # noqa: F811
+    check_balance_on_gpu(km, B, N, K, S, dtype, steps, masked=masked)
+
+
+@pytest.mark.parametrize("B, N, K, S, steps", [(2100, 1201, 100, 1, 76), (2050, 600, 200, 2, 75), (2050, 140, 1000, 1, 35),
+                                               (2050, 290, 601, 2, 73), (1, 600011, 1024, 1, 74), (1, 140003, 2048, 1, 69),
+                                               (1, 70001, 8192, 1, 69), (1, 36007, 12345, 1, 71)])
+def test_balance_of_more_steps_than_a_block(km, B, N, K, S, steps):  # noqa: F811
+    check_balance_on_gpu(km, B, N, K, S, BF16, steps)
+
+
+@pytest.mark.parametrize("masked", [True, False])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B, N, K, S", [(1, 64, 16385, 1), (1, 65, 16392, 2), (3, 129, 20001, 1), (2, 200, 40000, 3),
+                                        (1, 4100, 16389, 1), (1, 1, 1000001, 2), (5, 3, 50257, 1)])
+def test_balance_of_long_rows(km, dtype, B, N, K, S, masked):  # noqa: F811
+    check_balance_on_gpu(km, B, N, K, S, dtype, 0, masked=masked)
