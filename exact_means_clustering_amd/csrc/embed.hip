@@ -721,13 +721,6 @@ hipError_t embed_grad_v(const void* dout, const int32_t* ids, int64_t N, int K, 
 
 }  // namespace
 
-#define FKM_PAIR(FN, WIDTH, ...)                                                  \
-  switch (WIDTH) {                                                                \
-    case 8: return FN<TI, TO, 8>(__VA_ARGS__);                                    \
-    case 4: return FN<TI, TO, 4>(__VA_ARGS__);                                    \
-    default: return FN<TI, TO, 1>(__VA_ARGS__);                                   \
-  }
-
 // f(F32{} | F16{} | BF16{}) for a runtime type
 template <class F>
 static hipError_t with_type(int dt, F&& f) {
@@ -761,7 +754,11 @@ hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* 
     return with_type(gdt, [&](auto to) {
       using TI = decltype(ti);
       using TO = decltype(to);
-      FKM_PAIR(embed_grad_v, w, dout, ids, N, K, D, B, scale, acc, grad, buf, s)
+      if constexpr (TI::SZ == 2) {  // (four fp32 are 16 bytes)
+        if (w == 8) return embed_grad_v<TI, TO, 8>(dout, ids, N, K, D, B, scale, acc, grad, buf, s);
+      }
+      if (w == 4) return embed_grad_v<TI, TO, 4>(dout, ids, N, K, D, B, scale, acc, grad, buf, s);
+      return embed_grad_v<TI, TO, 1>(dout, ids, N, K, D, B, scale, acc, grad, buf, s);
     });
   });
 }
