@@ -2,15 +2,19 @@
 // gradient (formulas in flashkm_codebook.h).  Both are bound by reading the
 // logits (and writing the gradient) once.
 //
-// Rows up to kMaxK choices stay in registers.  A team of LPR lanes, or of W
-// whole waves, holds one row, E elements a lane, loaded 16 bytes at a time.  Forward, a lane owns its columns: after the row's maximum
-// and sum it adds its probabilities to its own column sums (fp32, by blocks of
-// kFold rows and over the lanes of a wave, then fp64), so the probabilities are
-// never written and the logits are read once.  A workgroup covers a chunk of rows of one
-// instance and leaves one partial sum per column (and its counts, from an LDS
-// histogram of integers); a second launch adds the chunks in a fixed order.
-// An instance of one chunk is finished by its own workgroup.  Longer rows
-// take two reads: row statistics, then column sums.
+// Rows up to kBalanceMaxK choices stay in registers.  A team of LPR lanes, or
+// of W whole waves, holds one row, E elements a lane, loaded 16 bytes at a time.
+// Forward, a lane owns its columns: after the row's maximum and sum it adds its
+// probabilities to its own column sums, so the probabilities are never written
+// and the logits are read once.  A column sum is fp32 over blocks of kFold rows,
+// over at most kFold such blocks and over a wave's lanes, and fp64 over the waves
+// of a workgroup (a team of whole waves has none to add).  A workgroup covers a
+// chunk of rows of one instance and leaves one partial sum per column, rounded
+// to fp32 (half the workspace of fp64, for half a step of a sum that already has
+// the roundings above), and its counts, from an LDS histogram of integers; a
+// second launch adds the chunks in fp64 in a fixed order.  An instance of one
+// chunk is finished by its own workgroup.  Longer rows take two reads: row
+// statistics (fp32 over a load, then fp64), then column sums of 64 rows (fp32).
 //
 // Exponentials are taken of differences from a row's maximum (forward) or
 // lse (backward), formed before the scaling by log2(e), so logits of the
@@ -27,8 +31,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kFold = kBalanceFold;
 // Rows in flight per team, forward and backward (1,048,576 x 1,024 bf16:
-// forward 463 us with 1, 443 with 2, 444 with 4; backward with the caches'
-// streaming hints 871 us with 2, 807 with 4).
+// forward 397 us with 1, 396 with 2, 513 with 4; backward 863 us with 2, 806
+// with 4).
 constexpr int kAheadF = 2, kAheadB = 4;
 constexpr int kEarly = 2;  // labels a thread reads ahead of the rows
 
@@ -155,9 +159,10 @@ __device__ __forceinline__ double block_sum_f64(double v, double* tmp) {
 // (W = 1) or W whole waves per row (LPR = 64).  LOOSE: rows that are no multiple
 // of 16 bytes or start anywhere: loads at element alignment, the last one of a
 // row ending with it, its elements that the load before has too left out
-// (65,536 x 5,001 bf16 forward 295 us, 1,048,576 x 100 90 us; with loads of
-// single elements 425 and 95 us; with single elements at a row's end only, whose
-// branches break the ring, 304 and 162 us).
+// (65,536 x 5,001 bf16 forward 295 us, 1,048,576 x 100 75 us.  When they took 295
+// and 90 us, loads of single elements took 425 and 95 us, and single elements at
+// a row's end only, whose branches break the ring, 304 and 162 us).  What it
+// costs: 1,048,576 x 189 159 us, x 192 124 us, with as many lanes idle.
 template <class T, int NV, int LPR, int W, bool LOOSE>
 struct Rows {
   static constexpr int V = 16 / T::SZ;
@@ -224,9 +229,9 @@ struct Rows {
 };
 
 // Bound by the logits' bytes where rows are long (1,048,576 x 1,024 bf16: 2.15
-// GB in 0.41 ms, 5.2 TB/s) and by the vector instructions, about 9 a value,
-// where they are short (8,388,608 x 8: 68 us, 3.5 TB/s).  Waves of 16 values a
-// lane: five per SIMD instead of four, 412 against 432 us.
+// GB in 0.395 ms, 5.4 TB/s) and by the vector instructions, about 9 a value,
+// where they are short (8,388,608 x 8, 2 labels: 60 us, 3.9 TB/s).  Waves of 16
+// values a lane: five per SIMD instead of four, 396 against 411 us.
 template <class T, int NV, int LPR, int W, bool LOOSE>
 __global__ __launch_bounds__((Rows<T, NV, LPR, W, LOOSE>::BLOCK),
                              (W == 1 && Rows<T, NV, LPR, W, LOOSE>::E == 16 && !LOOSE ? 5 : 1))
@@ -402,8 +407,8 @@ template <int CB>
 __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part, int64_t chunks,
                                                             const int32_t* cpart, int64_t cchunks,
                                                             const int32_t* __restrict__ vpart, int64_t vchunks,
-                                                            uint32_t K, int S, int kblocks, int64_t units, BalanceOut out,
-                                                            double* __restrict__ terms) {
+                                                            uint32_t K, int S, int kblocks, int64_t units,
+                                                            BalanceOut out, double* __restrict__ terms) {
   constexpr int G = 1024 / CB;
   __shared__ double sp[1024];
   __shared__ int sc[1024];
@@ -713,7 +718,8 @@ __global__ __launch_bounds__(256) void balance_grad_wide_kernel(const typename T
       const float inv = 1.f / t.x;
       mean = t.y * inv, scale = dloss[b] * inv;
     }
-    // the row again (from the cache) for the gradient
+    // the row again for the gradient (from the cache only while the rows of all
+    // resident workgroups fit it: 8,192 x 65,536 bf16 1,181 us)
     over_row<T, V>(logits + i * K, K, [&](const float (&x)[V], uint32_t k) {
       float o[V];
 #pragma unroll
@@ -750,8 +756,8 @@ void join_launch(const JoinIn& in, int K, int S, int B, const BalanceOut& out, d
 }
 hipError_t join(const JoinIn& in, int K, int S, int B, const BalanceOut& out, double* terms, hipStream_t s) {
   // one workgroup per instance while it reads little, else 32 columns each and
-  // a launch for the loss (8 x 4,095 x 128: 12.9 us in all, 15.4 by 32 columns;
-  // 16,384 x 1,024: 109 us with one workgroup, 26.4 by 32 columns)
+  // a launch for the loss (8 x 4,095 x 128: 10.9 us in all, 13.4 by 32 columns;
+  // 16,384 x 1,024: 109 us with one workgroup, 25.1 by 32 columns)
   const bool one = K <= 1024 && in.chunks * K <= 65536;
   if (K <= 32 || !one) join_launch<kBalanceJoinCols>(in, K, S, B, out, terms, s);
   else if (K <= 64) join_launch<64>(in, K, S, B, out, terms, s);
@@ -788,8 +794,8 @@ hipError_t rows_backward(const void* logits, int64_t N, int K, int B, const floa
   return hipGetLastError();
 }
 
-// f(Team) with the smallest team that holds a row of K elements, A loads of
-// 16 bytes making 8 elements.
+// f(Team) with the smallest team that holds a row of K elements; A loads of 16
+// bytes make 8 elements, and a lane holds 8, or 16 where a team takes 2 A loads.
 template <int NV_, int LPR_, int W_, bool LOOSE_>
 struct Team {
   static constexpr int NV = NV_, LPR = LPR_, W = W_;
@@ -843,7 +849,8 @@ hipError_t balance_t(const void* logits, int64_t N, int K, int B, const int32_t*
       using P = decltype(team);
       return rows_forward<T, P::NV, P::LPR, P::W, P::LOOSE>(logits, N, K, B, labels, S, valid, lse, out, buf, s);
     };
-    return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go) : with_team<8 / VEC, true>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go)
+                                                                  : with_team<8 / VEC, true>(K, go);
   }
   return vec_width(K, VEC, logits, T::SZ, logits, T::SZ) == VEC
              ? wide_forward<T, VEC>(logits, N, K, B, labels, S, valid, lse, out, buf, s)
@@ -859,7 +866,8 @@ hipError_t balance_grad_t(const void* logits, int64_t N, int K, int B, const flo
       using P = decltype(team);
       return rows_backward<T, P::NV, P::LPR, P::W, P::LOOSE>(logits, N, K, B, lse, coef, dloss, dlogits, s);
     };
-    return vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go) : with_team<8 / VEC, true>(K, go);
+    return vec_width(K, VEC, logits, T::SZ, dlogits, T::SZ) == VEC ? with_team<8 / VEC, false>(K, go)
+                                                                   : with_team<8 / VEC, true>(K, go);
   }
   const int64_t n = N * B;
   const dim3 grid((unsigned)capped(n));

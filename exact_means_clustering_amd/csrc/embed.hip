@@ -34,7 +34,7 @@ constexpr int kTileVecs = 256 * kVecs;    // vectors per workgroup tile
 // LOOSE: rows that are no multiple of 16 bytes or start anywhere.  Vectors have
 // element alignment, a row's last one ends with it, and of that one only the
 // elements that the one before does not have are stored (65,536 rows of 2,049
-// bf16: 102 us; element by element 288 us).
+// bf16: 95 us, of 2,048 53; element by element 288 us).
 template <class TI, class TO, int V, bool LOOSE>
 __global__ __launch_bounds__(256) void embed_kernel(const typename TI::raw* __restrict__ table,
                                                     const int32_t* __restrict__ ids, int64_t n, uint32_t N, uint32_t K,
@@ -160,10 +160,11 @@ __device__ __forceinline__ void zero_entries(typename TO::raw* __restrict__ grad
   }
 }
 
-// Few rows (n <= kGradDirect, 256): no sort (256 rows of 1,024 bf16 into
-// 32,000 fp32: 29 us either way, bound by the zeros; accumulated, without
-// zeros: 8.3 us so, 16.3 us sorted by one workgroup).  A wave takes row i and a slab of 64
-// vectors; if no earlier row has its id, it adds every row of that id in
+// Few rows (n <= kGradDirect, 256): no sort (256 rows of 1,024 bf16 accumulated
+// into 32,000 fp32: 7.4 us so, 16.3 us sorted by one workgroup; with the zeros of
+// a fresh gradient, which bound it, 29 us either way at 1,024 columns in one
+// buffer, and at 2,048 columns 58 us for 256 rows so, 45 us for 257 sorted).  A
+// wave takes row i and a slab of 64 vectors; if no earlier row has its id, it adds every row of that id in
 // order.  Further workgroups zero the entries that no row names, each
 // looking for its own range of entries among the ids.
 template <class TI, class TO, int V>
@@ -521,13 +522,15 @@ int64_t sum_launch(const void* dout, const uint2* kv, int64_t n, uint32_t mark, 
 }
 
 // Up to kSortOne rows, where a word holds key and row: 16,384 rows of 2,048
-// bf16 into 32,000 fp32 in 73 us against 106 us with the sort's own launches
-// and zeros by binary search; 4,099 rows accumulated into 131,072 in 36.5
-// against 52 us.  One workgroup argsorts the ids in LDS (stable radix
-// passes of 8 or 9 bits over 32-bit words: key, out-of-range bit, row), and the
-// other workgroups of the launch meanwhile zero the gradient.  Ranks as in
-// the sort of many rows: digit matches inside a wave, a counter per wave and
-// digit, waves in row order.
+// bf16 into 32,000 fp32 in 75 us (86 us when each call has another buffer),
+// 16,385 rows with the sort's own launches and zeros by binary search in 104 us;
+// 4,099 rows of 1,024 accumulated into 131,072 in 36.5 against 52 us when the
+// limit was chosen (now 32).  Against it: 16,384 rows of 16 into 1,000 take 49 us
+// so, 16,385 take 42.  One workgroup argsorts the ids in LDS (stable radix passes
+// of 8 or 9 bits over 32-bit words: key, out-of-range bit, row), and the other
+// workgroups of the launch meanwhile zero the gradient.  Ranks as in the sort of
+// many rows: digit matches inside a wave, a counter per wave and digit, waves in
+// row order.
 constexpr int kSortWaves = 16;
 // R: rounds of 64 keys per wave (the keys stay in registers); RB: digit bits
 // (9 where that saves a pass, as for keys of 17 and 18 bits: 36.5 to 33.4 us for

@@ -238,15 +238,19 @@ hipError_t launch_embed(int tdt, int odt, const void* table, const int32_t* ids,
 // Its gradient: grad[k] = (acc ? grad[k] : 0) + scale * (sum of the rows i of dout with key k = b * K + ids[i]).
 // The rows of the sorted order are summed by units of U rows and slabs of columns; pieces of an entry's segment that
 // cross a unit's edge go to fragments, two per unit, which are joined kJoin units at a time.
-constexpr int64_t kGradDirect = 256;  // up to this many rows the gradient needs no sort
-constexpr int kSortOne = 16384;       // up to this many rows are sorted by one workgroup, where a word holds them
+// Up to kGradDirect rows the gradient needs no sort (one key per thread of a workgroup; accumulated into 131,072 x
+// 1,024 fp32, 256 rows 7.9 us, 257 rows 18.6); up to kSortOne rows, the most that its LDS and registers hold, one
+// workgroup sorts them where a word holds key and row.
+constexpr int64_t kGradDirect = 256;
+constexpr int kSortOne = 16384;
 constexpr int kSlack = 32;             // readable pairs that the gradient's sort buffers have past the last row
 constexpr int kJoin = 256;            // units joined by one workgroup (16 waves of 16)
 // Rows per unit for n rows of D columns: 16 to 256, so that the waves (of 512 columns) number about 8,192 (16,384 rows
-// of 2,048: 16 rows a unit 106 us, 32 or 64 rows 115 us, both before the one-workgroup sort; 2^23 rows of 128: 128,
+// of 2,048: 16 rows a unit 106 us, 32 or 64 rows 115 us, all before the one-workgroup sort; 2^23 rows of 128: 128,
 // 256 and 512 rows a unit 0.545, 0.543 and 0.550 ms).
 inline int grad_unit(int64_t n, int D) {
-  const int64_t slabs = (D + 511) / 512, per = D <= 256 ? 512 / (D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256) : 1;
+  const int64_t slabs = (D + 511) / 512;
+  const int64_t per = D <= 256 ? 512 / (D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256) : 1;
   int u = 16;
   while (u < 256 && n * slabs / per / u > 8192) u *= 2;
   return u;
@@ -268,7 +272,8 @@ hipError_t launch_embed_grad(int idt, int gdt, const void* dout, const int32_t* 
                              float scale, bool acc, void* grad, GradBuffers& buf, hipStream_t s);
 
 // Balance loss and its gradient (see flashkm_codebook.h for the formulas).
-// Longest rows kept in registers (32,768 x 16,384 bf16 forward: 387 us so, 773 us by the two reads of longer rows).
+// Longest rows kept in registers (32,768 x 16,384 bf16 forward 392 us so; x 16,392, by the two reads of longer rows,
+// 767).
 constexpr int kBalanceMaxK = 16384;
 constexpr int kBalanceJoinCols = 32;  // fewest columns per workgroup that joins chunk sums
 constexpr int kBalanceFold = 64;      // rows of a block of a column sum, and the most blocks of one
@@ -280,9 +285,9 @@ constexpr int balance_step(int K) {
   while (lpr < 64 && lpr * 8 < K) lpr *= 2;
   return K > 1024 ? 1 : 4 * (64 / lpr);
 }
-// Steps per workgroup and chunks (workgroups) per instance of N rows: about 2,048 workgroups (1,048,576 x 256 bf16 131
-// us; 136 with 4,096, 148 with 1,024), each of 4 steps at least (8 x 4,095 x 128 fp16 12.9 us; 13.1 with 2, 18.0 with 8;
-// 16,384 x 1,024 bf16 26.4, 34.6 and 21.9 us).
+// Steps per workgroup and chunks (workgroups) per instance of N rows: about 2,048 workgroups (1,048,576 x 256 bf16 128
+// us; 135 with 4,096, 147 with 1,024), each of 4 steps at least (8 x 4,095 x 128 fp16 10.9 us; 11.9 with 2, 14.4 with
+// 8; 16,384 x 1,024 bf16 25.1, 34.4 and 21.6 us; the gradient of the first 8.2, 8.5 and 9.3 us).
 struct BalanceSplit {
   int steps;
   int64_t chunks;

@@ -8,8 +8,12 @@ namespace fkm {
 // fp32 -> storage, rounded to nearest even once (infinities and NaN kept).
 template <class T> __device__ __forceinline__ typename T::raw round_to(float f);
 template <> __device__ __forceinline__ float round_to<F32>(float f) { return f; }
-template <> __device__ __forceinline__ uint16_t round_to<F16>(float f) { return __builtin_bit_cast(uint16_t, (_Float16)f); }
-template <> __device__ __forceinline__ uint16_t round_to<BF16>(float f) { return __builtin_bit_cast(uint16_t, (__bf16)f); }
+template <> __device__ __forceinline__ uint16_t round_to<F16>(float f) {
+  return __builtin_bit_cast(uint16_t, (_Float16)f);
+}
+template <> __device__ __forceinline__ uint16_t round_to<BF16>(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
 
 // The 16-bit types' -infinity.
 template <class T> constexpr uint32_t neg_inf_bits() { return 0; }
@@ -154,7 +158,7 @@ template <class T, int V> struct Pack {
 // addresses must be aligned to the smaller of 16 bytes and the vector's size.
 // `most` is 16 bytes of what is streamed past the caches: a lane that moves
 // two 16-byte words of it makes every access of the wave touch half of each
-// 32 bytes (949,595 fp32 rows of 128 looked up: 210 us with 8, 82 with 4).
+// 32 bytes (949,595 fp32 rows of 128 looked up: 210 us with 8, 81 with 4).
 inline int vec_width(int D, int most, const void* a, int a_size, const void* b, int b_size) {
   for (int v : {8, 4}) {
     if (v > most) continue;
