@@ -90,10 +90,12 @@ KM_API int kmeans_balance(const void* logits, int32_t dtype, int64_t N, int32_t 
  * coef of kmeans_balance and the derivative dloss [B] fp32 of what follows:
  *   p              = softmax(logits[b,i,:])
  *   dlogits[b,i,:] = dloss[b] * p * (coef[b,:] - sum_k p_k coef[b,k])
- * rounded once into dtype.  lse only says which rows have probabilities: rows
- * with lse +inf (invalid) or -inf (nothing left) get zeros, whatever their
- * logits hold; a row with lse NaN gets NaN.  (p is taken from the logits again, since an fp32 lse of large
- * magnitude does not hold the logarithm of the sum.) */
+ * rounded once into dtype.  lse says which rows have probabilities: rows with
+ * lse +inf (invalid) or -inf (nothing left) get zeros, whatever their logits
+ * hold; a row with lse NaN gets NaN.  For the others it is only the shift of the
+ * exponentials, whose sum is taken from the logits again (an fp32 lse of large
+ * magnitude does not hold the logarithm of the sum): a value near the row's log
+ * sum exp gives the same p, one far from it overflows or leaves nothing. */
 KM_API int kmeans_balance_grad(const void* logits, int32_t dtype, int64_t N, int32_t K, int32_t B,
                                const float* lse, const float* coef, const float* dloss, void* dlogits, void* stream);
 
