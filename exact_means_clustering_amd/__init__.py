@@ -1,8 +1,8 @@
 """Exact Lloyd k-means on MI355X (gfx950): Python binding of libflashkm.so.
 
 The functions below only marshal torch tensors into the C ABI declared in
-``include/flashkm.h`` and ``include/flashkm_codebook.h`` (same names without the ``kmeans_`` prefix): every step
-of the computation runs in the library's HIP kernels, on the current torch
+``include/flashkm.h``, ``include/flashkm_codebook.h`` and ``include/flashkm_train.h`` (same names without the
+``kmeans_`` prefix): every step of the computation runs in the library's HIP kernels, on the current torch
 stream.  PyTorch provides device memory and streams, nothing else.  There is
 no CPU fallback: importing raises if the library is missing, and every call
 raises ``KMeansError`` on a non-zero status.
@@ -23,7 +23,7 @@ import torch
 __all__ = ["KMeansError", "lib_path", "workspace_bytes", "assign", "assign_top2", "assign_soft", "gauss_sum", "seed", "update",
            "fit", "fit_streamed", "tune", "tune_save", "tune_load", "assign_configs", "assign_noalloc",
            "stream_timeline", "embed", "embed_grad", "embed_grad_workspace_bytes", "balance", "balance_grad",
-           "balance_workspace_bytes", "DTYPES"]
+           "balance_workspace_bytes", "route", "route_grad", "adamw_states", "adamw_plan", "adamw", "AdamWPlan", "DTYPES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_NAME = "libflashkm.so"
@@ -92,6 +92,19 @@ def _load(path=None):
     lib.kmeans_balance.restype = ctypes.c_int
     lib.kmeans_balance_grad.argtypes = [P, i32, i64, i32, i32, P, P, P, P, P]
     lib.kmeans_balance_grad.restype = ctypes.c_int
+    f64 = ctypes.c_double
+    lib.kmeans_route.argtypes = [P, i32, i64, i32, P, i32, i32, i32, i32, i32, i32, f32, P, P, P, P, P]
+    lib.kmeans_route.restype = ctypes.c_int
+    lib.kmeans_route_grad.argtypes = [P, i32, i64, i32, P, P, P, i32, i32, i32, f32, i32, P, P]
+    lib.kmeans_route_grad.restype = ctypes.c_int
+    lib.kmeans_adamw_chunks.argtypes = [P, i32]
+    lib.kmeans_adamw_chunks.restype = i64
+    lib.kmeans_adamw_table_bytes.argtypes = [P, i32]
+    lib.kmeans_adamw_table_bytes.restype = sz
+    lib.kmeans_adamw_table.argtypes = [P, i32, i32, i32, i32, P, sz]
+    lib.kmeans_adamw_table.restype = ctypes.c_int
+    lib.kmeans_adamw.argtypes = [P, i32, i64, i32, i32, i32, i32, f64, f64, f64, f64, f64, i64, P, P, P, P, P]
+    lib.kmeans_adamw.restype = ctypes.c_int
     lib.kmeans_last_error.argtypes = []
     lib.kmeans_last_error.restype = ctypes.c_char_p
     return lib
@@ -629,3 +642,235 @@ def balance_grad(logits, saved, dloss, *, out=None):
     _check(_lib.kmeans_balance_grad(logits.data_ptr(), dt, N, K, B, lse.data_ptr(), coef.data_ptr(), dloss.data_ptr(),
                                     out.data_ptr(), _current(logits)))
     return out
+
+
+# ---- training operators (include/flashkm_train.h) ---------------------------------
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    try:
+        return _SCORES[score]
+    except (KeyError, TypeError):
+        raise KMeansError(KM_EUNSUPPORTED, f"unknown score {score!r} (softmax or sigmoid)") from None
+
+
+@_on_stream
+def route(logits, S: int, *, score: str = "softmax", bias=None, groups: int = 1, top_groups=None, group_best: int = 2,
+          renormalise: bool = True, scale: float = 1.0, valid=None):
+    """Routing of rows to S of K choices: logits [.., N, K]; scores by ``score`` ("softmax" or "sigmoid"); bias [K] fp32 or
+    None is added for the selection alone; with ``groups`` > 1 only the top_groups groups of the largest worth (the sum
+    of their group_best largest biased scores) take part; valid [.., N] bool or None.  Returns (ids int32, weights fp32,
+    chosen logits fp32), [.., N, S] each: ids in the order of the biased scores, ties to the lowest index, -1 (weight 0,
+    chosen -inf) where no choice is left; weights scale * score, divided by their row's sum if ``renormalise``.  ids are
+    labels for balance; chosen is what route_grad needs.  Runs on ``stream`` (default: the current one)."""
+    dt, _, _, K = _logits(logits)
+    S = _int32(S, "S")
+    lead = logits.shape[:-1]
+    if bias is not None:
+        _into(bias, "bias", (K,), torch.float32, logits)
+    if valid is not None:
+        _into(valid, "valid", lead, torch.bool, logits)
+    if not 1 <= S <= 64:  # (no outputs of a size that the call refuses)
+        raise KMeansError(KM_EINVAL if S < 1 else KM_EUNSUPPORTED, f"S={S} must be 1 to 64")
+    shape = (*lead, S)
+    ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
+    weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    chosen = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    groups = _int32(groups, "groups")
+    _check(_lib.kmeans_route(logits.data_ptr(), dt, lead.numel(), K, _at(bias), _score(score), groups,
+                             groups if top_groups is None else _int32(top_groups, "top_groups"),
+                             _int32(group_best, "group_best"), S, int(bool(renormalise)), float(scale), _at(valid),
+                             ids.data_ptr(), weights.data_ptr(), chosen.data_ptr(), _current(logits)))
+    return ids, weights, chosen
+
+
+@_on_stream
+def route_grad(logits, ids, chosen, dweights, *, score: str = "softmax", renormalise: bool = True, scale: float = 1.0,
+               out=None, accumulate: bool = False):
+    """Gradient of route's weights with respect to the logits, the ids held fixed: ids and chosen of route, dweights
+    [.., N, S] fp32 the derivative of what follows, the other arguments as in route.  Returns dlogits, of the logits'
+    shape and type; accumulate adds to ``out`` (for instance balance_grad's gradient) and leaves the entries that the
+    gradient does not reach untouched.  Runs on ``stream`` (default: the current one)."""
+    dt, _, _, K = _logits(logits)
+    lead = logits.shape[:-1]
+    _need(ids, "ids", torch.int32, like=logits)
+    if ids.dim() != logits.dim() or ids.shape[:-1] != lead:
+        raise KMeansError(KM_EINVAL, f"ids must be {tuple(lead)} + (S,) (got {tuple(ids.shape)})")
+    _into(chosen, "chosen", ids.shape, torch.float32, logits)
+    _into(dweights, "dweights", ids.shape, torch.float32, logits)
+    if out is None:
+        if accumulate:
+            raise KMeansError(KM_EINVAL, "accumulate needs out")
+        out = torch.empty_like(logits)
+    else:
+        _into(out, "out", logits.shape, logits.dtype, logits)
+    _check(_lib.kmeans_route_grad(logits.data_ptr(), dt, lead.numel(), K, ids.data_ptr(), chosen.data_ptr(),
+                                  dweights.data_ptr(), _int32(ids.shape[-1], "S"), _score(score),
+                                  int(bool(renormalise)), float(scale), int(bool(accumulate)), out.data_ptr(),
+                                  _current(logits)))
+    return out
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("decay", ctypes.c_float)]
+
+
+ADAMW_BLOCK = 256  # elements of an 8-bit state that share a scale
+
+
+def adamw_states(params, bits: int = 32):
+    """Zero states for the tensors ``params``: (exp_avg, exp_avg_sq, scales).  In 32 bits two lists of fp32 tensors of the
+    parameters' shapes and None; in 8 bits lists of float8_e4m3fn and float8_e5m2 tensors and the pair of lists of their
+    fp32 scales, one for each 256 consecutive elements (a state's value is code * scale)."""
+    if bits == 32:
+        return ([torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format) for p in params],
+                [torch.zeros_like(p, dtype=torch.float32, memory_format=torch.contiguous_format) for p in params], None)
+    if bits != 8:
+        raise KMeansError(KM_EUNSUPPORTED, f"unsupported bits={bits} (32 or 8)")
+    zero = lambda p, dt: torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(dt)  # noqa: E731
+    scale = lambda p: torch.zeros(-(-p.numel() // ADAMW_BLOCK), dtype=torch.float32, device=p.device)  # noqa: E731
+    return ([zero(p, torch.float8_e4m3fn) for p in params], [zero(p, torch.float8_e5m2) for p in params],
+            ([scale(p) for p in params], [scale(p) for p in params]))
+
+
+class AdamWPlan:
+    """The tensors of adamw calls, checked and laid out once (made by adamw_plan): it keeps them alive, and holds as long
+    as their memory stays in place."""
+
+    def __init__(self, groups, device, stream, tensors):
+        self._groups, self.device, self._stream, self._tensors = groups, device, stream, tensors
+
+
+def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None, decay=None):
+    """Lay out the tensors of AdamW steps: lists of one length of contiguous CUDA tensors on one device.  params and grads
+    of any of the three types (they may be mixed; each pair of types is a launch of its own), exp_avg and exp_avg_sq
+    fp32, or float8_e4m3fn and float8_e5m2 with ``scales`` (two lists of fp32 tensors, see adamw_states); masters: a list
+    of fp32 copies of the parameters on which the step is taken, with None for those without (and for fp32 parameters),
+    or None; decay: a factor of weight_decay for each tensor, or None (1)."""
+    params = list(params)
+    n = len(params)
+    if n == 0:
+        raise KMeansError(KM_EINVAL, "params must not be empty")
+    lists = {"grads": list(grads), "exp_avg": list(exp_avg), "exp_avg_sq": list(exp_avg_sq),
+             "masters": [None] * n if masters is None else list(masters),
+             "decay": [1.0] * n if decay is None else [float(d) for d in decay]}
+    if scales is not None:
+        lists["scales[0]"], lists["scales[1]"] = list(scales[0]), list(scales[1])
+    for name, v in lists.items():
+        if len(v) != n:
+            raise KMeansError(KM_EINVAL, f"{name} must have {n} entries (got {len(v)})")
+    bits = 32 if scales is None else 8
+    kinds = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+    groups = {}
+    for i, p in enumerate(params):
+        g, m, v, w = (lists[k][i] for k in ("grads", "exp_avg", "exp_avg_sq", "masters"))
+        _need(p, f"params[{i}]", like=params[0])
+        _into(g, f"grads[{i}]", p.shape, g.dtype if isinstance(g, torch.Tensor) else None, params[0])
+        _into(m, f"exp_avg[{i}]", p.shape, kinds[0], params[0])
+        _into(v, f"exp_avg_sq[{i}]", p.shape, kinds[1], params[0])
+        t = _AdamWTensor(p.data_ptr(), g.data_ptr(), None, m.data_ptr(), v.data_ptr(), None, None, p.numel(),
+                         lists["decay"][i])
+        if w is not None:
+            _into(w, f"masters[{i}]", p.shape, torch.float32, params[0])
+            t.master = w.data_ptr()
+        if bits == 8:
+            a, b = lists["scales[0]"][i], lists["scales[1]"][i]
+            for k, x in enumerate((a, b)):
+                _into(x, f"scales[{k}][{i}]", (-(-p.numel() // ADAMW_BLOCK),), torch.float32, params[0])
+            t.exp_avg_scale, t.exp_avg_sq_scale = a.data_ptr(), b.data_ptr()
+        if p.numel():
+            groups.setdefault((_dtype(p), _dtype(g), w is not None), []).append(t)
+        else:
+            _dtype(p), _dtype(g)
+    made = []
+    everything = [t for ts in groups.values() for t in ts]
+    device = params[0].device
+    with torch.cuda.device(device):
+        for (pdt, gdt, has), ts in groups.items():
+            array = (_AdamWTensor * len(ts))(*ts)
+            need = int(_lib.kmeans_adamw_table_bytes(array, len(ts)))
+            if need == 0:
+                _check(KM_EINVAL)
+            chunks = int(_lib.kmeans_adamw_chunks(array, len(ts)))
+            host = torch.zeros(need, dtype=torch.uint8)
+            _check(_lib.kmeans_adamw_table(array, len(ts), pdt, gdt, bits, host.data_ptr(), need))
+            made.append((host.to(device), len(ts), chunks, pdt, gdt, bits, int(has)))
+        if len(groups) > 1:  # nothing may overlap across the launches either
+            _across(groups, bits)
+        stream = _raw_stream(device.index)
+    return AdamWPlan(made, device, stream, (params, lists, everything))
+
+
+def _across(groups, bits):
+    """Refuse arrays that a step writes where another group's tensors lie."""
+    size = {0: 4, 1: 2, 2: 2}
+    ranges = []
+    for key, ts in groups.items():
+        for t in ts:
+            n, state = t.numel, 4 if bits == 32 else 1
+            scale = -(-n // ADAMW_BLOCK) * 4
+            for name, at, nbytes, out in (("param", t.param, n * size[key[0]], True),
+                                          ("grad", t.grad, n * size[key[1]], False),
+                                          ("master", t.master, n * 4, True), ("exp_avg", t.exp_avg, n * state, True),
+                                          ("exp_avg_sq", t.exp_avg_sq, n * state, True),
+                                          ("exp_avg_scale", t.exp_avg_scale, scale, True),
+                                          ("exp_avg_sq_scale", t.exp_avg_sq_scale, scale, True)):
+                if at:
+                    ranges.append((at, at + nbytes, name, out))
+    ranges.sort()
+    reach = {False: (0, ""), True: (0, "")}  # the furthest end of everything, and of what is written
+    for a, b, name, out in ranges:
+        end, other = reach[not out]
+        if a < end:
+            raise KMeansError(KM_EINVAL, f"{name} overlaps {other} of another tensor")
+        reach[False] = max(reach[False], (b, name))
+        if out:
+            reach[True] = max(reach[True], (b, name))
+
+
+def _scalar_at(t, name, dtype, device):
+    """A device scalar of a call, or None."""
+    if not isinstance(t, torch.Tensor):
+        return None
+    _need(t, name, dtype)
+    if t.numel() != 1 or t.device != device:
+        raise KMeansError(KM_EINVAL, f"{name} must be one value on {device}")
+    return t.data_ptr()
+
+
+def adamw(plan: AdamWPlan, *, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
+          grad_scale=None, skip=None, stream=None):
+    """One AdamW step over the plan's tensors, in place:
+    m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2, p = p (1 - lr weight_decay) - lr mhat / (sqrt(vhat) + eps), with
+    g = grad_scale * grad and mhat, vhat without the bias of a zero start after ``step`` steps (the first is 1).  lr may
+    be an fp32 CUDA tensor and step an int64 one, of one value, which are read on the device (for captured calls);
+    grad_scale is None or an fp32 CUDA tensor; skip is None or a bool or uint8 CUDA tensor: nothing changes where it is
+    true.  Runs on ``stream`` (default: the current one)."""
+    if not isinstance(plan, AdamWPlan):
+        raise KMeansError(KM_EINVAL, "plan must be made by adamw_plan")
+    device = plan.device
+    if stream is not None and stream.device != device:
+        raise KMeansError(KM_EINVAL, f"stream is on {stream.device}, the tensors on {device}")
+    lr_at = _scalar_at(lr, "lr", torch.float32, device)
+    step_at = _scalar_at(step, "step", torch.int64, device)
+    if grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
+        raise KMeansError(KM_EINVAL, "grad_scale must be a CUDA tensor")
+    scale_at = _scalar_at(grad_scale, "grad_scale", torch.float32, device)
+    if skip is not None and (not isinstance(skip, torch.Tensor) or skip.dtype not in (torch.bool, torch.uint8)):
+        raise KMeansError(KM_EINVAL, "skip must be a bool or uint8 CUDA tensor")
+    skip_at = _scalar_at(skip, "skip", skip.dtype if skip is not None else None, device)
+    with torch.cuda.device(device):
+        raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
+        if raw != plan._stream:  # the table must outlive the step there
+            on = stream if stream is not None else torch.cuda.current_stream()
+            for group in plan._groups:
+                group[0].record_stream(on)
+        for table, count, chunks, pdt, gdt, bits, masters in plan._groups:
+            _check(_lib.kmeans_adamw(table.data_ptr(), count, chunks, pdt, gdt, bits, masters,
+                                     0.0 if lr_at else float(lr), float(betas[0]), float(betas[1]), float(eps),
+                                     float(weight_decay), 1 if step_at else int(step), lr_at, step_at, scale_at,
+                                     skip_at, raw))

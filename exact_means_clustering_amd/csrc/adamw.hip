@@ -1,0 +1,271 @@
+// AdamW step over the tensors of a table (formulas in flashkm_train.h).
+//
+// Bound by bytes: a value's parameter, gradient and two states are read once and all but the gradient written once (28
+// bytes with fp32 everywhere, 20 in bf16 with fp32 copies and states in 8 bits).  A workgroup takes a chunk of 4,096
+// values of one tensor, a lane four neighbours at a time, so every access is up to 16 bytes a lane and a wave's four
+// times 64 values are one block of a scale: its largest magnitude is a reduction over the wave's lanes.
+#include "kernels.h"
+#include "teams.h"
+#include "vecio.h"
+
+namespace fkm {
+
+namespace {
+
+// What a step's values share.
+struct Rates {
+  float b1, c1, b2, c2;  // the betas and 1 - beta
+  float eps, lr_wd, rate, root;  // lr * weight_decay, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+};
+struct Live {  // what is read on the device, where it is there
+  const float* lr;
+  const int64_t* step;
+  const float* gscale;
+  const uint8_t* skip;
+  double lr_, b1, b2, wd;
+  int64_t step_;
+};
+
+__host__ __device__ inline void set_step(Rates& r, double lr, double b1, double b2, double wd, int64_t step) {
+  r.lr_wd = (float)(lr * wd);
+  r.rate = (float)(lr / (1.0 - pow(b1, (double)step)));
+  r.root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)step)));
+}
+
+// A state's value in 8 bits: a format's conversions, its code for a block's largest magnitude (a power of two), and the
+// least code of a positive value.
+struct E4M3 {
+  static constexpr float kTop = 256.f, kLeast = 0.f;
+  __device__ static uint32_t pack(const float (&y)[4]) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+  }
+  __device__ static void unpack(uint32_t w, float (&y)[4]) {
+    const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
+    y[0] = a[0], y[1] = a[1], y[2] = b[0], y[3] = b[1];
+  }
+};
+struct E5M2 {
+  static constexpr float kTop = 32768.f, kLeast = 0x1p-16f;
+  __device__ static uint32_t pack(const float (&y)[4]) {
+    int w = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], w, true);
+  }
+  __device__ static void unpack(uint32_t w, float (&y)[4]) {
+    const auto a = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, true);
+    y[0] = a[0], y[1] = a[1], y[2] = b[0], y[3] = b[1];
+  }
+};
+
+// Codes of a wave's 256 values and their scale (in every lane).
+template <class Q>
+__device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) {
+  float high = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float f = fabsf(x[e]);
+    high = f < INFINITY && f > high ? f : high;  // (a NaN or an infinity leaves the others' scale alone)
+  }
+  high = team_max<64>(high);
+  const float inv = high >= 0x1p-100f ? Q::kTop / high : 0.f;
+  scale = inv != 0.f ? high * (1.f / Q::kTop) : 0.f;
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e] = x[e] * inv;
+    if (Q::kLeast > 0.f && inv != 0.f && x[e] > 0.f && y[e] < Q::kLeast) y[e] = Q::kLeast;
+  }
+  return Q::pack(y);
+}
+
+// The sums and products of m and v are rounded one by one, as the formula has them: what is held in 8 bits then does
+// not depend on which of them a compiler joins.
+template <class TP, class TG, bool MASTER, int BITS>
+__global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ table, int64_t map_at, int64_t chunks,
+                                                    Rates r, Live live) {
+#pragma clang fp contract(off)
+  constexpr int U = kAdamChunk / 1024;  // groups of four values a lane
+  constexpr bool Q8 = BITS == 8;
+  if (live.skip && *live.skip) return;
+  if (live.step || live.lr) {
+    __shared__ Rates shared;
+    if (threadIdx.x == 0) {
+      shared = r;
+      set_step(shared, live.lr ? (double)*live.lr : live.lr_, live.b1, live.b2, live.wd,
+               live.step ? *live.step : live.step_);
+    }
+    __syncthreads();
+    r = shared;
+  }
+  const float gscale = live.gscale ? *live.gscale : 1.f;
+  const int32_t* map = reinterpret_cast<const int32_t*>(table + map_at);
+  for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const AdamItem t = reinterpret_cast<const AdamItem*>(table)[map[c]];
+    auto* p = static_cast<typename TP::raw*>(t.p);
+    auto* g = static_cast<const typename TG::raw*>(t.g);
+    const int64_t base = (c - t.first) * kAdamChunk;
+    const float keep = 1.f - r.lr_wd * t.decay;
+    auto at = [&](int u) { return base + u * 1024 + (int64_t)threadIdx.x * 4; };
+    // the lane's group u: values p, g, m, v in, and p, m, v out
+    auto step = [&](float (&pv)[4], const float (&gv)[4], float (&mv)[4], float (&vv)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float gr = gv[e] * gscale;
+        mv[e] = mv[e] * r.b1 + gr * r.c1;
+        vv[e] = vv[e] * r.b2 + (gr * gr) * r.c2;
+        const float d = sqrtf(vv[e]) * r.root + r.eps;
+        // 0 / 0 only where eps is 0 and nothing has moved
+        const float q = mv[e] == 0.f && d == 0.f ? 0.f : mv[e] / d;
+        pv[e] = pv[e] * keep - q * r.rate;
+      }
+    };
+    if (t.aligned && base + kAdamChunk <= t.numel) {  // uniform over the workgroup
+      Pack<TP, 4> pp[U];
+      Pack<F32, 4> pm[U], m[U], v[U];
+      Pack<TG, 4> gg[U];
+      uint32_t mq[U], vq[U];
+      float sm[U], sv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = at(u);
+        if constexpr (MASTER) pm[u].load(t.master + i);
+        else pp[u].load(p + i);
+        gg[u].load(g + i);
+        if constexpr (Q8) {
+          mq[u] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i);
+          vq[u] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i);
+          sm[u] = t.sm[i / kAdamBlock], sv[u] = t.sv[i / kAdamBlock];
+        } else {
+          m[u].load(static_cast<const float*>(t.m) + i);
+          v[u].load(static_cast<const float*>(t.v) + i);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = at(u);
+        float pv[4], gv[4], mv[4], vv[4];
+        if constexpr (MASTER) pm[u].unpack(pv);
+        else pp[u].unpack(pv);
+        gg[u].unpack(gv);
+        if constexpr (Q8) {
+          E4M3::unpack(mq[u], mv);
+          E5M2::unpack(vq[u], vv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mv[e] *= sm[u], vv[e] *= sv[u];
+        } else {
+          m[u].unpack(mv);
+          v[u].unpack(vv);
+        }
+        step(pv, gv, mv, vv);
+        pp[u].pack(pv);
+        pp[u].store(p + i);
+        if constexpr (MASTER) {
+          pm[u].pack(pv);
+          pm[u].store(t.master + i);
+        }
+        if constexpr (Q8) {
+          float a, b;
+          const uint32_t ma = to_codes<E4M3>(mv, a), va = to_codes<E5M2>(vv, b);
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i) = ma;
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i) = va;
+          if (i % kAdamBlock == 0) t.sm[i / kAdamBlock] = a, t.sv[i / kAdamBlock] = b;
+        } else {
+          m[u].pack(mv);
+          v[u].pack(vv);
+          m[u].store(static_cast<float*>(t.m) + i);
+          v[u].store(static_cast<float*>(t.v) + i);
+        }
+      }
+    } else {
+      // a tensor's end, or arrays at odd addresses: element by element
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = at(u);
+        float pv[4] = {}, gv[4] = {}, mv[4] = {}, vv[4] = {};
+        uint32_t mq = 0, vq = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (i + e >= t.numel) continue;
+          pv[e] = MASTER ? t.master[i + e] : TP::to_f32(p[i + e]);
+          gv[e] = TG::to_f32(g[i + e]);
+          if constexpr (Q8) {
+            mq |= (uint32_t) static_cast<const uint8_t*>(t.m)[i + e] << 8 * e;
+            vq |= (uint32_t) static_cast<const uint8_t*>(t.v)[i + e] << 8 * e;
+          } else {
+            mv[e] = static_cast<const float*>(t.m)[i + e];
+            vv[e] = static_cast<const float*>(t.v)[i + e];
+          }
+        }
+        if constexpr (Q8) {
+          E4M3::unpack(mq, mv);
+          E5M2::unpack(vq, vv);
+          const float a = i < t.numel ? t.sm[i / kAdamBlock] : 0.f, b = i < t.numel ? t.sv[i / kAdamBlock] : 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mv[e] *= a, vv[e] *= b;
+        }
+        step(pv, gv, mv, vv);
+        if constexpr (Q8) {
+          float a, b;
+          mq = to_codes<E4M3>(mv, a), vq = to_codes<E5M2>(vv, b);  // all lanes of the wave take part
+          if (i % kAdamBlock == 0 && i < t.numel) t.sm[i / kAdamBlock] = a, t.sv[i / kAdamBlock] = b;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (i + e >= t.numel) continue;
+          p[i + e] = round_to<TP>(pv[e]);
+          if constexpr (MASTER) t.master[i + e] = pv[e];
+          if constexpr (Q8) {
+            static_cast<uint8_t*>(t.m)[i + e] = (uint8_t)(mq >> 8 * e);
+            static_cast<uint8_t*>(t.v)[i + e] = (uint8_t)(vq >> 8 * e);
+          } else {
+            static_cast<float*>(t.m)[i + e] = mv[e];
+            static_cast<float*>(t.v)[i + e] = vv[e];
+          }
+        }
+      }
+    }
+  }
+}
+
+template <class TP, class TG, bool MASTER>
+hipError_t adamw_t(const AdamCall& c, hipStream_t s) {
+  Rates r{(float)c.b1, (float)(1.0 - c.b1), (float)c.b2, (float)(1.0 - c.b2), (float)c.eps, 0.f, 0.f, 0.f};
+  set_step(r, c.lr, c.b1, c.b2, c.wd, c.step_at ? 1 : c.step);
+  const Live live{c.lr_at, c.step_at, c.gscale_at, c.skip_at, c.lr, c.b1, c.b2, c.wd, c.step};
+  const int64_t grid = c.chunks < (1 << 22) ? c.chunks : (1 << 22);
+  const auto* table = static_cast<const char*>(c.table);
+  const int64_t map_at = (int64_t)adam_map_at(c.count);
+  if (c.bits == 8)
+    adamw_kernel<TP, TG, MASTER, 8><<<dim3((unsigned)grid), dim3(256), 0, s>>>(table, map_at, c.chunks, r, live);
+  else
+    adamw_kernel<TP, TG, MASTER, 32><<<dim3((unsigned)grid), dim3(256), 0, s>>>(table, map_at, c.chunks, r, live);
+  return hipGetLastError();
+}
+template <class TP>
+hipError_t adamw_g(int gdt, const AdamCall& c, hipStream_t s) {
+  auto go = [&](auto tg) {
+    using TG = decltype(tg);
+    if constexpr (TP::SZ == 2) {
+      if (c.masters) return adamw_t<TP, TG, true>(c, s);
+    }
+    return adamw_t<TP, TG, false>(c, s);
+  };
+  switch (gdt) {
+    case DT_F32: return go(F32{});
+    case DT_F16: return go(F16{});
+    case DT_BF16: return go(BF16{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(int pdt, int gdt, const AdamCall& c, hipStream_t s) {
+  switch (pdt) {
+    case DT_F32: return adamw_g<F32>(gdt, c, s);
+    case DT_F16: return adamw_g<F16>(gdt, c, s);
+    case DT_BF16: return adamw_g<BF16>(gdt, c, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace fkm

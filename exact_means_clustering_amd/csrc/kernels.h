@@ -315,4 +315,64 @@ hipError_t launch_balance(int dt, const void* logits, int64_t N, int K, int B, c
 hipError_t launch_balance_grad(int dt, const void* logits, int64_t N, int K, int B, const float* lse,
                                const float* coef, const float* dloss, void* dlogits, hipStream_t s);
 
+// ---- training operators (formulas in flashkm_train.h) ------------------------------
+struct RouteCall {
+  const void* logits;
+  int64_t n;
+  int K;
+  const float* bias;
+  int softmax, groups, keep, best, S, renorm;
+  float scale;
+  const uint8_t* valid;
+  int32_t* ids;
+  float* weights;
+  float* chosen;
+};
+hipError_t launch_route(int dt, const RouteCall& c, hipStream_t s);
+
+struct RouteGradCall {
+  const void* logits;
+  int64_t n;
+  int K;
+  const int32_t* ids;
+  const float* chosen;
+  const float* dweights;
+  int S, softmax, renorm;
+  float scale;
+  int accumulate;
+  void* dlogits;
+};
+hipError_t launch_route_grad(int dt, const RouteGradCall& c, hipStream_t s);
+
+// One tensor in the table of an AdamW step.  Its elements are the chunks first, first + 1, ... of kAdamChunk each.
+struct AdamItem {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  float* sm;
+  float* sv;
+  int64_t numel;
+  int64_t first;
+  float decay;
+  uint32_t aligned;  // every array may be moved four elements at a time
+};
+constexpr int kAdamChunk = 4096;  // elements per workgroup: 16 blocks of 256
+constexpr int kAdamBlock = 256;   // elements that share a scale
+// The table: the items, then (256-byte aligned) the item of each chunk.
+inline size_t adam_map_at(int64_t count) { return ((size_t)count * sizeof(AdamItem) + 255) & ~(size_t)255; }
+struct AdamCall {
+  const void* table;
+  int64_t count, chunks;
+  int bits, masters;
+  double lr, b1, b2, eps, wd;
+  int64_t step;
+  const float* lr_at;
+  const int64_t* step_at;
+  const float* gscale_at;
+  const uint8_t* skip_at;
+};
+hipError_t launch_adamw(int pdt, int gdt, const AdamCall& c, hipStream_t s);
+
 }  // namespace fkm
