@@ -36,18 +36,6 @@ constexpr int kFold = kBalanceFold;
 constexpr int kAheadF = 2, kAheadB = 4;
 constexpr int kEarly = 2;  // labels a thread reads ahead of the rows
 
-// Maximum of E values, two at a time (fmaxf would first canonicalise each value
-// unpacked from a word: one instruction more per value).  A NaN may win or lose:
-// the row's exponentials are NaN either way.
-template <int E>
-__device__ __forceinline__ float max_of(const float (&x)[E]) {
-  static_assert(E % 2 == 0, "pairs");
-  float m = x[0];
-  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(x[0]), "v"(x[1]));
-#pragma unroll
-  for (int e = 2; e < E; e += 2) asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(m), "v"(x[e]), "v"(x[e + 1]));
-  return m;
-}
 // v summed over the 64 / LPR lanes of a wave that are LPR apart, in every one of
 // them (rotations within 16 lanes, then swaps of 16 and 32).
 template <int LPR>

@@ -64,7 +64,7 @@ __device__ __forceinline__ void wave_top2(double& m1, double& m2) {
 // One row by one wave, scores in 64 bits.  Selection after selection, the next choice in the order of (score, index) is
 // looked for over the whole row, whose scores are computed again each time: no storage, any K.
 template <class T>
-__device__ void route_row_exact(const RouteArgs<T>& a, int64_t row) {
+__device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row) {
   const int lane = lane_id();
   const typename T::raw* x = a.logits + row * a.K;
   const bool valid = !a.valid || a.valid[row];

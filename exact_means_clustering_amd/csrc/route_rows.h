@@ -1,0 +1,525 @@
+// Routing of rows whose K choices a team of lanes holds in registers (internal).
+//
+// A key is the 64-bit pattern (score, index), made so that the order of the patterns, read as doubles, is the order of
+// the selection: the score's own 32 bits on top, and below them the index, inverted for scores that are not negative, so
+// that of equal scores the lower index is the larger key.  The patterns are finite doubles whatever the scores (a NaN's
+// row is found before), so v_max_f64 and v_min_f64, full-rate here, are a compare-exchange of two instructions that
+// carries the index along and is exact.  A lane sorts its keys eight (or L) at a time, keeps the largest L, and the
+// lists of a team's lanes are joined by bitonic merges: after log2(LPR) steps every lane holds the row's L largest keys in
+// order.
+//
+// Where c's order is the logits' own, a key's score is the logit.  Else it is c in 32 bits, and a bound of its error says
+// whether rounding could have changed the selection: a neighbour in the order, a choice next to the last one, or a group
+// next to the last one that is closer than the two errors, unless the two have the same logit and bias (their order is the
+// index's then).  Such rows, about one in a thousand on random scores, are decided again in 64 bits.
+#pragma once
+
+#include "route.h"
+
+namespace fkm {
+
+__device__ __forceinline__ double key_of(float score, uint32_t col) {
+  const uint32_t hi = __float_as_uint(score + 0.f);  // (-0 is 0)
+  const uint32_t lo = ~(col ^ (uint32_t)((int32_t)hi >> 31));
+  return __hiloint2double((int)hi, (int)lo);
+}
+__device__ __forceinline__ float key_score(double k) { return __int_as_float(__double2hiint(k)); }
+__device__ __forceinline__ uint32_t key_col(double k) {
+  return ~((uint32_t)__double2loint(k) ^ (uint32_t)(__double2hiint(k) >> 31));
+}
+
+// a >= b afterwards
+__device__ __forceinline__ void exchange(double& a, double& b) {
+  const double h = __builtin_fmax(a, b), l = __builtin_fmin(a, b);
+  a = h, b = l;
+}
+// Odd-even merge sort, descending.
+template <int L>
+__device__ __forceinline__ void sort_keys(double (&a)[L]) {
+#pragma unroll
+  for (int p = 1; p < L; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < L; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < L && (i + j) / (2 * p) == (i + j + k) / (2 * p)) exchange(a[i + j], a[i + j + k]);
+}
+// The L largest of two descending lists, descending.
+template <int L>
+__device__ __forceinline__ void merge_keys(double (&a)[L], const double (&b)[L]) {
+#pragma unroll
+  for (int i = 0; i < L; ++i) a[i] = __builtin_fmax(a[i], b[L - 1 - i]);
+#pragma unroll
+  for (int h = L / 2; h >= 1; h /= 2)
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (!(i & h)) exchange(a[i], a[i + h]);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const int lo = __double2loint(v), hi = __double2hiint(v);
+  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, true));
+}
+template <int L, int CTRL>
+__device__ __forceinline__ void merge_dpp(double (&a)[L]) {
+  double b[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) b[i] = dpp64<CTRL>(a[i]);
+  merge_keys<L>(a, b);
+}
+template <int L, bool FAR>
+__device__ __forceinline__ void merge_swap(double (&a)[L]) {  // lanes 16 (or 32) apart
+  double b[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const uint32_t lo = (uint32_t)__double2loint(a[i]), hi = (uint32_t)__double2hiint(a[i]);
+    const auto l = FAR ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
+                       : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+    const auto h = FAR ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
+                       : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    a[i] = __hiloint2double((int)h[0], (int)l[0]);
+    b[i] = __hiloint2double((int)h[1], (int)l[1]);
+  }
+  merge_keys<L>(a, b);
+}
+// The L largest keys of a team's lists, in every lane.
+template <int L, int LPR>
+__device__ __forceinline__ void join_lists(double (&a)[L]) {
+  if constexpr (LPR >= 2) merge_dpp<L, 0xB1>(a);
+  if constexpr (LPR >= 4) merge_dpp<L, 0x4E>(a);
+  if constexpr (LPR >= 8) merge_dpp<L, 0x141>(a);
+  if constexpr (LPR >= 16) merge_dpp<L, 0x140>(a);
+  if constexpr (LPR >= 32) merge_swap<L, false>(a);
+  if constexpr (LPR >= 64) merge_swap<L, true>(a);
+}
+
+// The part of a row (K choices, LPR * E at most) that a team's lanes hold: load j of lane g takes V columns from
+// (j LPR + g) V on, 16 bytes; -inf where there are none.  Rows that are no multiple of 16 bytes or start anywhere (loose)
+// are loaded at element alignment, their last few elements one by one.
+template <class T, int E, int LPR>
+struct Slice {
+  static constexpr int V = 16 / T::SZ, NV = E / V;
+  Pack<T, V> p[NV];
+  static __device__ __forceinline__ int first(int j, int g) { return j * LPR * V + g * V; }
+  __device__ __forceinline__ void load(const typename T::raw* row, int K, int g, bool loose, bool live) {
+    if (!loose) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        p[j].fill_neg_inf();
+        if (live && first(j, g) < K) p[j].load_nt(row + first(j, g));
+      }
+    } else {
+      // one load of the row, j = tail of one lane, has fewer than V elements
+      const int tail = K / (LPR * V), left = K % V;
+      Pack<T, V> last;
+      last.fill_neg_inf();
+      const bool mine = live && left && first(tail, g) + left == K;
+      if (mine) last.load_head(row + (K - left), left);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        p[j].fill_neg_inf();
+        if (live && first(j, g) + V <= K) p[j].load_loose(row + first(j, g));
+        if (mine && j == tail) p[j] = last;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[E]) const {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      float f[V];
+      p[j].unpack(f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j * V + v] = f[v];
+    }
+  }
+  // whether an element is NaN
+  __device__ __forceinline__ bool has_nan() const {
+    if constexpr (T::SZ == 2) {
+      typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+      u16x2 m = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, p[j].w[i] & 0x7FFF7FFFu));
+      const uint32_t inf = neg_inf_bits<T>() & 0x7FFFu;
+      return m[0] > inf || m[1] > inf;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = max(m, p[j].w[i] & 0x7FFFFFFFu);
+      return m > 0x7F800000u;
+    }
+  }
+};
+
+// The list's L largest joined with those of a lane's E values, the first of which has index `col`.
+template <class T, int E, int LPR, int L>
+__device__ __forceinline__ void add_keys(double (&top)[L], const float (&x)[E], int col, bool fresh) {
+  using Sl = Slice<T, E, LPR>;
+  static_assert(E % L == 0, "whole lists");
+#pragma unroll
+  for (int e0 = 0; e0 < E; e0 += L) {
+    double k[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) k[i] = key_of(x[e0 + i], col + Sl::first((e0 + i) / Sl::V, 0) + (e0 + i) % Sl::V);
+    sort_keys<L>(k);
+    if (fresh && e0 == 0) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) top[i] = k[i];
+    } else {
+      merge_keys<L>(top, k);
+    }
+  }
+}
+
+// Sum of a lane's values, pair by pair.
+template <int E>
+__device__ __forceinline__ float pair_sum(const float (&x)[E]) {
+  float s[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) s[e] = x[e];
+#pragma unroll
+  for (int h = E / 2; h >= 1; h /= 2)
+#pragma unroll
+    for (int e = 0; e < h; ++e) s[e] += s[e + h];
+  return s[0];
+}
+
+constexpr float kU = 0x1p-24f;
+// Bounds of the error of c in 32 bits.  A probability p = exp(t) / sum: (|t| + 3) u for the exponential, 18 u for the
+// sum of such (5 levels in a lane, 6 across, its terms' own), 3 u for the quotient; a sigmoid: 7 u; c itself u.
+// (2^-120: what is flushed below the normal range.)
+__device__ __forceinline__ float soft_error(float p, float t, float c) {
+  return kU * (p * (28.f + fabsf(t)) + fabsf(c)) + 0x1p-120f;
+}
+__device__ __forceinline__ float sigmoid_error(float c) { return kU * (8.f + fabsf(c)); }
+
+// One wave's LDS, in floats, for rows of K choices taken SL at a time.
+struct RouteLds {
+  int scores, worth, sel, z, e, info, flag, total;
+  static __host__ __device__ RouteLds of(int SL, int K, int G, int S) {
+    RouteLds o{};
+    int at = 0;
+    o.scores = at, at += G > 1 ? SL * ((K + 3) & ~3) : 0;  // (16-byte words: first)
+    o.sel = at, at += 2 * SL * S;              // keys
+    o.worth = at, at += G > 1 ? 2 * SL * G : 0;  // and its error
+    o.z = at, at += SL * S;                    // chosen logits, and their shares before the division
+    o.e = at, at += SL * S;
+    o.info = at, at += 2 * SL;                 // a row's largest logit, 1 / sum of exponentials
+    o.flag = at, at += SL;                     // a row to be decided in 64 bits
+    o.total = (at + 3) & ~3;
+    return o;
+  }
+};
+
+// What a kernel is made for: rows of K <= LPR * E choices whose order is the logits' own; the same of any K, taken
+// LPR * E at a time; and rows of K <= LPR * E with scores, a bias or groups.
+enum RouteMode { kPlain, kWide, kScored };
+constexpr int32_t kUnsure = INT32_MIN;  // an id that waits to be decided in 64 bits
+
+template <class T, int E, int LPR, int L, RouteMode MODE>
+__global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic) {
+  using Sl = Slice<T, E, LPR>;
+  constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR;
+  extern __shared__ __align__(16) float lds_all[];
+  const int lane = lane_id(), g = lane % LPR, slot = lane / LPR;
+  float* lds = lds_all + (threadIdx.x >> 6) * o.total;
+  double* sel = reinterpret_cast<double*>(lds + o.sel);
+  float *zs = lds + o.z, *es = lds + o.e, *info = lds + o.info;
+  int* flag = reinterpret_cast<int*>(lds + o.flag);
+  const bool arith = MODE == kScored && a.arith();
+  const bool sums = a.softmax && (arith || !a.renorm);
+  const int S = a.S;
+  const int64_t waves = (int64_t)gridDim.x * (blockDim.x >> 6);
+  const int64_t tiles = (a.n + SL - 1) / SL;
+  const uint64_t team = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (slot * LPR);
+
+  // the bias, with zeros where there is none, for all of the workgroup's waves
+  const float* bias = lds_all + (blockDim.x >> 6) * o.total;
+  bool bias_nan = false;
+  if constexpr (MODE == kScored) {
+    float* b = lds_all + (blockDim.x >> 6) * o.total;
+    int nan = 0;
+    for (int k = threadIdx.x; k < LPR * E; k += blockDim.x) {
+      b[k] = a.bias && k < a.K ? a.bias[k] : 0.f;
+      nan |= is_nan_bits(b[k]);
+    }
+    bias_nan = __syncthreads_or(nan);
+  }
+
+  Sl next;
+  bool next_live = false;
+  auto fetch = [&](int64_t t) {
+    const int64_t row = t * SL + slot;
+    next_live = t < tiles && row < a.n && (!a.valid || a.valid[row]);
+    if constexpr (MODE != kWide) next.load(a.logits + row * a.K, a.K, g, loose, next_live);
+  };
+  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+  const int64_t t0 = t;
+  bool again = false;
+  if constexpr (MODE == kPlain) fetch(t);
+  for (; t < tiles; t += waves) {
+    const int64_t row0 = t * SL, row = row0 + slot;
+    if constexpr (MODE != kPlain) fetch(t);
+    const Sl now = next;
+    const bool live = next_live;
+    if constexpr (MODE == kPlain) fetch(t + waves);
+    double top[L];
+    float high = -INFINITY, inv = 0.f;
+    bool bad = false;
+    if constexpr (MODE == kWide) {
+      float sum = 0.f;
+      for (int64_t off = 0; off < a.K; off += LPR * E) {
+        const int left = a.K - off < LPR * E ? (int)(a.K - off) : LPR * E;
+        Sl s;
+        s.load(a.logits + row * a.K + off, left, g, loose, live);
+        bad |= s.has_nan();
+        float x[E];
+        s.values(x);
+        if (sums) {
+          const float m = fmaxf(high, max_of(x));
+          const float shift = m == -INFINITY ? 0.f : m;
+          float e[E];
+#pragma unroll
+          for (int i = 0; i < E; ++i) e[i] = exp_diff<F32>(x[i], shift);
+          sum = fmaf(sum, high == -INFINITY ? 0.f : exp_diff<F32>(high, shift), pair_sum(e));
+          high = m;
+        }
+        add_keys<T, E, LPR, L>(top, x, (int)off + g * V, off == 0);
+      }
+      if (sums) {
+        const float m = team_max<LPR>(high);
+        sum = team_sum<LPR>(high == -INFINITY ? 0.f : sum * exp_diff<F32>(high, m));
+        high = m, inv = 1.f / sum;
+      }
+      bad = (__ballot(bad) & team) != 0;
+      join_lists<L, LPR>(top);
+    } else {
+      bad = now.has_nan();
+      float x[E];
+      now.values(x);
+      if (sums) {
+        high = team_max<LPR>(max_of(x));
+        const float shift = high == -INFINITY ? 0.f : high;
+        float e[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) e[i] = exp_diff<F32>(x[i], shift);
+        inv = 1.f / team_sum<LPR>(pair_sum(e));
+        if constexpr (MODE == kScored) {
+          if (arith) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) x[i] = x[i] == -INFINITY ? x[i] : fmaf(e[i], inv, bias[Sl::first(i / V, g) + i % V]);
+          }
+        }
+      }
+      if constexpr (MODE == kPlain) {
+        add_keys<T, E, LPR, L>(top, x, g * V, true);
+        join_lists<L, LPR>(top);
+        bad = (__ballot(bad) & team) != 0;
+      } else {
+        int unsure = 0;
+        if (arith && !a.softmax) {
+#pragma unroll
+          for (int i = 0; i < E; ++i)
+            x[i] = x[i] == -INFINITY
+                       ? x[i]
+                       : __builtin_amdgcn_rcpf(1.f + exp_to(-x[i])) + bias[Sl::first(i / V, g) + i % V];
+        }
+        bad |= bias_nan;
+        bad = live && (__ballot(bad) & team) != 0;
+        const float base = a.softmax ? 28.f * inv : 8.f;  // (|t| + 28) exp(t) is at most 28
+        if (a.G > 1) {
+          // the scores change hands: lanes add up groups, and put those that go out of reach
+          const int stride = (a.K + 3) & ~3, gs = a.K / a.G;
+          float* mine = lds + o.scores + slot * stride;
+          float *worth = lds + o.worth, *werr = worth + SL * a.G;
+          wave_sync();  // (the tile before is done with it)
+          if (g == 0) info[2 * slot] = base;
+          if (lane < SL) flag[lane] = 0;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < V; q += 4) {
+              const int c = Sl::first(j, g) + q;  // (a row's last words may run into its padding)
+              if (c < a.K)
+                *reinterpret_cast<float4*>(mine + c) =
+                    make_float4(x[j * V + q], x[j * V + q + 1], x[j * V + q + 2], x[j * V + q + 3]);
+            }
+          wave_sync();
+          for (int it = lane; it < SL * a.G; it += 64) {
+            const int r = it / a.G, gr = it - r * a.G;
+            const float* p = lds + o.scores + r * stride + gr * gs;
+            float m1 = -INFINITY, m2 = -INFINITY;
+            int k = it % gs;  // (lanes start at different places: banks)
+            for (int i = 0; i < gs; ++i) {
+              const float c = p[k];
+              m2 = fmaxf(m2, fminf(m1, c));
+              m1 = fmaxf(m1, c);
+              k = k + 1 < gs ? k + 1 : 0;
+            }
+            const bool two = a.best == 2 && m2 > -INFINITY;
+            worth[it] = two ? m1 + m2 : m1;
+            werr[it] = arith && m1 > -INFINITY
+                           ? kU * (2.f * info[2 * r] + 3.f * (fabsf(m1) + (two ? fabsf(m2) : 0.f))) + 0x1p-120f
+                           : 0.f;
+          }
+          wave_sync();
+          for (int it = lane; it < SL * a.G; it += 64) {
+            const int r = it / a.G, gr = it - r * a.G;
+            const float w = worth[it];
+            int better = 0;
+            float err = 0.f, gap = INFINITY;  // the largest error, and the distance to the next group down
+            for (int q = 0; q < a.G; ++q) {
+              const float other = worth[r * a.G + q];
+              const bool b = other > w || (other == w && q < gr);
+              better += b;
+              err = fmaxf(err, werr[r * a.G + q]);
+              if (!b && q != gr) gap = fminf(gap, w - other);
+            }
+            // the last group that stays and the first that goes (worths of two groups without choices are not compared)
+            if (arith && better == a.keep - 1 && w > -INFINITY && gap <= 2.2f * err) flag[r] = 1;
+            if (better >= a.keep) {
+              float* p = lds + o.scores + r * stride + gr * gs;
+              int k = it % gs;
+              for (int i = 0; i < gs; ++i) {
+                p[k] = -INFINITY;
+                k = k + 1 < gs ? k + 1 : 0;
+              }
+            }
+          }
+          wave_sync();
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int q = 0; q < V; q += 4) {
+              const int c = Sl::first(j, g) + q;
+              if (c < a.K) {
+                const float4 f = *reinterpret_cast<const float4*>(mine + c);
+                x[j * V + q] = f.x, x[j * V + q + 1] = f.y, x[j * V + q + 2] = f.z, x[j * V + q + 3] = f.w;
+              }
+            }
+          unsure = flag[slot];
+        }
+        add_keys<T, E, LPR, L>(top, x, g * V, true);
+        join_lists<L, LPR>(top);
+        if (arith) {
+          // choices that are not selected and no further from the last one than rounding goes
+          double last = top[0];
+#pragma unroll
+          for (int i = 1; i < L; ++i) last = i == S - 1 ? top[i] : last;
+          const float vs = key_score(last);
+          const float border = vs - 2.2f * (kU * (base + fabsf(vs)) + 0x1p-120f);
+          int count = 0;
+#pragma unroll
+          for (int i = 0; i < E; ++i) count += x[i] >= border;
+          count = (int)team_sum<LPR>((float)count);
+          if (vs > -INFINITY && count > S && live && !bad) {
+            // all of them with the last one's logit and bias: the index decides
+            const float zl = T::to_f32(a.logits[row * a.K + key_col(last)]);
+            const float bl = bias[key_col(last)];
+            for (int k = g; k < a.K; k += LPR) {
+              const float f = T::to_f32(a.logits[row * a.K + k]), b = bias[k];
+              if (f == zl && b == bl) continue;
+              const float c = f == -INFINITY ? f
+                              : a.softmax    ? fmaf(exp_diff<F32>(f, high), inv, b)
+                                             : __builtin_amdgcn_rcpf(1.f + exp_to(-f)) + b;
+              // (a group that is out of reach holds -inf in LDS)
+              const bool out = a.G > 1 && lds[o.scores + slot * ((a.K + 3) & ~3) + k] == -INFINITY;
+              if (!out && c >= border && key_of(c, k) < last) unsure = 1;
+            }
+          }
+          unsure = (__ballot(unsure) & team) != 0;
+        }
+        wave_sync();
+        if (g == 0) flag[slot] = arith && unsure && live && !bad;
+      }
+    }
+    if (a.softmax && (arith ? high : key_score(top[0])) == INFINITY) bad = true;
+    // ---- the selections change hands: item it is selection it % S of row it / S
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (i < S && g == i % LPR) sel[slot * S + i] = bad ? __hiloint2double(0x7FC00000, 0) : top[i];
+    if (g == 0) info[2 * slot] = high, info[2 * slot + 1] = inv;
+    wave_sync();
+    const int items = (int)(a.n - row0 < SL ? a.n - row0 : SL) * S;
+    for (int it = lane; it < items; it += 64) {
+      const int r = (int)(((uint32_t)it * magic) >> 16);
+      const double k = sel[it];
+      float z = key_score(k);
+      if (arith && z > -INFINITY && !is_nan_bits(z)) z = T::to_f32(a.logits[(row0 + r) * a.K + key_col(k)]);
+      zs[it] = z;
+    }
+    wave_sync();
+    if (arith) {
+      for (int it = lane; it < items; it += 64) {
+        const int r = (int)(((uint32_t)it * magic) >> 16);
+        if (it + 1 >= (r + 1) * S) continue;
+        const double k = sel[it], k1 = sel[it + 1];
+        const float c = key_score(k), c1 = key_score(k1), z = zs[it], z1 = zs[it + 1];
+        if (is_nan_bits(c) || !(c1 > -INFINITY)) continue;
+        float err;
+        if (a.softmax) {
+          const float m = info[2 * r], pi = info[2 * r + 1];
+          err = soft_error(exp_diff<F32>(z, m) * pi, z - m, c) + soft_error(exp_diff<F32>(z1, m) * pi, z1 - m, c1);
+        } else {
+          err = sigmoid_error(c) + sigmoid_error(c1);
+        }
+        if (c - c1 <= 1.1f * err && (z != z1 || bias[key_col(k)] != bias[key_col(k1)])) flag[r] = 1;
+      }
+      wave_sync();
+    }
+    if (a.renorm) {
+      for (int it = lane; it < items; it += 64) {
+        const int r = (int)(((uint32_t)it * magic) >> 16);
+        float m = -INFINITY;
+        for (int j = 0; j < S; ++j) m = fmaxf(m, zs[r * S + j]);
+        es[it] = zs[it] == -INFINITY ? 0.f : share_term(zs[it], share_shift(m, a.softmax), a.softmax);
+      }
+      wave_sync();
+    }
+    for (int it = lane; it < items; it += 64) {
+      const int r = (int)(((uint32_t)it * magic) >> 16);
+      const double k = sel[it];
+      const float z = zs[it];
+      const bool nan = is_nan_bits(z);
+      const bool out = nan || !(key_score(k) > -INFINITY);
+      float w;
+      if (a.renorm) {
+        float sum = 0.f;
+        for (int j = 0; j < S; ++j) sum += es[r * S + j];
+        w = a.scale * (es[it] / sum);
+      } else {
+        w = a.scale * (a.softmax ? exp_diff<F32>(z, info[2 * r]) * info[2 * r + 1] : 1.f / (1.f + exp_to(-z)));
+      }
+      const int64_t at = row0 * S + it;
+      if (arith && flag[r]) {  // left for the end of the launch
+        a.ids[at] = kUnsure;
+        again = true;
+        continue;
+      }
+      a.ids[at] = out ? -1 : (int32_t)key_col(k);
+      a.weights[at] = nan ? __uint_as_float(0x7FC00000u) : out ? 0.f : w;
+      a.chosen[at] = nan ? __uint_as_float(0x7FC00000u) : out ? -INFINITY : z;
+    }
+  }
+  if constexpr (MODE == kScored) {
+    if (!__ballot(again)) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the marks that this wave's lanes have written
+    for (int64_t t = t0; t < tiles; t += waves) {
+      uint64_t rows = __ballot(lane < SL && t * SL + lane < a.n && a.ids[(t * SL + lane) * S] == kUnsure);
+      while (rows) {
+        route_row_exact(a, t * SL + __builtin_ctzll(rows));
+        rows &= rows - 1;
+      }
+    }
+  }
+}
+
+}  // namespace fkm

@@ -51,6 +51,18 @@ __device__ __forceinline__ float team_op(float v, Op op) {
   }
   return v;
 }
+// Maximum of E values, two at a time (fmaxf would first canonicalise each value
+// unpacked from a word: one instruction more per value).  A NaN may win or lose:
+// the row's exponentials are NaN either way.
+template <int E>
+__device__ __forceinline__ float max_of(const float (&x)[E]) {
+  static_assert(E % 2 == 0, "pairs");
+  float m = x[0];
+  asm("v_max_f32 %0, %1, %2" : "=v"(m) : "v"(x[0]), "v"(x[1]));
+#pragma unroll
+  for (int e = 2; e < E; e += 2) asm("v_max3_f32 %0, %1, %2, %3" : "=v"(m) : "v"(m), "v"(x[e]), "v"(x[e + 1]));
+  return m;
+}
 template <int LPR>
 __device__ __forceinline__ float team_max(float v) {
   return team_op<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
