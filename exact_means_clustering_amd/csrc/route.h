@@ -49,23 +49,79 @@ __device__ __forceinline__ float share_term(float z, float shift, bool softmax) 
   return z > 0.f ? 1.f / (1.f + exp_to(-z)) : e / (1.f + exp_to(z));
 }
 
-// The largest two of the values of all lanes of a wave, m1 >= m2, in every lane.
+// A double as the halves that lane exchanges move.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const int lo = __double2loint(v), hi = __double2hiint(v);
+  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, true),
+                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, true));
+}
+// The values of the two lanes that are 16 (or FAR: 32) apart, in both of them.
+template <bool FAR>
+__device__ __forceinline__ void swap32(uint32_t v, uint32_t& a, uint32_t& b) {
+  const auto p = FAR ? __builtin_amdgcn_permlane32_swap(v, v, false, false)
+                     : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  a = p[0], b = p[1];
+}
+template <bool FAR>
+__device__ __forceinline__ void swap64(double v, double& a, double& b) {
+  uint32_t la, lb, ha, hb;
+  swap32<FAR>((uint32_t)__double2loint(v), la, lb);
+  swap32<FAR>((uint32_t)__double2hiint(v), ha, hb);
+  a = __hiloint2double((int)ha, (int)la), b = __hiloint2double((int)hb, (int)lb);
+}
+// Reductions over the 64 lanes of a wave, in every lane.
+template <class Op>
+__device__ __forceinline__ double wave_op(double v, Op op) {
+  v = op(v, dpp64<0xB1>(v));
+  v = op(v, dpp64<0x4E>(v));
+  v = op(v, dpp64<0x141>(v));
+  v = op(v, dpp64<0x140>(v));
+  double a, b;
+  swap64<false>(v, a, b);
+  v = op(a, b);
+  swap64<true>(v, a, b);
+  return op(a, b);
+}
+__device__ __forceinline__ double wave_max(double v) {
+  return wave_op(v, [](double a, double b) { return a < b ? b : a; });
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  auto d = [](uint32_t a, uint32_t b) { return a < b ? a : b; };
+  v = d(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0xB1, 0xF, 0xF, true));
+  v = d(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x4E, 0xF, 0xF, true));
+  v = d(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x141, 0xF, 0xF, true));
+  v = d(v, (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x140, 0xF, 0xF, true));
+  uint32_t a, b;
+  swap32<false>(v, a, b);
+  v = d(a, b);
+  swap32<true>(v, a, b);
+  return d(a, b);
+}
+
+// A value into the largest two, m1 >= m2.
+__device__ __forceinline__ void take2(double& m1, double& m2, double c) {
+  const double low = c < m1 ? c : m1;
+  m1 = c < m1 ? m1 : c;
+  m2 = m2 < low ? low : m2;
+}
+// The largest two of the values of all lanes of a wave, in every lane.
 __device__ __forceinline__ void wave_top2(double& m1, double& m2) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
     const double a = __shfl_xor(m1, o), b = __shfl_xor(m2, o);
-    const double low = m1 < a ? m1 : a;
-    m1 = m1 < a ? a : m1;
-    m2 = m2 < b ? b : m2;
-    m2 = m2 < low ? low : m2;
+    take2(m1, m2, a);
+    m2 = m2 < b ? b : m2;  // (b <= a)
   }
 }
 
 // One row by one wave, scores in 64 bits.  Selection after selection, the next choice in the order of (score, index) is
-// looked for over the whole row, whose scores are computed again each time: no storage, any K.
-template <class T>
-__device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row) {
+// looked for over the whole row.  HELD: the K scores stay in the wave's LDS (c); else they are computed again each time,
+// for rows of any length.
+template <class T, bool HELD>
+__device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row, double* c) {
   const int lane = lane_id();
+  const uint32_t K = a.K;
   const typename T::raw* x = a.logits + row * a.K;
   const bool valid = !a.valid || a.valid[row];
   const bool arith = a.arith();
@@ -74,11 +130,15 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
   float total = 0.f;    // softmax: the sum of exp(logit - top)
   float top = -INFINITY;
   bool bad = false;
+  auto logit = [&](uint32_t k) { return HELD ? c[k] : (double)T::to_f32(x[k]); };
   if (valid) {
-    for (int64_t k = lane; k < a.K; k += 64) {
+    if constexpr (HELD) wave_sync();
+#pragma unroll 4
+    for (uint32_t k = lane; k < K; k += 64) {
       const float f = T::to_f32(x[k]);
       bad |= is_nan_bits(f) || (a.bias && is_nan_bits(a.bias[k]));
       top = fmaxf(top, f);
+      if constexpr (HELD) c[k] = (double)f;
     }
     top = team_max<64>(top);
     bad = __ballot(bad) != 0 || (a.softmax && top == INFINITY);
@@ -86,31 +146,48 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
   if (valid && !bad && top > -INFINITY) {
     double sum = 0.0;
     if (a.softmax && (arith || !a.renorm)) {
-      for (int64_t k = lane; k < a.K; k += 64) sum += exp((double)T::to_f32(x[k]) - (double)top);
-      sum = wave_sum_f64(sum);
+#pragma unroll 2
+      for (uint32_t k = lane; k < K; k += 64) sum += exp(logit(k) - (double)top);
+      sum = wave_op(sum, [](double a, double b) { return a + b; });
       total = (float)sum;
     }
-    auto key = [&](int64_t k) {
-      const double f = (double)T::to_f32(x[k]);
+    auto score = [&](uint32_t k) {
+      const double f = logit(k);
       if (!arith || f == -INFINITY) return f;
-      double s = a.softmax ? exp(f - (double)top) / sum : 1.0 / (1.0 + exp(-f));
+      const double e = exp(a.softmax ? f - (double)top : -f);
+      double s = a.softmax ? e / sum : 1.0 / (1.0 + e);
       if (a.bias) s += (double)a.bias[k];
       return s;
     };
-    const int gs = a.K / a.G;
+    if constexpr (HELD) {
+#pragma unroll 2
+      for (uint32_t k = lane; k < K; k += 64) c[k] = score(k);
+      wave_sync();
+    }
+    auto key = [&](uint32_t k) { return HELD ? c[k] : score(k); };
+    const uint32_t gs = K / a.G;
     uint64_t kept = ~0ull;
     if (a.G > 1) {
       double worth = -INFINITY;  // of group `lane`
-      for (int g = 0; g < a.G; ++g) {
-        double m1 = -INFINITY, m2 = -INFINITY;
-        for (int64_t k = (int64_t)g * gs + lane; k < (int64_t)(g + 1) * gs; k += 64) {
-          const double c = key(k);
-          const double low = c < m1 ? c : m1;
-          m1 = c < m1 ? m1 : c;
-          m2 = m2 < low ? low : m2;
+      auto of = [&](double m1, double m2) { return a.best == 2 && m2 > -INFINITY ? m1 + m2 : m1; };
+      if constexpr (HELD) {
+        if (lane < a.G) {
+          double m1 = -INFINITY, m2 = -INFINITY;
+          uint32_t k = lane % gs;  // (lanes start at different places: banks)
+#pragma unroll 4
+          for (uint32_t i = 0; i < gs; ++i) {
+            take2(m1, m2, c[lane * gs + k]);
+            k = k + 1 < gs ? k + 1 : 0;
+          }
+          worth = of(m1, m2);
         }
-        wave_top2(m1, m2);
-        if (lane == g) worth = a.best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+      } else {
+        for (int g = 0; g < a.G; ++g) {
+          double m1 = -INFINITY, m2 = -INFINITY;
+          for (uint32_t k = g * gs + lane; k < (g + 1) * gs; k += 64) take2(m1, m2, key(k));
+          wave_top2(m1, m2);
+          if (lane == g) worth = of(m1, m2);
+        }
       }
       int better = 0;
       for (int g = 0; g < a.G; ++g) {
@@ -123,21 +200,18 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
     int64_t pk = -1;
     for (int j = 0; j < a.S; ++j) {
       double bc = -INFINITY;
-      int64_t bk = INT64_MAX;
-      for (int64_t k = lane; k < a.K; k += 64) {
+      uint32_t bk = ~0u;
+#pragma unroll 4
+      for (uint32_t k = lane; k < K; k += 64) {
         if (!(kept >> (a.G > 1 ? k / gs : 0) & 1)) continue;
-        const double c = key(k);
-        if ((c < pc || (c == pc && k > pk)) && c > bc) bc = c, bk = k;
+        const double f = key(k);
+        if ((f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
       }
-#pragma unroll
-      for (int o = 32; o >= 1; o >>= 1) {
-        const double c = __shfl_xor(bc, o);
-        const int64_t k = __shfl_xor((long long)bk, o);
-        if (c > bc || (c == bc && k < bk)) bc = c, bk = k;
-      }
-      if (bk == INT64_MAX) break;  // uniform: every lane holds the same
-      if (lane == j) id = (int)bk;
-      pc = bc, pk = bk;
+      pc = wave_max(bc);
+      const uint32_t k = wave_min(bc == pc ? bk : ~0u);
+      if (k == ~0u) break;  // uniform: every lane holds the same
+      if (lane == j) id = (int)k;
+      pk = k;
     }
     if (id >= 0) z = T::to_f32(x[id]);
   }

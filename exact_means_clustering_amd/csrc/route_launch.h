@@ -1,32 +1,40 @@
 // Which of the routing kernels a call takes (internal).
 #pragma once
 
+#include <stdlib.h>
 #include "route_rows.h"
 
 namespace fkm {
 
 namespace {
 
+// Fewer choices than this in all (2,048 for each of 1,024 SIMDs) are few rows.
+inline int64_t route_few() {
+  static const char* e = getenv("ROUTE_FEW");
+  return e ? atoll(e) : (int64_t)2048 * 1024;
+}
+#define kRouteFew route_few()
+
 template <class T>
 __global__ __launch_bounds__(256) void route_exact_kernel(RouteArgs<T> a) {
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.n; row += (int64_t)gridDim.x * 4)
-    route_row_exact(a, row);
+    route_row_exact<T, false>(a, row, nullptr);
 }
 
 template <class T, int E, int LPR, int L, RouteMode MODE>
 hipError_t route_rows(const RouteArgs<T>& a, hipStream_t s) {
   constexpr int SL = 64 / LPR, V = 16 / T::SZ;
-  const RouteLds o = RouteLds::of(SL, a.K, a.G, a.S);
+  const RouteLds o = RouteLds::of(SL, MODE == kScored ? a.K : 0, a.G, a.S, MODE == kScored);
   // waves of a workgroup share nothing: as many as leave room for several workgroups a CU
   int waves = 4;
   while (waves > 1 && waves * o.total * 4 > 40960) waves /= 2;
   const int64_t tiles = (a.n + SL - 1) / SL;
-  const int64_t want = (tiles + waves - 1) / waves, most = 256 * 32 / waves;
+  const int64_t want = (tiles + waves - 1) / waves, most = 256 * (getenv("ROUTE_W") ? atoll(getenv("ROUTE_W")) : 32) / waves;
   const bool loose = a.K % V != 0 || (uintptr_t)a.logits % 16 != 0;
   route_rows_kernel<T, E, LPR, L, MODE>
       <<<dim3((unsigned)(want < most ? want : most)), dim3(64 * waves),
          waves * o.total * 4 + (MODE == kScored ? LPR * E * 4 : 0), s>>>(
-          a, loose, o, (65536u + a.S - 1) / a.S);
+          a, loose, o, ((1u << 20) + a.S - 1) / a.S);
   return hipGetLastError();
 }
 
@@ -34,6 +42,16 @@ template <class T, int L, RouteMode MODE>
 hipError_t route_l(const RouteArgs<T>& a, hipStream_t s) {
   if (a.K <= 8) return route_rows<T, 8, 1, (L < 8 ? L : 8), MODE>(a, s);
   if (a.K <= 16) return route_rows<T, 16, 1, (L < 16 ? L : 16), MODE>(a, s);
+  // few rows: four times the lanes for each, so that a wave has less to do after the other
+  if constexpr (L <= 8) {
+    if (a.n * a.K < kRouteFew) {
+      if (a.K <= 32) return route_rows<T, 8, 4, L, MODE>(a, s);
+      if (a.K <= 64) return route_rows<T, 8, 8, L, MODE>(a, s);
+      if (a.K <= 128) return route_rows<T, 8, 16, L, MODE>(a, s);
+      if (a.K <= 256) return route_rows<T, 8, 32, L, MODE>(a, s);
+      if (a.K <= 512) return route_rows<T, 8, 64, L, MODE>(a, s);
+    }
+  }
   if (a.K <= 32) return route_rows<T, 32, 1, L, MODE>(a, s);
   if (a.K <= 64) return route_rows<T, 32, 2, L, MODE>(a, s);
   if (a.K <= 128) return route_rows<T, 32, 4, L, MODE>(a, s);

@@ -9,9 +9,11 @@
 // order.
 //
 // Where c's order is the logits' own, a key's score is the logit.  Else it is c in 32 bits, and a bound of its error says
-// whether rounding could have changed the selection: a neighbour in the order, a choice next to the last one, or a group
-// next to the last one that is closer than the two errors, unless the two have the same logit and bias (their order is the
-// index's then).  Such rows, about one in a thousand on random scores, are decided again in 64 bits.
+// what rounding could have changed.  Where two neighbours of the selection are closer than their errors, or one choice
+// that is not selected is as close to the last one, the row's candidates are put in order by their c in 64 bits, one a
+// lane (unless the two have the same logit and bias: their order is the index's).  What is still open after that (more
+// such choices, groups whose worths are closer than their errors, and probabilities that their common divisor in 32 bits
+// leaves undecided), a few rows in ten thousand on random scores, is decided by the wave at its end, all in 64 bits.
 #pragma once
 
 #include "route.h"
@@ -57,12 +59,6 @@ __device__ __forceinline__ void merge_keys(double (&a)[L], const double (&b)[L])
     for (int i = 0; i < L; ++i)
       if (!(i & h)) exchange(a[i], a[i + h]);
 }
-template <int CTRL>
-__device__ __forceinline__ double dpp64(double v) {
-  const int lo = __double2loint(v), hi = __double2hiint(v);
-  return __hiloint2double(__builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, true),
-                          __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, true));
-}
 template <int L, int CTRL>
 __device__ __forceinline__ void merge_dpp(double (&a)[L]) {
   double b[L];
@@ -74,15 +70,7 @@ template <int L, bool FAR>
 __device__ __forceinline__ void merge_swap(double (&a)[L]) {  // lanes 16 (or 32) apart
   double b[L];
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const uint32_t lo = (uint32_t)__double2loint(a[i]), hi = (uint32_t)__double2hiint(a[i]);
-    const auto l = FAR ? __builtin_amdgcn_permlane32_swap(lo, lo, false, false)
-                       : __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
-    const auto h = FAR ? __builtin_amdgcn_permlane32_swap(hi, hi, false, false)
-                       : __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
-    a[i] = __hiloint2double((int)h[0], (int)l[0]);
-    b[i] = __hiloint2double((int)h[1], (int)l[1]);
-  }
+  for (int i = 0; i < L; ++i) swap64<FAR>(a[i], a[i], b[i]);
   merge_keys<L>(a, b);
 }
 // The L largest keys of a team's lists, in every lane.
@@ -104,12 +92,17 @@ struct Slice {
   static constexpr int V = 16 / T::SZ, NV = E / V;
   Pack<T, V> p[NV];
   static __device__ __forceinline__ int first(int j, int g) { return j * LPR * V + g * V; }
+  // (ONCE: nothing of the row is read again)
+  template <bool ONCE>
   __device__ __forceinline__ void load(const typename T::raw* row, int K, int g, bool loose, bool live) {
     if (!loose) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         p[j].fill_neg_inf();
-        if (live && first(j, g) < K) p[j].load_nt(row + first(j, g));
+        if (live && first(j, g) < K) {
+          if constexpr (ONCE) p[j].load_nt(row + first(j, g));
+          else p[j].load(row + first(j, g));
+        }
       }
     } else {
       // one load of the row, j = tail of one lane, has fewer than V elements
@@ -191,32 +184,47 @@ __device__ __forceinline__ float pair_sum(const float (&x)[E]) {
   return s[0];
 }
 
-constexpr float kU = 0x1p-24f;
-// Bounds of the error of c in 32 bits.  A probability p = exp(t) / sum: (|t| + 3) u for the exponential, 18 u for the
-// sum of such (5 levels in a lane, 6 across, its terms' own), 3 u for the quotient; a sigmoid: 7 u; c itself u.
-// (2^-120: what is flushed below the normal range.)
-__device__ __forceinline__ float soft_error(float p, float t, float c) {
-  return kU * (p * (28.f + fabsf(t)) + fabsf(c)) + 0x1p-120f;
+// exp(x - shift) to (2 |x - shift| + 3) u, and the sigmoid of x (0 for -inf).
+__device__ __forceinline__ float quick_exp(float x, float shift) { return exp_diff<BF16>(x, shift); }
+__device__ __forceinline__ float quick_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
-__device__ __forceinline__ float sigmoid_error(float c) { return kU * (8.f + fabsf(c)); }
 
-// One wave's LDS, in floats, for rows of K choices taken SL at a time.
+constexpr float kU = 0x1p-24f;
+// Bounds of the error of c in 32 bits: for a probability p = exp(t) / sum, (2 |t| + 3) u for the exponential (the
+// difference's rounding and its scaling), 18 u for the sum of such (5 levels in a lane, 6 across, and its terms' own, of
+// which |t| exp(t) is at most 0.37) and 3 u for the quotient; for a sigmoid s, 0.8 u for the exponential (s (1 - s) |t| is
+// at most 0.23), u for 1 + e and u for the reciprocal; for c itself u |c|.  (2^-120: what is flushed below the normal
+// range.)  score_error is without the last, for every choice of a row: (2 |t| + 28) exp(t) is at most 28.
+__device__ __forceinline__ float score_error(bool softmax, float inv) { return softmax ? 28.f * inv : 4.f; }
+__device__ __forceinline__ float pair_error(bool softmax, float high, float inv, float z, float c) {
+  const float t = z - high;
+  return kU * ((softmax ? quick_exp(z, high) * inv * (28.f - 2.f * t) : 4.f) + fabsf(c)) + 0x1p-120f;
+}
+
+// One wave's LDS, in floats, for rows of K choices taken SL at a time, S selections each.
 struct RouteLds {
-  int scores, worth, sel, z, e, info, flag, total;
-  static __host__ __device__ RouteLds of(int SL, int K, int G, int S) {
+  int worth, z, e, info, flag, extra, total;
+  static __host__ __device__ RouteLds of(int SL, int K, int G, int S, bool scored) {
     RouteLds o{};
-    int at = 0;
-    o.scores = at, at += G > 1 ? SL * ((K + 3) & ~3) : 0;  // (16-byte words: first)
-    o.sel = at, at += 2 * SL * S;              // keys
-    o.worth = at, at += G > 1 ? 2 * SL * G : 0;  // and its error
-    o.z = at, at += SL * S;                    // chosen logits, and their shares before the division
-    o.e = at, at += SL * S;
-    o.info = at, at += 2 * SL;                 // a row's largest logit, 1 / sum of exponentials
-    o.flag = at, at += SL;                     // a row to be decided in 64 bits
+    // groups first: a row's scores (or the largest two of four), its groups' worths, their errors, and whether they stay
+    const int scores = G > 1 ? SL * ((K + 3) & ~3) : 0;
+    o.worth = scores;
+    const int groups = scores + (G > 1 ? 3 * SL * G : 0);
+    // then, in the same place, the selections: keys, logits, shares before the division
+    o.z = 2 * SL * S, o.e = o.z + SL * S;
+    int at = o.e + SL * S;
+    if (at < groups) at = groups;
+    if (scored && at < 2 * K) at = 2 * K;    // at last, one row's scores in 64 bits
+    at = (at + 1) & ~1;
+    o.extra = at, at += scored ? 2 * SL : 0;  // the key of a choice that may belong to the selection
+    o.info = at, at += 2 * SL;               // a row's largest logit, 1 / sum of exponentials
+    o.flag = at, at += SL;                   // kOpen, kLast
     o.total = (at + 3) & ~3;
     return o;
   }
 };
+constexpr int kOpen = 2, kLast = 1;  // a row whose candidates are put in order in 64 bits; one that is decided at last
 
 // What a kernel is made for: rows of K <= LPR * E choices whose order is the logits' own; the same of any K, taken
 // LPR * E at a time; and rows of K <= LPR * E with scores, a bias or groups.
@@ -228,9 +236,10 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
   using Sl = Slice<T, E, LPR>;
   constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR;
   extern __shared__ __align__(16) float lds_all[];
-  const int lane = lane_id(), g = lane % LPR, slot = lane / LPR;
+  const int lane = lane_id(), slot = lane / LPR;
+  int g = lane % LPR;
   float* lds = lds_all + (threadIdx.x >> 6) * o.total;
-  double* sel = reinterpret_cast<double*>(lds + o.sel);
+  double* sel = reinterpret_cast<double*>(lds);
   float *zs = lds + o.z, *es = lds + o.e, *info = lds + o.info;
   int* flag = reinterpret_cast<int*>(lds + o.flag);
   const bool arith = MODE == kScored && a.arith();
@@ -240,6 +249,17 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
   const int64_t tiles = (a.n + SL - 1) / SL;
   const uint64_t team = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (slot * LPR);
 
+  Sl next;
+  bool next_live = false;
+  auto fetch = [&](int64_t t) {
+    const int64_t row = t * SL + slot;
+    next_live = t < tiles && row < a.n && (!a.valid || a.valid[row]);
+    if constexpr (MODE != kWide) next.template load<MODE == kPlain>(a.logits + row * a.K, a.K, g, loose, next_live);
+  };
+  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
+  const int64_t t0 = t;
+  bool again = false;
+  if constexpr (MODE != kWide) fetch(t);
   // the bias, with zeros where there is none, for all of the workgroup's waves
   const float* bias = lds_all + (blockDim.x >> 6) * o.total;
   bool bias_nan = false;
@@ -252,21 +272,11 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
     }
     bias_nan = __syncthreads_or(nan);
   }
-
-  Sl next;
-  bool next_live = false;
-  auto fetch = [&](int64_t t) {
-    const int64_t row = t * SL + slot;
-    next_live = t < tiles && row < a.n && (!a.valid || a.valid[row]);
-    if constexpr (MODE != kWide) next.load(a.logits + row * a.K, a.K, g, loose, next_live);
-  };
-  int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-  const int64_t t0 = t;
-  bool again = false;
-  if constexpr (MODE == kPlain) fetch(t);
   for (; t < tiles; t += waves) {
     const int64_t row0 = t * SL, row = row0 + slot;
-    if constexpr (MODE != kPlain) fetch(t);
+    // (what a lane's columns say is formed anew for every tile: kept in registers, it would push out the row)
+    asm volatile("" : "+v"(g), "+s"(a.K), "+s"(a.G));
+    if constexpr (MODE == kWide) fetch(t);
     const Sl now = next;
     const bool live = next_live;
     if constexpr (MODE == kPlain) fetch(t + waves);
@@ -278,8 +288,8 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       for (int64_t off = 0; off < a.K; off += LPR * E) {
         const int left = a.K - off < LPR * E ? (int)(a.K - off) : LPR * E;
         Sl s;
-        s.load(a.logits + row * a.K + off, left, g, loose, live);
-        bad |= s.has_nan();
+        s.template load<true>(a.logits + row * a.K + off, left, g, loose, live);
+        if (!sums) bad |= s.has_nan();
         float x[E];
         s.values(x);
         if (sums) {
@@ -287,7 +297,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
           const float shift = m == -INFINITY ? 0.f : m;
           float e[E];
 #pragma unroll
-          for (int i = 0; i < E; ++i) e[i] = exp_diff<F32>(x[i], shift);
+          for (int i = 0; i < E; ++i) e[i] = quick_exp(x[i], shift);
           sum = fmaf(sum, high == -INFINITY ? 0.f : exp_diff<F32>(high, shift), pair_sum(e));
           high = m;
         }
@@ -297,20 +307,25 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
         const float m = team_max<LPR>(high);
         sum = team_sum<LPR>(high == -INFINITY ? 0.f : sum * exp_diff<F32>(high, m));
         high = m, inv = 1.f / sum;
+        bad = sum != sum;
+      } else {
+        bad = (__ballot(bad) & team) != 0;
       }
-      bad = (__ballot(bad) & team) != 0;
       join_lists<L, LPR>(top);
     } else {
-      bad = now.has_nan();
       float x[E];
       now.values(x);
-      if (sums) {
+      if (!sums) {
+        bad = (__ballot(now.has_nan()) & team) != 0;
+      } else {
         high = team_max<LPR>(max_of(x));
         const float shift = high == -INFINITY ? 0.f : high;
         float e[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) e[i] = exp_diff<F32>(x[i], shift);
-        inv = 1.f / team_sum<LPR>(pair_sum(e));
+        for (int i = 0; i < E; ++i) e[i] = quick_exp(x[i], shift);
+        const float sum = team_sum<LPR>(pair_sum(e));
+        inv = 1.f / sum;
+        bad = sum != sum;  // (a NaN, or +inf - inf)
         if constexpr (MODE == kScored) {
           if (arith) {
 #pragma unroll
@@ -321,7 +336,6 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       if constexpr (MODE == kPlain) {
         add_keys<T, E, LPR, L>(top, x, g * V, true);
         join_lists<L, LPR>(top);
-        bad = (__ballot(bad) & team) != 0;
       } else {
         int unsure = 0;
         if (arith && !a.softmax) {
@@ -329,39 +343,63 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
           for (int i = 0; i < E; ++i)
             x[i] = x[i] == -INFINITY
                        ? x[i]
-                       : __builtin_amdgcn_rcpf(1.f + exp_to(-x[i])) + bias[Sl::first(i / V, g) + i % V];
+                       : quick_sigmoid(x[i]) + bias[Sl::first(i / V, g) + i % V];
         }
-        bad |= bias_nan;
-        bad = live && (__ballot(bad) & team) != 0;
-        const float base = a.softmax ? 28.f * inv : 8.f;  // (|t| + 28) exp(t) is at most 28
+        bad = live && (bad || bias_nan);
+        const float base = score_error(a.softmax, inv);
         if (a.G > 1) {
-          // the scores change hands: lanes add up groups, and put those that go out of reach
-          const int stride = (a.K + 3) & ~3, gs = a.K / a.G;
-          float* mine = lds + o.scores + slot * stride;
-          float *worth = lds + o.worth, *werr = worth + SL * a.G;
+          // the scores change hands: lanes take a group each, and say which of them stay
+          const int gs = a.K / a.G;
+          const float per = 1.f / (float)gs;
+          auto group_of = [&](int k) { return (int)(((float)k + 0.5f) * per); };  // (exact: k < 2,048)
+          float *worth = lds + o.worth, *werr = worth + SL * a.G, *keep = werr + SL * a.G;
           wave_sync();  // (the tile before is done with it)
           if (g == 0) info[2 * slot] = base;
           if (lane < SL) flag[lane] = 0;
+          const bool fours = gs % 4 == 0;
+          if (fours) {
+            // four neighbours of a group leave their largest two
+            float2* mine = reinterpret_cast<float2*>(lds) + slot * (a.K / 4);
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int q = 0; q < V; q += 4) {
-              const int c = Sl::first(j, g) + q;  // (a row's last words may run into its padding)
+            for (int i = 0; i < E; i += 4) {
+              const int c = Sl::first(i / V, g) + i % V;
+              const float h0 = fmaxf(x[i], x[i + 1]), l0 = fminf(x[i], x[i + 1]);
+              const float h1 = fmaxf(x[i + 2], x[i + 3]), l1 = fminf(x[i + 2], x[i + 3]);
               if (c < a.K)
-                *reinterpret_cast<float4*>(mine + c) =
-                    make_float4(x[j * V + q], x[j * V + q + 1], x[j * V + q + 2], x[j * V + q + 3]);
+                mine[c / 4] = make_float2(fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1)));
             }
+          } else {
+            float* mine = lds + slot * ((a.K + 3) & ~3);
+#pragma unroll
+            for (int i = 0; i < E; i += 4) {
+              const int c = Sl::first(i / V, g) + i % V;  // (a row's last words may run into its padding)
+              if (c < a.K) *reinterpret_cast<float4*>(mine + c) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            }
+          }
           wave_sync();
           for (int it = lane; it < SL * a.G; it += 64) {
             const int r = it / a.G, gr = it - r * a.G;
-            const float* p = lds + o.scores + r * stride + gr * gs;
             float m1 = -INFINITY, m2 = -INFINITY;
-            int k = it % gs;  // (lanes start at different places: banks)
-            for (int i = 0; i < gs; ++i) {
-              const float c = p[k];
-              m2 = fmaxf(m2, fminf(m1, c));
-              m1 = fmaxf(m1, c);
-              k = k + 1 < gs ? k + 1 : 0;
+            const int steps = fours ? gs / 4 : gs;
+            int k = it % steps;  // (lanes start at different places: banks)
+            if (fours) {
+              const float2* p = reinterpret_cast<const float2*>(lds) + r * (a.K / 4) + gr * steps;
+#pragma unroll 8
+              for (int i = 0; i < steps; ++i) {
+                const float2 c = p[k];
+                m2 = fmaxf(fmaxf(m2, c.y), fminf(m1, c.x));
+                m1 = fmaxf(m1, c.x);
+                k = k + 1 < steps ? k + 1 : 0;
+              }
+            } else {
+              const float* p = lds + r * ((a.K + 3) & ~3) + gr * steps;
+#pragma unroll 4
+              for (int i = 0; i < steps; ++i) {
+                const float c = p[k];
+                m2 = fmaxf(m2, fminf(m1, c));
+                m1 = fmaxf(m1, c);
+                k = k + 1 < steps ? k + 1 : 0;
+              }
             }
             const bool two = a.best == 2 && m2 > -INFINITY;
             worth[it] = two ? m1 + m2 : m1;
@@ -375,6 +413,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
             const float w = worth[it];
             int better = 0;
             float err = 0.f, gap = INFINITY;  // the largest error, and the distance to the next group down
+#pragma unroll 4
             for (int q = 0; q < a.G; ++q) {
               const float other = worth[r * a.G + q];
               const bool b = other > w || (other == w && q < gr);
@@ -383,31 +422,28 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
               if (!b && q != gr) gap = fminf(gap, w - other);
             }
             // the last group that stays and the first that goes (worths of two groups without choices are not compared)
-            if (arith && better == a.keep - 1 && w > -INFINITY && gap <= 2.2f * err) flag[r] = 1;
-            if (better >= a.keep) {
-              float* p = lds + o.scores + r * stride + gr * gs;
-              int k = it % gs;
-              for (int i = 0; i < gs; ++i) {
-                p[k] = -INFINITY;
-                k = k + 1 < gs ? k + 1 : 0;
-              }
-            }
+            if (arith && better == a.keep - 1 && w > -INFINITY && gap <= 2.2f * err) flag[r] = kLast;
+            keep[it] = better < a.keep ? 1.f : 0.f;
           }
           wave_sync();
 #pragma unroll
-          for (int j = 0; j < NV; ++j)
+          for (int i = 0; i < E; i += 4) {
+            const int c = Sl::first(i / V, g) + i % V;
+            if (fours) {
+              const float stays = c < a.K ? keep[slot * a.G + group_of(c)] : 0.f;
 #pragma unroll
-            for (int q = 0; q < V; q += 4) {
-              const int c = Sl::first(j, g) + q;
-              if (c < a.K) {
-                const float4 f = *reinterpret_cast<const float4*>(mine + c);
-                x[j * V + q] = f.x, x[j * V + q + 1] = f.y, x[j * V + q + 2] = f.z, x[j * V + q + 3] = f.w;
-              }
+              for (int v = 0; v < 4; ++v) x[i + v] = stays != 0.f ? x[i + v] : -INFINITY;
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                x[i + v] = c + v < a.K && keep[slot * a.G + group_of(c + v)] != 0.f ? x[i + v] : -INFINITY;
             }
+          }
           unsure = flag[slot];
         }
         add_keys<T, E, LPR, L>(top, x, g * V, true);
         join_lists<L, LPR>(top);
+        double extra = __hiloint2double((int)0xFF800000u, 0);  // (a score of -inf: none)
         if (arith) {
           // choices that are not selected and no further from the last one than rounding goes
           double last = top[0];
@@ -419,28 +455,42 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
 #pragma unroll
           for (int i = 0; i < E; ++i) count += x[i] >= border;
           count = (int)team_sum<LPR>((float)count);
-          if (vs > -INFINITY && count > S && live && !bad) {
-            // all of them with the last one's logit and bias: the index decides
-            const float zl = T::to_f32(a.logits[row * a.K + key_col(last)]);
-            const float bl = bias[key_col(last)];
-            for (int k = g; k < a.K; k += LPR) {
-              const float f = T::to_f32(a.logits[row * a.K + k]), b = bias[k];
-              if (f == zl && b == bl) continue;
-              const float c = f == -INFINITY ? f
-                              : a.softmax    ? fmaf(exp_diff<F32>(f, high), inv, b)
-                                             : __builtin_amdgcn_rcpf(1.f + exp_to(-f)) + b;
-              // (a group that is out of reach holds -inf in LDS)
-              const bool out = a.G > 1 && lds[o.scores + slot * ((a.K + 3) & ~3) + k] == -INFINITY;
-              if (!out && c >= border && key_of(c, k) < last) unsure = 1;
+          const bool many = vs > -INFINITY && count > S && live && !bad;
+          if (__ballot(many)) {  // the largest of them joins; others than it and its equals are for the end
+            auto score = [&](int k, float& f, float& b) {
+              f = T::to_f32(a.logits[row * a.K + k]), b = bias[k];
+              const bool out = a.G > 1 && lds[o.worth + (2 * SL + slot) * a.G + k / (a.K / a.G)] == 0.f;  // (stays?)
+              return out || f == -INFINITY ? -INFINITY
+                     : a.softmax           ? fmaf(quick_exp(f, high), inv, b)
+                                           : quick_sigmoid(f) + b;
+            };
+            double best[1] = {extra};
+            float f, b;
+            if (many)
+              for (int k = g; k < a.K; k += LPR) {
+                const double key = key_of(score(k, f, b), k);
+                if (key_score(key) >= border && key < last && key > best[0]) best[0] = key;
+              }
+            join_lists<1, LPR>(best);
+            extra = best[0];
+            if (many && count > S + 1) {
+              const float fe = T::to_f32(a.logits[row * a.K + key_col(extra)]), be = bias[key_col(extra)];
+              for (int k = g; k < a.K; k += LPR) {
+                const double key = key_of(score(k, f, b), k);
+                if (key_score(key) >= border && key < extra && (f != fe || b != be)) unsure = 1;
+              }
             }
           }
           unsure = (__ballot(unsure) & team) != 0;
         }
         wave_sync();
-        if (g == 0) flag[slot] = arith && unsure && live && !bad;
+        if (g == 0) {
+          flag[slot] = !arith || !live || bad ? 0 : unsure ? kLast : key_score(extra) > -INFINITY ? kOpen : 0;
+          reinterpret_cast<double*>(lds + o.extra)[slot] = extra;
+        }
       }
     }
-    if (a.softmax && (arith ? high : key_score(top[0])) == INFINITY) bad = true;
+    if (a.softmax && !sums && key_score(top[0]) == INFINITY) bad = true;
     // ---- the selections change hands: item it is selection it % S of row it / S
     wave_sync();
 #pragma unroll
@@ -449,35 +499,66 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
     if (g == 0) info[2 * slot] = high, info[2 * slot + 1] = inv;
     wave_sync();
     const int items = (int)(a.n - row0 < SL ? a.n - row0 : SL) * S;
+    auto row_of = [&](int it) { return (int)(((uint32_t)it * magic) >> 20); };
     for (int it = lane; it < items; it += 64) {
-      const int r = (int)(((uint32_t)it * magic) >> 16);
+      const int r = row_of(it);
       const double k = sel[it];
       float z = key_score(k);
       if (arith && z > -INFINITY && !is_nan_bits(z)) z = T::to_f32(a.logits[(row0 + r) * a.K + key_col(k)]);
       zs[it] = z;
     }
     wave_sync();
-    if (arith) {
-      for (int it = lane; it < items; it += 64) {
-        const int r = (int)(((uint32_t)it * magic) >> 16);
-        if (it + 1 >= (r + 1) * S) continue;
-        const double k = sel[it], k1 = sel[it + 1];
-        const float c = key_score(k), c1 = key_score(k1), z = zs[it], z1 = zs[it + 1];
-        if (is_nan_bits(c) || !(c1 > -INFINITY)) continue;
-        float err;
-        if (a.softmax) {
+    if constexpr (MODE == kScored) {
+      if (arith) {
+        for (int it = lane; it < items; it += 64) {
+          const int r = row_of(it);
+          if (it + 1 >= (r + 1) * S) continue;
+          const double k = sel[it], k1 = sel[it + 1];
+          const float c = key_score(k), c1 = key_score(k1), z = zs[it], z1 = zs[it + 1];
+          if (is_nan_bits(c) || !(c1 > -INFINITY)) continue;
           const float m = info[2 * r], pi = info[2 * r + 1];
-          err = soft_error(exp_diff<F32>(z, m) * pi, z - m, c) + soft_error(exp_diff<F32>(z1, m) * pi, z1 - m, c1);
-        } else {
-          err = sigmoid_error(c) + sigmoid_error(c1);
+          const float err = pair_error(a.softmax, m, pi, z, c) + pair_error(a.softmax, m, pi, z1, c1);
+          if (c - c1 <= 1.1f * err && (z != z1 || bias[key_col(k)] != bias[key_col(k1)])) atomicOr(&flag[r], kOpen);
         }
-        if (c - c1 <= 1.1f * err && (z != z1 || bias[key_col(k)] != bias[key_col(k1)])) flag[r] = 1;
+        wave_sync();
+        uint64_t open = __ballot(lane < SL && flag[lane < SL ? lane : 0] == kOpen);
+        while (open) {  // lane j takes candidate j, the extra one is the last
+          const int r = __builtin_ctzll(open);
+          open &= open - 1;
+          const double k = lane < S ? sel[r * S + lane] : reinterpret_cast<double*>(lds + o.extra)[r];
+          const bool some = lane <= S && key_score(k) > -INFINITY;
+          float z = -INFINITY, b = 0.f;
+          double p = 0.0, c = -INFINITY;
+          if (some) {
+            z = T::to_f32(a.logits[(row0 + r) * a.K + key_col(k)]), b = bias[key_col(k)];
+            const double e = exp(a.softmax ? (double)z - (double)info[2 * r] : -(double)z);
+            p = a.softmax ? e * (double)info[2 * r + 1] : 1.0 / (1.0 + e);
+            c = p + (double)b;
+          }
+          int rank = 0;
+          bool last = false;
+          for (int i = 0; i <= S; ++i) {
+            const double ci = __shfl(c, i), pi = __shfl(p, i);
+            const float zi = __shfl(z, i), bi = __shfl(b, i);
+            const uint32_t ki = __shfl(some ? key_col(k) : ~0u, i);
+            rank += ci > c || (ci == c && (some ? ki < key_col(k) : i < lane));
+            // (the error of 1 / sum is the same in both: 20 u of the probabilities' difference)
+            if (a.softmax && some && ci > -INFINITY && fabs(ci - c) <= 0x1p-19 * fabs(pi - p) + 0x1p-48 * (pi + p))
+              last |= zi != z || bi != b;
+          }
+          if (__ballot(last)) {
+            if (lane == 0) flag[r] = kLast;
+          } else if (lane <= S && rank < S) {
+            sel[r * S + rank] = some ? key_of(0.f, key_col(k)) : __hiloint2double((int)0xFF800000u, 0);
+            zs[r * S + rank] = z;
+          }
+          wave_sync();
+        }
       }
-      wave_sync();
     }
     if (a.renorm) {
       for (int it = lane; it < items; it += 64) {
-        const int r = (int)(((uint32_t)it * magic) >> 16);
+        const int r = row_of(it);
         float m = -INFINITY;
         for (int j = 0; j < S; ++j) m = fmaxf(m, zs[r * S + j]);
         es[it] = zs[it] == -INFINITY ? 0.f : share_term(zs[it], share_shift(m, a.softmax), a.softmax);
@@ -485,11 +566,16 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       wave_sync();
     }
     for (int it = lane; it < items; it += 64) {
-      const int r = (int)(((uint32_t)it * magic) >> 16);
-      const double k = sel[it];
+      const int r = row_of(it);
       const float z = zs[it];
+      const int64_t at = row0 * S + it;
+      if (MODE == kScored && flag[r] & kLast) {
+        a.ids[at] = kUnsure;
+        again = true;
+        continue;
+      }
       const bool nan = is_nan_bits(z);
-      const bool out = nan || !(key_score(k) > -INFINITY);
+      const bool out = nan || !(z > -INFINITY);
       float w;
       if (a.renorm) {
         float sum = 0.f;
@@ -498,16 +584,11 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       } else {
         w = a.scale * (a.softmax ? exp_diff<F32>(z, info[2 * r]) * info[2 * r + 1] : 1.f / (1.f + exp_to(-z)));
       }
-      const int64_t at = row0 * S + it;
-      if (arith && flag[r]) {  // left for the end of the launch
-        a.ids[at] = kUnsure;
-        again = true;
-        continue;
-      }
-      a.ids[at] = out ? -1 : (int32_t)key_col(k);
+      a.ids[at] = out ? -1 : (int32_t)key_col(sel[it]);
       a.weights[at] = nan ? __uint_as_float(0x7FC00000u) : out ? 0.f : w;
       a.chosen[at] = nan ? __uint_as_float(0x7FC00000u) : out ? -INFINITY : z;
     }
+    if constexpr (MODE == kScored) fetch(t + waves);  // (no earlier: it would push the row out)
   }
   if constexpr (MODE == kScored) {
     if (!__ballot(again)) return;
@@ -515,7 +596,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
     for (int64_t t = t0; t < tiles; t += waves) {
       uint64_t rows = __ballot(lane < SL && t * SL + lane < a.n && a.ids[(t * SL + lane) * S] == kUnsure);
       while (rows) {
-        route_row_exact(a, t * SL + __builtin_ctzll(rows));
+        route_row_exact<T, true>(a, t * SL + __builtin_ctzll(rows), reinterpret_cast<double*>(lds));
         rows &= rows - 1;
       }
     }
