@@ -70,6 +70,14 @@ __device__ __forceinline__ void swap64(double v, double& a, double& b) {
   swap32<FAR>((uint32_t)__double2hiint(v), ha, hb);
   a = __hiloint2double((int)ha, (int)la), b = __hiloint2double((int)hb, (int)lb);
 }
+// The value of lane i (the same i in all lanes).
+__device__ __forceinline__ float lane_value(float v, int i) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+}
+__device__ __forceinline__ double lane_value(double v, int i) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), i),
+                          __builtin_amdgcn_readlane(__double2loint(v), i));
+}
 // Reductions over the 64 lanes of a wave, in every lane.
 template <class Op>
 __device__ __forceinline__ double wave_op(double v, Op op) {
@@ -115,11 +123,92 @@ __device__ __forceinline__ void wave_top2(double& m1, double& m2) {
   }
 }
 
-// One row by one wave, scores in 64 bits.  Selection after selection, the next choice in the order of (score, index) is
-// looked for over the whole row.  HELD: the K scores stay in the wave's LDS (c); else they are computed again each time,
-// for rows of any length.
-template <class T, bool HELD>
-__device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row, double* c) {
+// The next choice of a wave's scores in the order of (score, index): pc and pk the one before, of which each lane has
+// looked for the next (bc, bk; -inf and ~0 if it has none).  False if there is none.
+__device__ __forceinline__ bool next_choice(double bc, uint32_t bk, double& pc, int64_t& pk) {
+  pc = wave_max(bc);
+  const uint32_t k = wave_min(bc == pc ? bk : ~0u);
+  pk = k;
+  return k != ~0u;  // uniform: every lane holds the same
+}
+// Which groups stay, from the worth of group `lane`.
+__device__ __forceinline__ uint64_t groups_kept(double worth, int G, int keep) {
+  const int lane = lane_id();
+  int better = 0;
+  for (int g = 0; g < G; ++g) {
+    const double w = lane_value(worth, g);
+    better += w > worth || (w == worth && g < lane);
+  }
+  return __ballot(lane < G && better < keep && worth > -INFINITY);
+}
+__device__ __forceinline__ double worth_of(double m1, double m2, int best) {
+  return best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+}
+
+// The selections of one row with scores, by one wave in 64 bits: the choice of selection `lane`, or -1.  The K scores
+// stay in the wave's LDS (c).  The row is valid and has no NaN (nor +inf under softmax).  Few calls come here: the code is
+// kept small (one exponential, one quotient, no unrolled loops), since it is not in the instruction cache.
+template <class T>
+__device__ __forceinline__ int decide_row(const RouteArgs<T>& a, int64_t row, const float* bias, double* c) {
+  const int lane = lane_id();
+  const uint32_t K = a.K, gs = K / a.G;
+  const typename T::raw* x = a.logits + row * a.K;
+  float top = -INFINITY;
+#pragma unroll 1
+  for (uint32_t k = lane; k < K; k += 64) {
+    const float f = T::to_f32(x[k]);
+    top = fmaxf(top, f);
+    c[k] = (double)f;
+  }
+  top = team_max<64>(top);
+  double sum = 0.0;
+#pragma unroll 1
+  for (uint32_t k = lane; k < K; k += 64) {
+    const double f = c[k], e = exp(a.softmax ? f - (double)top : -f);
+    sum += e;
+    c[k] = f == -INFINITY ? f : e;
+  }
+  sum = wave_op(sum, [](double a, double b) { return a + b; });
+#pragma unroll 1
+  for (uint32_t k = lane; k < K; k += 64) {
+    const double e = c[k], s = (a.softmax ? e : 1.0) / (a.softmax ? sum : 1.0 + e);
+    c[k] = e == -INFINITY ? e : s + (double)bias[k];
+  }
+  wave_sync();
+  uint64_t kept = ~0ull;
+  if (a.G > 1) {
+    double m1 = -INFINITY, m2 = -INFINITY;
+    if (lane < a.G) {
+      uint32_t k = lane % gs;  // (lanes start at different places: banks)
+#pragma unroll 1
+      for (uint32_t i = 0; i < gs; ++i) {
+        take2(m1, m2, c[lane * gs + k]);
+        k = k + 1 < gs ? k + 1 : 0;
+      }
+    }
+    kept = groups_kept(worth_of(m1, m2, a.best), a.G, a.keep);
+  }
+  int id = -1;
+  double pc = INFINITY;
+  int64_t pk = -1;
+#pragma unroll 1
+  for (int j = 0; j < a.S; ++j) {
+    double bc = -INFINITY;
+    uint32_t bk = ~0u;
+#pragma unroll 1
+    for (uint32_t k = lane; k < K; k += 64) {
+      const double f = c[k];
+      if ((kept >> (a.G > 1 ? k / gs : 0) & 1) && (f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
+    }
+    if (!next_choice(bc, bk, pc, pk)) break;
+    if (lane == j) id = (int)pk;
+  }
+  return id;
+}
+
+// One row of any length by one wave, scores in 64 bits, computed again for each selection.
+template <class T>
+__device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row) {
   const int lane = lane_id();
   const uint32_t K = a.K;
   const typename T::raw* x = a.logits + row * a.K;
@@ -130,15 +219,12 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
   float total = 0.f;    // softmax: the sum of exp(logit - top)
   float top = -INFINITY;
   bool bad = false;
-  auto logit = [&](uint32_t k) { return HELD ? c[k] : (double)T::to_f32(x[k]); };
   if (valid) {
-    if constexpr (HELD) wave_sync();
 #pragma unroll 4
     for (uint32_t k = lane; k < K; k += 64) {
       const float f = T::to_f32(x[k]);
       bad |= is_nan_bits(f) || (a.bias && is_nan_bits(a.bias[k]));
       top = fmaxf(top, f);
-      if constexpr (HELD) c[k] = (double)f;
     }
     top = team_max<64>(top);
     bad = __ballot(bad) != 0 || (a.softmax && top == INFINITY);
@@ -147,54 +233,28 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
     double sum = 0.0;
     if (a.softmax && (arith || !a.renorm)) {
 #pragma unroll 2
-      for (uint32_t k = lane; k < K; k += 64) sum += exp(logit(k) - (double)top);
+      for (uint32_t k = lane; k < K; k += 64) sum += exp((double)T::to_f32(x[k]) - (double)top);
       sum = wave_op(sum, [](double a, double b) { return a + b; });
       total = (float)sum;
     }
-    auto score = [&](uint32_t k) {
-      const double f = logit(k);
+    auto key = [&](uint32_t k) {
+      const double f = (double)T::to_f32(x[k]);
       if (!arith || f == -INFINITY) return f;
       const double e = exp(a.softmax ? f - (double)top : -f);
-      double s = a.softmax ? e / sum : 1.0 / (1.0 + e);
-      if (a.bias) s += (double)a.bias[k];
-      return s;
+      const double s = (a.softmax ? e : 1.0) / (a.softmax ? sum : 1.0 + e);
+      return a.bias ? s + (double)a.bias[k] : s;
     };
-    if constexpr (HELD) {
-#pragma unroll 2
-      for (uint32_t k = lane; k < K; k += 64) c[k] = score(k);
-      wave_sync();
-    }
-    auto key = [&](uint32_t k) { return HELD ? c[k] : score(k); };
     const uint32_t gs = K / a.G;
     uint64_t kept = ~0ull;
     if (a.G > 1) {
       double worth = -INFINITY;  // of group `lane`
-      auto of = [&](double m1, double m2) { return a.best == 2 && m2 > -INFINITY ? m1 + m2 : m1; };
-      if constexpr (HELD) {
-        if (lane < a.G) {
-          double m1 = -INFINITY, m2 = -INFINITY;
-          uint32_t k = lane % gs;  // (lanes start at different places: banks)
-#pragma unroll 4
-          for (uint32_t i = 0; i < gs; ++i) {
-            take2(m1, m2, c[lane * gs + k]);
-            k = k + 1 < gs ? k + 1 : 0;
-          }
-          worth = of(m1, m2);
-        }
-      } else {
-        for (int g = 0; g < a.G; ++g) {
-          double m1 = -INFINITY, m2 = -INFINITY;
-          for (uint32_t k = g * gs + lane; k < (g + 1) * gs; k += 64) take2(m1, m2, key(k));
-          wave_top2(m1, m2);
-          if (lane == g) worth = of(m1, m2);
-        }
-      }
-      int better = 0;
       for (int g = 0; g < a.G; ++g) {
-        const double w = __shfl(worth, g);
-        better += w > worth || (w == worth && g < lane);
+        double m1 = -INFINITY, m2 = -INFINITY;
+        for (uint32_t k = g * gs + lane; k < (g + 1) * gs; k += 64) take2(m1, m2, key(k));
+        wave_top2(m1, m2);
+        if (lane == g) worth = worth_of(m1, m2, a.best);
       }
-      kept = __ballot(lane < a.G && better < a.keep && worth > -INFINITY);
+      kept = groups_kept(worth, a.G, a.keep);
     }
     double pc = INFINITY;  // the selection before
     int64_t pk = -1;
@@ -207,11 +267,8 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
         const double f = key(k);
         if ((f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
       }
-      pc = wave_max(bc);
-      const uint32_t k = wave_min(bc == pc ? bk : ~0u);
-      if (k == ~0u) break;  // uniform: every lane holds the same
-      if (lane == j) id = (int)k;
-      pk = k;
+      if (!next_choice(bc, bk, pc, pk)) break;
+      if (lane == j) id = (int)pk;
     }
     if (id >= 0) z = T::to_f32(x[id]);
   }

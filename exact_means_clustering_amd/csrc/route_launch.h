@@ -1,24 +1,20 @@
 // Which of the routing kernels a call takes (internal).
 #pragma once
 
-#include <stdlib.h>
 #include "route_rows.h"
 
 namespace fkm {
 
 namespace {
 
-// Fewer choices than this in all (2,048 for each of 1,024 SIMDs) are few rows.
-inline int64_t route_few() {
-  static const char* e = getenv("ROUTE_FEW");
-  return e ? atoll(e) : (int64_t)2048 * 1024;
-}
-#define kRouteFew route_few()
+// Fewer choices than this in all (2,048 for each of 1,024 SIMDs) are few rows (16,384 x 128 bf16 5.9 us as few rows, 6.2
+// as many; 32,768 x 128 10.0 and 7.3; 8,192 x 64 3.5 and 4.8; 16,384 x 256 fp32 in 8 groups 48 and 51).
+constexpr int64_t kRouteFew = (int64_t)1 << 21;
 
 template <class T>
 __global__ __launch_bounds__(256) void route_exact_kernel(RouteArgs<T> a) {
   for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.n; row += (int64_t)gridDim.x * 4)
-    route_row_exact<T, false>(a, row, nullptr);
+    route_row_exact(a, row);
 }
 
 template <class T, int E, int LPR, int L, RouteMode MODE>
@@ -29,7 +25,9 @@ hipError_t route_rows(const RouteArgs<T>& a, hipStream_t s) {
   int waves = 4;
   while (waves > 1 && waves * o.total * 4 > 40960) waves /= 2;
   const int64_t tiles = (a.n + SL - 1) / SL;
-  const int64_t want = (tiles + waves - 1) / waves, most = 256 * (getenv("ROUTE_W") ? atoll(getenv("ROUTE_W")) : 32) / waves;
+  // waves that loop where there are many rows (1,048,576 x 8 bf16 12.4 us with 64 a CU, 13.5 with 32, 14.7 with 16;
+  // 65,536 x 256 fp32 in 8 groups 63 with 64, 54 with 32)
+  const int64_t want = (tiles + waves - 1) / waves, most = 256 * (MODE == kScored ? 32 : 64) / waves;
   const bool loose = a.K % V != 0 || (uintptr_t)a.logits % 16 != 0;
   route_rows_kernel<T, E, LPR, L, MODE>
       <<<dim3((unsigned)(want < most ? want : most)), dim3(64 * waves),

@@ -13,7 +13,7 @@
 // that is not selected is as close to the last one, the row's candidates are put in order by their c in 64 bits, one a
 // lane (unless the two have the same logit and bias: their order is the index's).  What is still open after that (more
 // such choices, groups whose worths are closer than their errors, and probabilities that their common divisor in 32 bits
-// leaves undecided), a few rows in ten thousand on random scores, is decided by the wave at its end, all in 64 bits.
+// leaves undecided), a few rows in ten thousand on random scores, is decided by the whole wave, all in 64 bits.
 #pragma once
 
 #include "route.h"
@@ -196,15 +196,15 @@ constexpr float kU = 0x1p-24f;
 // which |t| exp(t) is at most 0.37) and 3 u for the quotient; for a sigmoid s, 0.8 u for the exponential (s (1 - s) |t| is
 // at most 0.23), u for 1 + e and u for the reciprocal; for c itself u |c|.  (2^-120: what is flushed below the normal
 // range.)  score_error is without the last, for every choice of a row: (2 |t| + 28) exp(t) is at most 28.
-__device__ __forceinline__ float score_error(bool softmax, float inv) { return softmax ? 28.f * inv : 4.f; }
+__device__ __forceinline__ float score_error(bool softmax, float inv) { return softmax ? 28.f * inv : 3.f; }
 __device__ __forceinline__ float pair_error(bool softmax, float high, float inv, float z, float c) {
   const float t = z - high;
-  return kU * ((softmax ? quick_exp(z, high) * inv * (28.f - 2.f * t) : 4.f) + fabsf(c)) + 0x1p-120f;
+  return kU * ((softmax ? quick_exp(z, high) * inv * (28.f - 2.f * t) : 3.f) + fabsf(c)) + 0x1p-120f;
 }
 
 // One wave's LDS, in floats, for rows of K choices taken SL at a time, S selections each.
 struct RouteLds {
-  int worth, z, e, info, flag, extra, total;
+  int worth, z, e, exact, info, flag, extra, total;
   static __host__ __device__ RouteLds of(int SL, int K, int G, int S, bool scored) {
     RouteLds o{};
     // groups first: a row's scores (or the largest two of four), its groups' worths, their errors, and whether they stay
@@ -215,8 +215,8 @@ struct RouteLds {
     o.z = 2 * SL * S, o.e = o.z + SL * S;
     int at = o.e + SL * S;
     if (at < groups) at = groups;
-    if (scored && at < 2 * K) at = 2 * K;    // at last, one row's scores in 64 bits
     at = (at + 1) & ~1;
+    o.exact = at, at += scored ? 2 * K : 0;  // one row's scores in 64 bits
     o.extra = at, at += scored ? 2 * SL : 0;  // the key of a choice that may belong to the selection
     o.info = at, at += 2 * SL;               // a row's largest logit, 1 / sum of exponentials
     o.flag = at, at += SL;                   // kOpen, kLast
@@ -224,15 +224,14 @@ struct RouteLds {
     return o;
   }
 };
-constexpr int kOpen = 2, kLast = 1;  // a row whose candidates are put in order in 64 bits; one that is decided at last
+constexpr int kOpen = 2, kLast = 1;  // a row whose candidates are put in order in 64 bits; one that is so as a whole
 
 // What a kernel is made for: rows of K <= LPR * E choices whose order is the logits' own; the same of any K, taken
 // LPR * E at a time; and rows of K <= LPR * E with scores, a bias or groups.
 enum RouteMode { kPlain, kWide, kScored };
-constexpr int32_t kUnsure = INT32_MIN;  // an id that waits to be decided in 64 bits
 
 template <class T, int E, int LPR, int L, RouteMode MODE>
-__global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic) {
+__global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 : 4) void route_rows_kernel(RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic) {
   using Sl = Slice<T, E, LPR>;
   constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR;
   extern __shared__ __align__(16) float lds_all[];
@@ -257,8 +256,6 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
     if constexpr (MODE != kWide) next.template load<MODE == kPlain>(a.logits + row * a.K, a.K, g, loose, next_live);
   };
   int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6);
-  const int64_t t0 = t;
-  bool again = false;
   if constexpr (MODE != kWide) fetch(t);
   // the bias, with zeros where there is none, for all of the workgroup's waves
   const float* bias = lds_all + (blockDim.x >> 6) * o.total;
@@ -521,16 +518,19 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
           if (c - c1 <= 1.1f * err && (z != z1 || bias[key_col(k)] != bias[key_col(k1)])) atomicOr(&flag[r], kOpen);
         }
         wave_sync();
-        uint64_t open = __ballot(lane < SL && flag[lane < SL ? lane : 0] == kOpen);
+        const int state = lane < SL ? flag[lane] : 0;
+        uint64_t open = __ballot(state == kOpen), whole = __ballot(state & kLast);
         while (open) {  // lane j takes candidate j, the extra one is the last
           const int r = __builtin_ctzll(open);
           open &= open - 1;
           const double k = lane < S ? sel[r * S + lane] : reinterpret_cast<double*>(lds + o.extra)[r];
           const bool some = lane <= S && key_score(k) > -INFINITY;
+          const int ck = some ? (int)key_col(k) : -1;
           float z = -INFINITY, b = 0.f;
           double p = 0.0, c = -INFINITY;
           if (some) {
-            z = T::to_f32(a.logits[(row0 + r) * a.K + key_col(k)]), b = bias[key_col(k)];
+            z = lane < S ? zs[r * S + lane] : T::to_f32(a.logits[(row0 + r) * a.K + ck]);
+            b = bias[ck];
             const double e = exp(a.softmax ? (double)z - (double)info[2 * r] : -(double)z);
             p = a.softmax ? e * (double)info[2 * r + 1] : 1.0 / (1.0 + e);
             c = p + (double)b;
@@ -538,22 +538,33 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
           int rank = 0;
           bool last = false;
           for (int i = 0; i <= S; ++i) {
-            const double ci = __shfl(c, i), pi = __shfl(p, i);
-            const float zi = __shfl(z, i), bi = __shfl(b, i);
-            const uint32_t ki = __shfl(some ? key_col(k) : ~0u, i);
-            rank += ci > c || (ci == c && (some ? ki < key_col(k) : i < lane));
+            const double ci = lane_value(c, i);
+            const int ki = __builtin_amdgcn_readlane(ck, i);
+            rank += ci > c || (ci == c && (some ? ki < ck : i < lane));
             // (the error of 1 / sum is the same in both: 20 u of the probabilities' difference)
-            if (a.softmax && some && ci > -INFINITY && fabs(ci - c) <= 0x1p-19 * fabs(pi - p) + 0x1p-48 * (pi + p))
-              last |= zi != z || bi != b;
+            if (a.softmax && some && ki >= 0) {
+              const double pi = lane_value(p, i);
+              if (fabs(ci - c) <= 0x1p-19 * fabs(pi - p) + 0x1p-48 * (pi + p))
+                last |= lane_value(z, i) != z || lane_value(b, i) != b;
+            }
           }
           if (__ballot(last)) {
-            if (lane == 0) flag[r] = kLast;
+            whole |= 1ull << r;
           } else if (lane <= S && rank < S) {
-            sel[r * S + rank] = some ? key_of(0.f, key_col(k)) : __hiloint2double((int)0xFF800000u, 0);
+            sel[r * S + rank] = some ? key_of(0.f, ck) : __hiloint2double((int)0xFF800000u, 0);
             zs[r * S + rank] = z;
           }
-          wave_sync();
         }
+        while (whole) {
+          const int r = __builtin_ctzll(whole);
+          whole &= whole - 1;
+          const int id = decide_row(a, row0 + r, bias, reinterpret_cast<double*>(lds + o.exact));
+          if (lane < S) {
+            sel[r * S + lane] = id < 0 ? __hiloint2double((int)0xFF800000u, 0) : key_of(0.f, id);
+            zs[r * S + lane] = id < 0 ? -INFINITY : T::to_f32(a.logits[(row0 + r) * a.K + id]);
+          }
+        }
+        wave_sync();
       }
     }
     if (a.renorm) {
@@ -569,11 +580,6 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       const int r = row_of(it);
       const float z = zs[it];
       const int64_t at = row0 * S + it;
-      if (MODE == kScored && flag[r] & kLast) {
-        a.ids[at] = kUnsure;
-        again = true;
-        continue;
-      }
       const bool nan = is_nan_bits(z);
       const bool out = nan || !(z > -INFINITY);
       float w;
@@ -589,17 +595,6 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : 4) void route_rows_kernel(RouteA
       a.chosen[at] = nan ? __uint_as_float(0x7FC00000u) : out ? -INFINITY : z;
     }
     if constexpr (MODE == kScored) fetch(t + waves);  // (no earlier: it would push the row out)
-  }
-  if constexpr (MODE == kScored) {
-    if (!__ballot(again)) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the marks that this wave's lanes have written
-    for (int64_t t = t0; t < tiles; t += waves) {
-      uint64_t rows = __ballot(lane < SL && t * SL + lane < a.n && a.ids[(t * SL + lane) * S] == kUnsure);
-      while (rows) {
-        route_row_exact<T, true>(a, t * SL + __builtin_ctzll(rows), reinterpret_cast<double*>(lds));
-        rows &= rows - 1;
-      }
-    }
   }
 }
 
