@@ -1,5 +1,10 @@
 // Gradient of the routing weights with respect to the logits (formulas in flashkm_train.h).
-#include "route.h"
+//
+// Renormalised weights and sigmoids reach only the selected logits: a thread takes a selection, a row's sums are taken
+// over LDS, and what is left is to write the rows (or, accumulating, to add to S elements of each).  Softmax without
+// renormalisation reaches every choice: a team of lanes holds a row and its probabilities, and finds the selections'
+// derivatives in LDS.
+#include "route_rows.h"
 
 namespace fkm {
 
@@ -19,64 +24,314 @@ struct GradArgs {
   typename T::raw* dlogits;
 };
 
-// One row by one wave; lane j holds selection j.
-template <class T>
-__global__ __launch_bounds__(256) void route_grad_simple_kernel(GradArgs<T> a) {
-  const int lane = lane_id();
-  const bool dense = a.softmax && !a.renorm;
-  for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.n; row += (int64_t)gridDim.x * 4) {
-    const int64_t at = row * a.S + lane;
-    const uint32_t id = lane < a.S ? (uint32_t)a.ids[at] : ~0u;
+// ---------------------------------------------------------------------------
+// gradients of the selected logits only
+// ---------------------------------------------------------------------------
+// A workgroup takes R rows, a thread one selection of them.  Fresh gradients are laid out in LDS as the rows are in
+// memory (with the same address modulo 16), zeros with the selections' derivatives among them, and leave in 16-byte
+// words whatever K and the address; of rows longer than the tile a workgroup takes `width` columns of one.  Bound by the
+// bytes written.  Accumulated, a selection's element is read, added to and written by its thread: bound by the sectors
+// that these touch, two a selection.
+constexpr int kGradTile = 16384;  // bytes of rows in LDS
+
+template <class T, bool ACC>
+__global__ __launch_bounds__(256) void route_grad_items_kernel(GradArgs<T> a, int R, int width, int parts,
+                                                               int64_t tiles) {
+  constexpr int V = 16 / T::SZ;
+  __shared__ __align__(16) uint4 tile[ACC ? 1 : kGradTile / 16 + 2];
+  __shared__ float zs[256], es[256], gs[256];
+  __shared__ uint32_t is[256];
+  const int tid = threadIdx.x, S = a.S;
+  const int r = tid / S, first = r * S;  // the thread's row, and its first selection's thread
+  for (int64_t u = blockIdx.x; u < tiles; u += gridDim.x) {
+    const int64_t row0 = parts == 1 ? u * R : u / parts;
+    const int c0 = parts == 1 ? 0 : (int)(u - row0 * parts) * width;
+    const int rows = (int)(a.n - row0 < R ? a.n - row0 : R);
+    const int cols = a.K - c0 < width ? a.K - c0 : width;
+    const bool item = tid < rows * S;
+    const int64_t at = row0 * S + tid;
+    const uint32_t id = item ? (uint32_t)a.ids[at] : ~0u;
     const bool live = id < (uint32_t)a.K;
     const float g = live ? a.scale * a.dweights[at] : 0.f;
-    const typename T::raw* x = dense ? a.logits + row * a.K : nullptr;
-    typename T::raw* out = a.dlogits + row * a.K;
-    float d = 0.f, high = -INFINITY, inv = 0.f, mean = 0.f;
-    const bool any = __ballot(live) != 0;
-    if (dense) {
-      for (int k = lane; any && k < a.K; k += 64) high = fmaxf(high, T::to_f32(x[k]));
-      high = team_max<64>(high);
-      float s = 0.f;
-      for (int k = lane; any && k < a.K; k += 64) s += exp_diff<F32>(T::to_f32(x[k]), high);
-      inv = any ? 1.f / team_sum<64>(s) : 0.f;
-      mean = team_sum<64>(live ? g * exp_diff<F32>(T::to_f32(x[id]), high) * inv : 0.f);
-      d = g;
+    const float z = live ? a.chosen[at] : -INFINITY;
+    typename T::raw* mine = a.dlogits + (row0 + r) * a.K + id;  // (live only)
+    float old = 0.f;
+    if constexpr (ACC) old = live ? T::to_f32(*mine) : 0.f;
+    typename T::raw* from = a.dlogits + row0 * a.K + c0;
+    const int shift = (int)(((uintptr_t)from & 15) / T::SZ);
+    const int count = parts == 1 ? rows * a.K : cols;
+    const int words = (shift + count + V - 1) / V;
+    if constexpr (!ACC) {
+      for (int i = tid; i < words; i += 256) tile[i] = make_uint4(0, 0, 0, 0);
+    }
+    is[tid] = id;
+    float d;
+    if (a.renorm) {
+      zs[tid] = z;
+      __syncthreads();
+      float m = -INFINITY;
+      if (item)
+        for (int j = 0; j < S; ++j) m = fmaxf(m, zs[first + j]);
+      const float t = live ? share_term(z, share_shift(m, a.softmax), a.softmax) : 0.f;
+      es[tid] = t, gs[tid] = t * g;
+      __syncthreads();
+      float sum = 0.f, dot = 0.f;
+      if (item)
+        for (int j = 0; j < S; ++j) sum += es[first + j], dot += gs[first + j];
+      d = live ? t / sum * (g - dot / sum) : 0.f;
+      if (!a.softmax && live) d *= 1.f / (1.f + exp_to(z));
     } else {
-      const float z = live ? a.chosen[at] : -INFINITY;
-      if (a.renorm) {
-        const float shift = share_shift(team_max<64>(z), a.softmax);
-        const float t = live ? share_term(z, shift, a.softmax) : 0.f;
-        const float w = t / team_sum<64>(t);
-        mean = team_sum<64>(live ? w * g : 0.f);
-        d = w * (g - mean);
-        if (!a.softmax) d *= 1.f / (1.f + exp_to(z));
-      } else {
-        d = g * (1.f / (1.f + exp_to(-z))) * (1.f / (1.f + exp_to(z)));
+      d = live ? g * (1.f / (1.f + exp_to(-z))) * (1.f / (1.f + exp_to(z))) : 0.f;
+    }
+    zs[tid] = d;  // (every thread has read its row's logits before the barrier above)
+    __syncthreads();
+    // the same id again in a row adds up, and its first selection writes
+    if (live) {
+      float total = 0.f;
+      bool lead = true;
+      for (int j = 0; j < S; ++j)
+        if (is[first + j] == id) {
+          total += zs[first + j];
+          if (first + j < tid) lead = false;
+        }
+      if constexpr (ACC) {
+        if (lead) *mine = round_to<T>(old + total);
+      } else if (lead && id - (uint32_t)c0 < (uint32_t)cols) {
+        reinterpret_cast<typename T::raw*>(tile)[shift + (parts == 1 ? r * a.K : 0) + (id - c0)] = round_to<T>(total);
       }
     }
-    for (int64_t k0 = 0; k0 < a.K; k0 += 64) {
-      const int64_t k = k0 + lane;
-      float sum = 0.f;
-      bool hit = dense && any;
-      for (int j = 0; j < a.S; ++j) {
-        const uint32_t ij = __shfl(id, j);
-        const float dj = __shfl(d, j);
-        if (ij < (uint32_t)a.K && ij == (uint64_t)k) sum += dj, hit = true;
+    __syncthreads();
+    if constexpr (!ACC) {
+      for (int i = tid; i < words; i += 256) {
+        typename T::raw* to = from - shift + i * V;
+        Pack<T, V> p;
+        p.load(reinterpret_cast<const typename T::raw*>(tile + i));
+        if (i * V >= shift && (i + 1) * V <= shift + count) p.store_nt(to);
+        else p.store_range(to, shift - i * V > 0 ? shift - i * V : 0, shift + count - i * V < V ? shift + count - i * V : V);
       }
-      if (k >= a.K) continue;
-      if (dense) sum = any ? exp_diff<F32>(T::to_f32(x[k]), high) * inv * (sum - mean) : 0.f;
-      if (!hit && a.accumulate) continue;
-      out[k] = round_to<T>(a.accumulate ? T::to_f32(out[k]) + sum : sum);
+      __syncthreads();  // the tile is laid out again
     }
   }
 }
 
+// ---------------------------------------------------------------------------
+// gradients of whole rows
+// ---------------------------------------------------------------------------
+// d = p (g - sum p g), g the derivatives of the selections of a choice.  Rows of K <= LPR * E choices stay in a team's
+// registers; a wave's rows have their g in its LDS, zero but for the selections, which clear it again.
+template <class T, int E, int LPR>
+__global__ __launch_bounds__(256) void route_grad_rows_kernel(GradArgs<T> a, bool loose, uint32_t magic) {
+  using Sl = Slice<T, E, LPR>;
+  constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR, ROW = LPR * E;
+  __shared__ __align__(16) float lds_all[4 * SL * ROW];
+  const int lane = lane_id(), slot = lane / LPR, g = lane % LPR, S = a.S;
+  float* lds = lds_all + (threadIdx.x >> 6) * SL * ROW;
+  for (int i = lane; i < SL * ROW; i += 64) lds[i] = 0.f;
+  wave_sync();
+  const int64_t tiles = (a.n + SL - 1) / SL, waves = (int64_t)gridDim.x * 4;
+  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < tiles; t += waves) {
+    const int64_t row0 = t * SL, row = row0 + slot;
+    const int items = (int)(a.n - row0 < SL ? a.n - row0 : SL) * S;
+    Sl s;
+    s.template load<true>(a.logits + row * a.K, a.K, g, loose, row < a.n);
+    // selections of one id add up in their order: a row's by one lane where an id comes again
+    bool again = false;
+    for (int it = lane; it < items; it += 64) {
+      const int r = (int)(((uint32_t)it * magic) >> 20);
+      const uint32_t id = (uint32_t)a.ids[row0 * S + it];
+      if (id < (uint32_t)a.K) {
+        const float w = a.scale * a.dweights[row0 * S + it];
+        again |= atomicExch(&lds[r * ROW + id], w) != 0.f;
+      }
+    }
+    wave_sync();
+    if (__ballot(again)) {
+      for (int it = lane; it < items; it += 64) {
+        const uint32_t id = (uint32_t)a.ids[row0 * S + it];
+        if (id < (uint32_t)a.K) lds[(int)(((uint32_t)it * magic) >> 20) * ROW + id] = 0.f;
+      }
+      wave_sync();
+      if (lane < SL && row0 + lane < a.n)
+        for (int j = 0; j < S; ++j) {
+          const int64_t at = (row0 + lane) * S + j;
+          const uint32_t id = (uint32_t)a.ids[at];
+          if (id < (uint32_t)a.K) lds[lane * ROW + id] += a.scale * a.dweights[at];
+        }
+      wave_sync();
+    }
+    // rows with a selection
+    uint64_t some = 0;
+    for (int it = lane; it < ((items + 63) & ~63); it += 64) {
+      const bool in = it < items && (uint32_t)a.ids[row0 * S + it] < (uint32_t)a.K;
+      const int r = (int)(((uint32_t)it * magic) >> 20);
+      some |= in ? 1ull << (r & 63) : 0ull;
+    }
+    some |= (uint64_t)__shfl_xor((long long)some, 1), some |= (uint64_t)__shfl_xor((long long)some, 2);
+    some |= (uint64_t)__shfl_xor((long long)some, 4), some |= (uint64_t)__shfl_xor((long long)some, 8);
+    some |= (uint64_t)__shfl_xor((long long)some, 16), some |= (uint64_t)__shfl_xor((long long)some, 32);
+    const bool any = some >> slot & 1;
+    float x[E], w[E];
+    s.values(x);
+    const float high = team_max<LPR>(max_of(x));
+#pragma unroll
+    for (int i = 0; i < E; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(lds + slot * ROW + Sl::first(i / V, g) + i % V);
+      w[i] = f.x, w[i + 1] = f.y, w[i + 2] = f.z, w[i + 3] = f.w;
+    }
+    const float shift = high == -INFINITY ? 0.f : high;
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] = exp_diff<T>(x[i], shift);
+    const float inv = 1.f / team_sum<LPR>(pair_sum(x));
+    float pw[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) x[i] *= inv, pw[i] = x[i] * w[i];
+    const float mean = team_sum<LPR>(pair_sum(pw));
+    wave_sync();
+    for (int it = lane; it < items; it += 64) {
+      const uint32_t id = (uint32_t)a.ids[row0 * S + it];
+      if (id < (uint32_t)a.K) lds[(int)(((uint32_t)it * magic) >> 20) * ROW + id] = 0.f;
+    }
+    wave_sync();
+    if (row < a.n && (any || !a.accumulate)) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = Sl::first(j, g), left = a.K - c;
+        if (left <= 0) continue;
+        typename T::raw* to = a.dlogits + row * a.K + c;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = any ? x[j * V + v] * (w[j * V + v] - mean) : 0.f;
+        Pack<T, V> p;
+        if (a.accumulate) {
+          float f[V];
+          p.zero();
+          if (!loose) p.load(to);
+          else if (left >= V) p.load_loose(to);
+          else p.load_head(to, left);
+          p.unpack(f);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += f[v];
+        }
+        p.pack(o);
+        if (!loose) p.store_nt(to);
+        else if (left >= V) p.store_loose(to);
+        else p.store_range(to, 0, left);
+      }
+    }
+  }
+}
+
+// Rows of any length, a workgroup each: the row's maximum and sum (fp32 over a thread's values, in 64 bits over its
+// groups of eight), then the row again.  The selections' elements are written last, by their threads.
+template <class T>
+__global__ __launch_bounds__(256) void route_grad_wide_kernel(GradArgs<T> a) {
+  __shared__ float tmp[2][4];
+  __shared__ uint32_t is[64];
+  __shared__ float gs[64];
+  const int tid = threadIdx.x, S = a.S;
+  const uint32_t K = a.K;
+  auto join = [&](float v, bool largest, int k) {
+    v = largest ? team_max<64>(v) : team_sum<64>(v);
+    if ((tid & 63) == 0) tmp[k][tid >> 6] = v;
+    __syncthreads();
+    const float* p = tmp[k];
+    return largest ? fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])) : (p[0] + p[1]) + (p[2] + p[3]);
+  };
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    __syncthreads();  // the row before is done with the LDS
+    if (tid < S) {
+      is[tid] = (uint32_t)a.ids[row * S + tid];
+      gs[tid] = is[tid] < K ? a.scale * a.dweights[row * S + tid] : 0.f;
+    }
+    const bool any = __syncthreads_or(tid < S && is[tid] < K);
+    const typename T::raw* x = a.logits + row * K;
+    typename T::raw* out = a.dlogits + row * K;
+    if (!any) {
+      if (!a.accumulate)
+        for (uint32_t k = tid; k < K; k += 256) out[k] = round_to<T>(0.f);
+      continue;
+    }
+    float m = -INFINITY;
+#pragma unroll 8
+    for (uint32_t k = tid; k < K; k += 256) m = fmaxf(m, T::to_f32(x[k]));
+    m = join(m, true, 0);
+    const float shift = m == -INFINITY ? 0.f : m;
+    double sum = 0.0;
+    for (uint32_t k = tid; k < K; k += 2048) {
+      float s = 0.f;
+#pragma unroll
+      for (uint32_t i = 0; i < 2048; i += 256) s += k + i < K ? exp_diff<F32>(T::to_f32(x[k + i]), shift) : 0.f;
+      sum += (double)s;
+    }
+    const float inv = 1.f / join((float)sum, false, 1);
+    // the sum of a choice's derivatives, its probability, and its old value
+    float mine = 0.f, p = 0.f, old = 0.f;
+    bool lead = false;
+    if (tid < S && is[tid] < K) {
+      lead = true;
+      for (int j = 0; j < S; ++j)
+        if (is[j] == is[tid]) {
+          mine += gs[j];
+          if (j < tid) lead = false;
+        }
+      p = exp_diff<F32>(T::to_f32(x[is[tid]]), shift) * inv;
+      if (a.accumulate) old = T::to_f32(out[is[tid]]);
+    }
+    __syncthreads();  // (tmp is free, and the old values are read)
+    const float mean = join(lead ? p * mine : 0.f, false, 0);
+#pragma unroll 4
+    for (uint32_t k = tid; k < K; k += 256) {
+      const float d = -mean * (exp_diff<F32>(T::to_f32(x[k]), shift) * inv);
+      out[k] = round_to<T>(a.accumulate ? T::to_f32(out[k]) + d : d);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the row's values have arrived before the selections' are sent
+    __syncthreads();
+    if (lead) out[is[tid]] = round_to<T>(old + p * (mine - mean));
+  }
+}
+
+template <class T, int E, int LPR>
+hipError_t grad_rows(const GradArgs<T>& a, hipStream_t s) {
+  constexpr int SL = 64 / LPR, V = 16 / T::SZ;
+  const int64_t blocks = ((a.n + SL - 1) / SL + 3) / 4, most = 256 * 16;
+  const bool loose = a.K % V != 0 || (uintptr_t)a.logits % 16 != 0 || (uintptr_t)a.dlogits % 16 != 0;
+  route_grad_rows_kernel<T, E, LPR><<<dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s>>>(
+      a, loose, ((1u << 20) + a.S - 1) / a.S);
+  return hipGetLastError();
+}
+
+int64_t grid_of(int64_t tiles) { return tiles < (1 << 22) ? tiles : (1 << 22); }
+
 template <class T>
 hipError_t route_grad_t(const RouteGradCall& c, hipStream_t s) {
-  GradArgs<T> a{static_cast<const typename T::raw*>(c.logits), c.n, c.K, c.ids, c.chosen, c.dweights, c.S, c.softmax,
-                c.renorm, c.scale, c.accumulate, static_cast<typename T::raw*>(c.dlogits)};
-  const int64_t blocks = (a.n + 3) / 4;
-  route_grad_simple_kernel<T><<<dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0, s>>>(a);
+  const GradArgs<T> a{static_cast<const typename T::raw*>(c.logits), c.n, c.K, c.ids, c.chosen, c.dweights, c.S, c.softmax,
+                      c.renorm, c.scale, c.accumulate, static_cast<typename T::raw*>(c.dlogits)};
+  if (a.softmax && !a.renorm) {
+    if (a.K <= 8) return grad_rows<T, 8, 1>(a, s);
+    if (a.K <= 16) return grad_rows<T, 16, 1>(a, s);
+    if (a.K <= 32) return grad_rows<T, 16, 2>(a, s);
+    if (a.K <= 64) return grad_rows<T, 16, 4>(a, s);
+    if (a.K <= 128) return grad_rows<T, 16, 8>(a, s);
+    if (a.K <= 256) return grad_rows<T, 16, 16>(a, s);
+    if (a.K <= 512) return grad_rows<T, 16, 32>(a, s);
+    if (a.K <= 1024) return grad_rows<T, 16, 64>(a, s);
+    if (a.K <= 2048) return grad_rows<T, 32, 64>(a, s);
+    route_grad_wide_kernel<T><<<dim3((unsigned)grid_of(a.n)), dim3(256), 0, s>>>(a);
+    return hipGetLastError();
+  }
+  int R = 256 / a.S;
+  if (a.accumulate) {
+    const int64_t tiles = (a.n + R - 1) / R;
+    route_grad_items_kernel<T, true><<<dim3((unsigned)grid_of(tiles)), dim3(256), 0, s>>>(a, R, a.K, 1, tiles);
+    return hipGetLastError();
+  }
+  constexpr int most = kGradTile / T::SZ;  // elements of a tile
+  const int fit = a.K <= most ? most / a.K : 1;
+  if (R > fit) R = fit;
+  const int parts = (int)(((int64_t)a.K + most - 1) / most);
+  const int64_t tiles = parts == 1 ? (a.n + R - 1) / R : a.n * parts;
+  route_grad_items_kernel<T, false><<<dim3((unsigned)grid_of(tiles)), dim3(256), 0, s>>>(
+      a, R, parts == 1 ? a.K : most, parts, tiles);
   return hipGetLastError();
 }
 
