@@ -13,6 +13,7 @@ centroids are [K, D] or [B, K, D] fp32.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import inspect
@@ -675,9 +676,9 @@ def route(logits, S: int, *, score: str = "softmax", bias=None, groups: int = 1,
     if not 1 <= S <= 64:  # (no outputs of a size that the call refuses)
         raise KMeansError(KM_EINVAL if S < 1 else KM_EUNSUPPORTED, f"S={S} must be 1 to 64")
     shape = (*lead, S)
-    ids = torch.empty(shape, dtype=torch.int32, device=logits.device)
-    weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    chosen = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    ids = logits.new_empty(shape, dtype=torch.int32)
+    weights = torch.empty_like(ids, dtype=torch.float32)
+    chosen = torch.empty_like(weights)
     groups = _int32(groups, "groups")
     _check(_lib.kmeans_route(logits.data_ptr(), dt, lead.numel(), K, _at(bias), _score(score), groups,
                              groups if top_groups is None else _int32(top_groups, "top_groups"),
@@ -863,7 +864,7 @@ def adamw(plan: AdamWPlan, *, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, w
     if skip is not None and (not isinstance(skip, torch.Tensor) or skip.dtype not in (torch.bool, torch.uint8)):
         raise KMeansError(KM_EINVAL, "skip must be a bool or uint8 CUDA tensor")
     skip_at = _scalar_at(skip, "skip", skip.dtype if skip is not None else None, device)
-    with torch.cuda.device(device):
+    with contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device):
         raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
         if raw != plan._stream:  # the table must outlive the step there
             on = stream if stream is not None else torch.cuda.current_stream()

@@ -312,6 +312,16 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
     } else {
       float x[E];
       now.values(x);
+      // x = f(i, bias of element i), but for choices that are out (all is computed and then chosen from: no branches)
+      auto add_bias = [&](auto f) {
+#pragma unroll
+        for (int i = 0; i < E; i += 4) {
+          const float4 b = *reinterpret_cast<const float4*>(bias + Sl::first(i / V, g) + i % V);
+          const float c[4] = {f(i, b.x), f(i + 1, b.y), f(i + 2, b.z), f(i + 3, b.w)};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) x[i + v] = x[i + v] == -INFINITY ? -INFINITY : c[v];
+        }
+      };
       if (!sums) {
         bad = (__ballot(now.has_nan()) & team) != 0;
       } else {
@@ -325,8 +335,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
         bad = sum != sum;  // (a NaN, or +inf - inf)
         if constexpr (MODE == kScored) {
           if (arith) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = x[i] == -INFINITY ? x[i] : fmaf(e[i], inv, bias[Sl::first(i / V, g) + i % V]);
+            add_bias([&](int i, float b) { return fmaf(e[i], inv, b); });
           }
         }
       }
@@ -336,11 +345,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
       } else {
         int unsure = 0;
         if (arith && !a.softmax) {
-#pragma unroll
-          for (int i = 0; i < E; ++i)
-            x[i] = x[i] == -INFINITY
-                       ? x[i]
-                       : quick_sigmoid(x[i]) + bias[Sl::first(i / V, g) + i % V];
+          add_bias([&](int i, float b) { return quick_sigmoid(x[i]) + b; });
         }
         bad = live && (bad || bias_nan);
         const float base = score_error(a.softmax, inv);
@@ -427,13 +432,13 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
           for (int i = 0; i < E; i += 4) {
             const int c = Sl::first(i / V, g) + i % V;
             if (fours) {
-              const float stays = c < a.K ? keep[slot * a.G + group_of(c)] : 0.f;
+              const float stays = keep[slot * a.G + group_of(c < a.K ? c : 0)];  // (beyond K all is -inf)
 #pragma unroll
               for (int v = 0; v < 4; ++v) x[i + v] = stays != 0.f ? x[i + v] : -INFINITY;
             } else {
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                x[i + v] = c + v < a.K && keep[slot * a.G + group_of(c + v)] != 0.f ? x[i + v] : -INFINITY;
+                x[i + v] = keep[slot * a.G + group_of(c + v < a.K ? c + v : 0)] != 0.f ? x[i + v] : -INFINITY;
             }
           }
           unsure = flag[slot];
