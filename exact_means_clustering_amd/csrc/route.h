@@ -41,12 +41,11 @@ __device__ __forceinline__ float share_shift(float high, bool softmax) {
   if (high == -INFINITY) return 0.f;
   return softmax ? high : fminf(high, 0.f);
 }
-// A chosen logit's score over exp(shift): its share of the row's sum, before the division.
+// A chosen logit's score over exp(shift): its share of the row's sum, before the division.  A sigmoid is
+// exp(z) / (1 + exp(z)), for z > 0 (where the shift is 0) 1 / (1 + exp(-z)).
 __device__ __forceinline__ float share_term(float z, float shift, bool softmax) {
-  const float e = exp_diff<F32>(z, shift);
-  if (softmax) return e;
-  // exp(z - shift) / (1 + exp(z)), or where that could overflow 1 / (1 + exp(-z)) (the shift is 0 then)
-  return z > 0.f ? 1.f / (1.f + exp_to(-z)) : e / (1.f + exp_to(z));
+  const float e = exp_diff<F32>(z > 0.f && !softmax ? 0.f : z, shift);
+  return softmax ? e : e * __builtin_amdgcn_rcpf(1.f + exp_diff<F32>(-fabsf(z), 0.f));
 }
 
 // A double as the halves that lane exchanges move.
@@ -65,6 +64,7 @@ __device__ __forceinline__ void swap32(uint32_t v, uint32_t& a, uint32_t& b) {
 }
 template <bool FAR>
 __device__ __forceinline__ void swap64(double v, double& a, double& b) {
+  asm("s_nop 1" : "+v"(v));  // (two wait states between a write by inline code and the swap that reads it)
   uint32_t la, lb, ha, hb;
   swap32<FAR>((uint32_t)__double2loint(v), la, lb);
   swap32<FAR>((uint32_t)__double2hiint(v), ha, hb);
@@ -92,7 +92,7 @@ __device__ __forceinline__ double wave_op(double v, Op op) {
   return op(a, b);
 }
 __device__ __forceinline__ double wave_max(double v) {
-  return wave_op(v, [](double a, double b) { return a < b ? b : a; });
+  return wave_op(v, [](double a, double b) { return __builtin_fmax(a, b); });
 }
 __device__ __forceinline__ uint32_t wave_min(uint32_t v) {
   auto d = [](uint32_t a, uint32_t b) { return a < b ? a : b; };
@@ -109,9 +109,8 @@ __device__ __forceinline__ uint32_t wave_min(uint32_t v) {
 
 // A value into the largest two, m1 >= m2.
 __device__ __forceinline__ void take2(double& m1, double& m2, double c) {
-  const double low = c < m1 ? c : m1;
-  m1 = c < m1 ? m1 : c;
-  m2 = m2 < low ? low : m2;
+  m2 = __builtin_fmax(m2, __builtin_fmin(m1, c));
+  m1 = __builtin_fmax(m1, c);
 }
 // The largest two of the values of all lanes of a wave, in every lane.
 __device__ __forceinline__ void wave_top2(double& m1, double& m2) {
@@ -147,14 +146,14 @@ __device__ __forceinline__ double worth_of(double m1, double m2, int best) {
 
 // The selections of one row with scores, by one wave in 64 bits: the choice of selection `lane`, or -1.  The K scores
 // stay in the wave's LDS (c).  The row is valid and has no NaN (nor +inf under softmax).  Few calls come here: the code is
-// kept small (one exponential, one quotient, no unrolled loops), since it is not in the instruction cache.
+// kept small (one exponential, one quotient), since it is seldom in the instruction cache (about 8 us with 256 choices).
 template <class T>
 __device__ __forceinline__ int decide_row(const RouteArgs<T>& a, int64_t row, const float* bias, double* c) {
   const int lane = lane_id();
   const uint32_t K = a.K, gs = K / a.G;
   const typename T::raw* x = a.logits + row * a.K;
   float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll 4
   for (uint32_t k = lane; k < K; k += 64) {
     const float f = T::to_f32(x[k]);
     top = fmaxf(top, f);
@@ -180,7 +179,7 @@ __device__ __forceinline__ int decide_row(const RouteArgs<T>& a, int64_t row, co
     double m1 = -INFINITY, m2 = -INFINITY;
     if (lane < a.G) {
       uint32_t k = lane % gs;  // (lanes start at different places: banks)
-#pragma unroll 1
+#pragma unroll 4
       for (uint32_t i = 0; i < gs; ++i) {
         take2(m1, m2, c[lane * gs + k]);
         k = k + 1 < gs ? k + 1 : 0;
@@ -189,18 +188,22 @@ __device__ __forceinline__ int decide_row(const RouteArgs<T>& a, int64_t row, co
     kept = groups_kept(worth_of(m1, m2, a.best), a.G, a.keep);
   }
   int id = -1;
-  double pc = INFINITY;
+  double pc = INFINITY, bc = -INFINITY;
   int64_t pk = -1;
+  uint32_t bk = ~0u;
+  bool look = true;  // every lane for its first choice, then the lane whose choice was taken for its next one
 #pragma unroll 1
   for (int j = 0; j < a.S; ++j) {
-    double bc = -INFINITY;
-    uint32_t bk = ~0u;
-#pragma unroll 1
-    for (uint32_t k = lane; k < K; k += 64) {
-      const double f = c[k];
-      if ((kept >> (a.G > 1 ? k / gs : 0) & 1) && (f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
+    if (look) {
+      bc = -INFINITY, bk = ~0u;
+#pragma unroll 4
+      for (uint32_t k = lane; k < K; k += 64) {
+        const double f = c[k];
+        if ((kept >> (a.G > 1 ? k / gs : 0) & 1) && (f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
+      }
     }
     if (!next_choice(bc, bk, pc, pk)) break;
+    look = bk == pk;
     if (lane == j) id = (int)pk;
   }
   return id;

@@ -25,14 +25,14 @@ hipError_t route_rows(const RouteArgs<T>& a, hipStream_t s) {
   int waves = 4;
   while (waves > 1 && waves * o.total * 4 > 40960) waves /= 2;
   const int64_t tiles = (a.n + SL - 1) / SL;
-  // waves that loop where there are many rows (1,048,576 x 8 bf16 12.4 us with 64 a CU, 13.5 with 32, 14.7 with 16;
-  // 65,536 x 256 fp32 in 8 groups 63 with 64, 54 with 32)
-  const int64_t want = (tiles + waves - 1) / waves, most = 256 * (MODE == kScored ? 32 : 64) / waves;
+  // waves that loop where there are many rows (262,144 x 1,024 bf16, 8 a row, 201 us with 64 a CU, 216 with 24; 65,536 x
+  // 256 fp32 in 8 groups with a bias 41 us with 24, 44 with 20, 49 with 16, 54 with 64)
+  const int64_t want = (tiles + waves - 1) / waves, most = 256 * (MODE == kScored ? 24 : 64) / waves;
   const bool loose = a.K % V != 0 || (uintptr_t)a.logits % 16 != 0;
   route_rows_kernel<T, E, LPR, L, MODE>
       <<<dim3((unsigned)(want < most ? want : most)), dim3(64 * waves),
-         waves * o.total * 4 + (MODE == kScored ? LPR * E * 4 : 0), s>>>(
-          a, loose, o, ((1u << 20) + a.S - 1) / a.S);
+         waves * o.total * 4 + (MODE == kScored ? LPR * E * 4 + 16 : 0), s>>>(
+          a, loose, o, ((1u << 20) + a.S - 1) / a.S, ((1u << 20) + a.G - 1) / a.G);
   return hipGetLastError();
 }
 

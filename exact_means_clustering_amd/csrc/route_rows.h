@@ -30,9 +30,21 @@ __device__ __forceinline__ uint32_t key_col(double k) {
   return ~((uint32_t)__double2loint(k) ^ (uint32_t)(__double2hiint(k) >> 31));
 }
 
+// The larger and the smaller key.  (As instructions: the compiler would first quiet a NaN in each key that comes from
+// integers, one v_max_f64 more for each, and no key is one.)
+__device__ __forceinline__ double key_max(double a, double b) {
+  double m;
+  asm("v_max_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+  return m;
+}
+__device__ __forceinline__ double key_min(double a, double b) {
+  double m;
+  asm("v_min_f64 %0, %1, %2" : "=v"(m) : "v"(a), "v"(b));
+  return m;
+}
 // a >= b afterwards
 __device__ __forceinline__ void exchange(double& a, double& b) {
-  const double h = __builtin_fmax(a, b), l = __builtin_fmin(a, b);
+  const double h = key_max(a, b), l = key_min(a, b);
   a = h, b = l;
 }
 // Odd-even merge sort, descending.
@@ -52,7 +64,7 @@ __device__ __forceinline__ void sort_keys(double (&a)[L]) {
 template <int L>
 __device__ __forceinline__ void merge_keys(double (&a)[L], const double (&b)[L]) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) a[i] = __builtin_fmax(a[i], b[L - 1 - i]);
+  for (int i = 0; i < L; ++i) a[i] = key_max(a[i], b[L - 1 - i]);
 #pragma unroll
   for (int h = L / 2; h >= 1; h /= 2)
 #pragma unroll
@@ -141,12 +153,12 @@ struct Slice {
       const uint32_t inf = neg_inf_bits<T>() & 0x7FFFu;
       return m[0] > inf || m[1] > inf;
     } else {
-      uint32_t m = 0;
+      bool nan = false;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m = max(m, p[j].w[i] & 0x7FFFFFFFu);
-      return m > 0x7F800000u;
+        for (int i = 0; i < 4; ++i) nan |= __uint_as_float(p[j].w[i]) != __uint_as_float(p[j].w[i]);
+      return nan;
     }
   }
 };
@@ -207,10 +219,11 @@ struct RouteLds {
   int worth, z, e, exact, info, flag, extra, total;
   static __host__ __device__ RouteLds of(int SL, int K, int G, int S, bool scored) {
     RouteLds o{};
-    // groups first: a row's scores (or the largest two of four), its groups' worths, their errors, and whether they stay
-    const int scores = G > 1 ? SL * ((K + 3) & ~3) : 0;
-    o.worth = scores;
-    const int groups = scores + (G > 1 ? 3 * SL * G : 0);
+    // groups first: a row's scores (or the largest two of four, and a place a group), its groups' worths, and whether
+    // they stay
+    const int fours = 2 * SL * (K / 4 + G), ones = SL * ((K + 3) & ~3);
+    o.worth = G > 1 ? (fours > ones ? fours : ones) : 0;
+    const int groups = o.worth + (G > 1 ? 2 * SL * G : 0);
     // then, in the same place, the selections: keys, logits, shares before the division
     o.z = 2 * SL * S, o.e = o.z + SL * S;
     int at = o.e + SL * S;
@@ -231,7 +244,8 @@ constexpr int kOpen = 2, kLast = 1;  // a row whose candidates are put in order 
 enum RouteMode { kPlain, kWide, kScored };
 
 template <class T, int E, int LPR, int L, RouteMode MODE>
-__global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 : 4) void route_rows_kernel(RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic) {
+__global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 : 4) void route_rows_kernel(
+    RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic, uint32_t group_magic) {
   using Sl = Slice<T, E, LPR>;
   constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR;
   extern __shared__ __align__(16) float lds_all[];
@@ -260,14 +274,23 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
   // the bias, with zeros where there is none, for all of the workgroup's waves
   const float* bias = lds_all + (blockDim.x >> 6) * o.total;
   bool bias_nan = false;
+  float bias_max = 0.f;  // largest finite magnitude
   if constexpr (MODE == kScored) {
     float* b = lds_all + (blockDim.x >> 6) * o.total;
-    int nan = 0;
+    float* high = b + LPR * E;  // of each wave
+    bool nan = false;
+    float mine = 0.f;
     for (int k = threadIdx.x; k < LPR * E; k += blockDim.x) {
-      b[k] = a.bias && k < a.K ? a.bias[k] : 0.f;
-      nan |= is_nan_bits(b[k]);
+      const float f = a.bias && k < a.K ? a.bias[k] : 0.f;
+      b[k] = f;
+      nan |= is_nan_bits(f);
+      if (fabsf(f) < INFINITY) mine = fmaxf(mine, fabsf(f));
     }
-    bias_nan = __syncthreads_or(nan);
+    mine = team_max<64>(mine);
+    const bool none = __ballot(nan) != 0;
+    if (lane == 0) high[threadIdx.x >> 6] = none ? -1.f : mine;
+    __syncthreads();
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) bias_nan |= high[w] < 0.f, bias_max = fmaxf(bias_max, high[w]);
   }
   for (; t < tiles; t += waves) {
     const int64_t row0 = t * SL, row = row0 + slot;
@@ -354,21 +377,21 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
           const int gs = a.K / a.G;
           const float per = 1.f / (float)gs;
           auto group_of = [&](int k) { return (int)(((float)k + 0.5f) * per); };  // (exact: k < 2,048)
-          float *worth = lds + o.worth, *werr = worth + SL * a.G, *keep = werr + SL * a.G;
+          float *worth = lds + o.worth, *keep = worth + SL * a.G;
           wave_sync();  // (the tile before is done with it)
           if (g == 0) info[2 * slot] = base;
           if (lane < SL) flag[lane] = 0;
           const bool fours = gs % 4 == 0;
           if (fours) {
-            // four neighbours of a group leave their largest two
-            float2* mine = reinterpret_cast<float2*>(lds) + slot * (a.K / 4);
+            // four neighbours of a group leave their largest two; between groups one place stays empty (banks)
+            float2* mine = reinterpret_cast<float2*>(lds) + slot * (a.K / 4 + a.G);
 #pragma unroll
             for (int i = 0; i < E; i += 4) {
               const int c = Sl::first(i / V, g) + i % V;
               const float h0 = fmaxf(x[i], x[i + 1]), l0 = fminf(x[i], x[i + 1]);
               const float h1 = fmaxf(x[i + 2], x[i + 3]), l1 = fminf(x[i + 2], x[i + 3]);
               if (c < a.K)
-                mine[c / 4] = make_float2(fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1)));
+                mine[c / 4 + group_of(c)] = make_float2(fmaxf(h0, h1), fmaxf(fminf(h0, h1), fmaxf(l0, l1)));
             }
           } else {
             float* mine = lds + slot * ((a.K + 3) & ~3);
@@ -380,50 +403,43 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
           }
           wave_sync();
           for (int it = lane; it < SL * a.G; it += 64) {
-            const int r = it / a.G, gr = it - r * a.G;
+            const int r = (int)(((uint32_t)it * group_magic) >> 20), gr = it - r * a.G;
             float m1 = -INFINITY, m2 = -INFINITY;
-            const int steps = fours ? gs / 4 : gs;
-            int k = it % steps;  // (lanes start at different places: banks)
             if (fours) {
-              const float2* p = reinterpret_cast<const float2*>(lds) + r * (a.K / 4) + gr * steps;
-#pragma unroll 8
-              for (int i = 0; i < steps; ++i) {
-                const float2 c = p[k];
+              const float2* p = reinterpret_cast<const float2*>(lds) + r * (a.K / 4 + a.G) + gr * (gs / 4 + 1);
+#pragma unroll 4
+              for (int i = 0; i < gs / 4; ++i) {
+                const float2 c = p[i];
                 m2 = fmaxf(fmaxf(m2, c.y), fminf(m1, c.x));
                 m1 = fmaxf(m1, c.x);
-                k = k + 1 < steps ? k + 1 : 0;
               }
             } else {
-              const float* p = lds + r * ((a.K + 3) & ~3) + gr * steps;
+              const float* p = lds + r * ((a.K + 3) & ~3) + gr * gs;
 #pragma unroll 4
-              for (int i = 0; i < steps; ++i) {
-                const float c = p[k];
+              for (int i = 0; i < gs; ++i) {
+                const float c = p[i];
                 m2 = fmaxf(m2, fminf(m1, c));
                 m1 = fmaxf(m1, c);
-                k = k + 1 < steps ? k + 1 : 0;
               }
             }
-            const bool two = a.best == 2 && m2 > -INFINITY;
-            worth[it] = two ? m1 + m2 : m1;
-            werr[it] = arith && m1 > -INFINITY
-                           ? kU * (2.f * info[2 * r] + 3.f * (fabsf(m1) + (two ? fabsf(m2) : 0.f))) + 0x1p-120f
-                           : 0.f;
+            worth[it] = a.best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
           }
           wave_sync();
           for (int it = lane; it < SL * a.G; it += 64) {
-            const int r = it / a.G, gr = it - r * a.G;
+            const int r = (int)(((uint32_t)it * group_magic) >> 20), gr = it - r * a.G;
             const float w = worth[it];
             int better = 0;
-            float err = 0.f, gap = INFINITY;  // the largest error, and the distance to the next group down
+            float gap = INFINITY;  // the distance to the next group down
 #pragma unroll 4
             for (int q = 0; q < a.G; ++q) {
               const float other = worth[r * a.G + q];
               const bool b = other > w || (other == w && q < gr);
               better += b;
-              err = fmaxf(err, werr[r * a.G + q]);
               if (!b && q != gr) gap = fminf(gap, w - other);
             }
-            // the last group that stays and the first that goes (worths of two groups without choices are not compared)
+            // the last group that stays and the first that goes (worths of two groups without choices are not compared);
+            // a worth is the sum of two c, none of them larger than 1 and the largest finite bias, whose errors add up
+            const float err = kU * (2.f * info[2 * r] + 4.f * (1.f + bias_max)) + 0x1p-119f;
             if (arith && better == a.keep - 1 && w > -INFINITY && gap <= 2.2f * err) flag[r] = kLast;
             keep[it] = better < a.keep ? 1.f : 0.f;
           }
@@ -453,15 +469,16 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
           for (int i = 1; i < L; ++i) last = i == S - 1 ? top[i] : last;
           const float vs = key_score(last);
           const float border = vs - 2.2f * (kU * (base + fabsf(vs)) + 0x1p-120f);
-          int count = 0;
+          uint32_t count = 0;  // (a comparison and an addition of its bit each)
 #pragma unroll
-          for (int i = 0; i < E; ++i) count += x[i] >= border;
-          count = (int)team_sum<LPR>((float)count);
-          const bool many = vs > -INFINITY && count > S && live && !bad;
+          for (int i = 0; i < E; ++i)
+            asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, 0, %0, vcc" : "+v"(count) : "v"(x[i]), "v"(border) : "vcc");
+          count = (uint32_t)team_sum<LPR>((float)count);
+          const bool many = vs > -INFINITY && (int)count > S && live && !bad;
           if (__ballot(many)) {  // the largest of them joins; others than it and its equals are for the end
             auto score = [&](int k, float& f, float& b) {
               f = T::to_f32(a.logits[row * a.K + k]), b = bias[k];
-              const bool out = a.G > 1 && lds[o.worth + (2 * SL + slot) * a.G + k / (a.K / a.G)] == 0.f;  // (stays?)
+              const bool out = a.G > 1 && lds[o.worth + (SL + slot) * a.G + k / (a.K / a.G)] == 0.f;  // (stays?)
               return out || f == -INFINITY ? -INFINITY
                      : a.softmax           ? fmaf(quick_exp(f, high), inv, b)
                                            : quick_sigmoid(f) + b;
@@ -475,7 +492,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
               }
             join_lists<1, LPR>(best);
             extra = best[0];
-            if (many && count > S + 1) {
+            if (many && (int)count > S + 1) {
               const float fe = T::to_f32(a.logits[row * a.K + key_col(extra)]), be = bias[key_col(extra)];
               for (int k = g; k < a.K; k += LPR) {
                 const double key = key_of(score(k, f, b), k);
@@ -493,6 +510,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
       }
     }
     if (a.softmax && !sums && key_score(top[0]) == INFINITY) bad = true;
+    if constexpr (MODE == kScored) fetch(t + waves);  // (no earlier: it would push the row out)
     // ---- the selections change hands: item it is selection it % S of row it / S
     wave_sync();
 #pragma unroll
@@ -591,15 +609,14 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
       if (a.renorm) {
         float sum = 0.f;
         for (int j = 0; j < S; ++j) sum += es[r * S + j];
-        w = a.scale * (es[it] / sum);
+        w = a.scale * (es[it] * __builtin_amdgcn_rcpf(sum));
       } else {
-        w = a.scale * (a.softmax ? exp_diff<F32>(z, info[2 * r]) * info[2 * r + 1] : 1.f / (1.f + exp_to(-z)));
+        w = a.scale * (a.softmax ? exp_diff<F32>(z, info[2 * r]) * info[2 * r + 1] : __builtin_amdgcn_rcpf(1.f + exp_to(-z)));
       }
       a.ids[at] = out ? -1 : (int32_t)key_col(sel[it]);
       a.weights[at] = nan ? __uint_as_float(0x7FC00000u) : out ? 0.f : w;
       a.chosen[at] = nan ? __uint_as_float(0x7FC00000u) : out ? -INFINITY : z;
     }
-    if constexpr (MODE == kScored) fetch(t + waves);  // (no earlier: it would push the row out)
   }
 }
 
