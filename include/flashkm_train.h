@@ -53,7 +53,9 @@ enum km_score { KM_SOFTMAX = 0, KM_SIGMOID = 1 };
  * Exactness of the ids: where c's order is the logits' own (no bias, and no
  * sums of two c as worths) it is taken from the logits, exactly.  Else it is
  * the order of c and of the worths in 64-bit arithmetic: rows in which 32 bits
- * could change it are decided in 64.
+ * could change it are decided in 64.  Values that differ by less than the
+ * rounding of 64-bit arithmetic (sums of equal parts in another order) come in
+ * the order that this rounding gives them.
  * A valid row with a NaN among its logits or the bias, or with a logit of +inf
  * under softmax, has no scores: its ids are -1, its weights and chosen NaN. */
 KM_API int kmeans_route(const void* logits, int32_t dtype, int64_t N, int32_t K, const float* bias, int32_t score,
