@@ -590,7 +590,16 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
         wave_sync();
       }
     }
-    if (a.renorm) {
+    // a row's selections are neighbouring lanes where S divides 64: their sums need no LDS
+    const bool lanes = a.renorm && S <= 16 && (S & (S - 1)) == 0;
+    auto over_row = [&](float v, auto op) {
+      if (S >= 2) v = op(v, dpp<0xB1>(v));
+      if (S >= 4) v = op(v, dpp<0x4E>(v));
+      if (S >= 8) v = op(v, dpp<0x141>(v));
+      if (S >= 16) v = op(v, dpp<0x140>(v));
+      return v;
+    };
+    if (a.renorm && !lanes) {
       for (int it = lane; it < items; it += 64) {
         const int r = row_of(it);
         float m = -INFINITY;
@@ -599,20 +608,27 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
       }
       wave_sync();
     }
-    for (int it = lane; it < items; it += 64) {
-      const int r = row_of(it);
-      const float z = zs[it];
-      const int64_t at = row0 * S + it;
-      const bool nan = is_nan_bits(z);
-      const bool out = nan || !(z > -INFINITY);
+    for (int it0 = 0; it0 < items; it0 += 64) {
+      const int it = it0 + lane;
+      const float z = it < items ? zs[it] : -INFINITY;
       float w;
-      if (a.renorm) {
+      if (lanes) {
+        const float m = over_row(z, [](float a, float b) { return fmaxf(a, b); });
+        const float t = z == -INFINITY ? 0.f : share_term(z, share_shift(m, a.softmax), a.softmax);
+        w = a.scale * (t * __builtin_amdgcn_rcpf(over_row(t, [](float a, float b) { return a + b; })));
+      }
+      if (it >= items) continue;
+      const int r = row_of(it);
+      if (a.renorm && !lanes) {
         float sum = 0.f;
         for (int j = 0; j < S; ++j) sum += es[r * S + j];
         w = a.scale * (es[it] * __builtin_amdgcn_rcpf(sum));
-      } else {
+      } else if (!a.renorm) {
         w = a.scale * (a.softmax ? exp_diff<F32>(z, info[2 * r]) * info[2 * r + 1] : __builtin_amdgcn_rcpf(1.f + exp_to(-z)));
       }
+      const int64_t at = row0 * S + it;
+      const bool nan = is_nan_bits(z);
+      const bool out = nan || !(z > -INFINITY);
       a.ids[at] = out ? -1 : (int32_t)key_col(sel[it]);
       a.weights[at] = nan ? __uint_as_float(0x7FC00000u) : out ? 0.f : w;
       a.chosen[at] = nan ? __uint_as_float(0x7FC00000u) : out ? -INFINITY : z;
