@@ -1,9 +1,14 @@
 // AdamW step over the tensors of a table (formulas in flashkm_train.h).
 //
 // Bound by bytes: a value's parameter, gradient and two states are read once and all but the gradient written once (28
-// bytes with fp32 everywhere, 20 in bf16 with fp32 copies and states in 8 bits).  A workgroup takes a chunk of 4,096
-// values of one tensor, a lane four neighbours at a time, so every access is up to 16 bytes a lane and a wave's four
-// times 64 values are one block of a scale: its largest magnitude is a reduction over the wave's lanes.
+// bytes with fp32 everywhere; 16 1/16 with bf16 parameters and gradients, fp32 copies and states in 8 bits; parameters
+// that have copies are not read).  A workgroup takes a chunk of 4,096 values of one tensor, a lane four neighbours at a
+// time, so every access is up to 16 bytes a lane and a wave's four times 64 values are one block of a scale: its largest
+// magnitude is a reduction over the wave's lanes.  Measured: 8.4 million fp32 values 40 us (5.9 TB/s), 124 million bf16
+// values with copies 605 (5.7), 350 million with states in 8 bits 983 (5.7; a copy of 4 GiB moves 4.7).  With 8 bits the
+// vector units are busy four fifths of that time: a third of the instructions are the codes and their scales.
+#include <type_traits>
+
 #include "kernels.h"
 #include "teams.h"
 #include "vecio.h"
@@ -57,25 +62,45 @@ struct E5M2 {
   }
 };
 
-// Codes of a wave's 256 values and their scale (in every lane).
+// Codes of a wave's 256 values and their scale (in every lane).  A NaN or an infinity leaves the others' scale alone: the
+// maximum passes a NaN over, and infinities are looked for only where it is one.
 template <class Q>
 __device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) {
-  float high = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float f = fabsf(x[e]);
-    high = f < INFINITY && f > high ? f : high;  // (a NaN or an infinity leaves the others' scale alone)
-  }
+  float high = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
   high = team_max<64>(high);
-  const float inv = high >= 0x1p-100f ? Q::kTop / high : 0.f;
-  scale = inv != 0.f ? high * (1.f / Q::kTop) : 0.f;
+  if (high == INFINITY) {  // uniform over the wave
+    high = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) high = fabsf(x[e]) < INFINITY ? fmaxf(high, fabsf(x[e])) : high;
+    high = team_max<64>(high);
+  }
+  const bool some = high >= 0x1p-100f;
+  const float inv = some ? Q::kTop / high : 0.f, least = some ? Q::kLeast : 0.f;
+  scale = some ? high * (1.f / Q::kTop) : 0.f;
   float y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     y[e] = x[e] * inv;
-    if (Q::kLeast > 0.f && inv != 0.f && x[e] > 0.f && y[e] < Q::kLeast) y[e] = Q::kLeast;
+    if (Q::kLeast > 0.f && x[e] > 0.f) y[e] = y[e] < least ? least : y[e];
   }
   return Q::pack(y);
+}
+
+// Square root to one unit in the last place.  (The instruction takes values below the normal range as 0: scaled first.)
+__device__ __forceinline__ float quick_sqrt(float v) {
+  const bool low = v < 0x1p-96f;
+  const float s = __builtin_amdgcn_sqrtf(low ? v * 0x1p64f : v);
+  return low ? s * 0x1p-32f : s;
+}
+
+// A pointer of the table: the same in all lanes (in scalar registers, so that accesses are an address and a lane's
+// distance from it) and to global memory (what is read from memory could be any address, which takes flat accesses).
+template <class X>
+__device__ __forceinline__ X* uniform(X* x) {
+  const uint64_t b = (uint64_t)x;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  typedef __attribute__((address_space(1))) X Global;
+  return (X*)(Global*)((uint64_t)hi << 32 | lo);
 }
 
 // The sums and products of m and v are rounded one by one, as the formula has them: what is held in 8 bits then does
@@ -100,9 +125,13 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
   const float gscale = live.gscale ? *live.gscale : 1.f;
   const int32_t* map = reinterpret_cast<const int32_t*>(table + map_at);
   for (int64_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const AdamItem t = reinterpret_cast<const AdamItem*>(table)[map[c]];
-    auto* p = static_cast<typename TP::raw*>(t.p);
-    auto* g = static_cast<const typename TG::raw*>(t.g);
+    AdamItem t = reinterpret_cast<const AdamItem*>(table)[map[c]];
+    auto* p = uniform(static_cast<typename TP::raw*>(t.p));
+    auto* g = uniform(static_cast<const typename TG::raw*>(t.g));
+    t.master = uniform(t.master), t.sm = uniform(t.sm), t.sv = uniform(t.sv);
+    using S = std::conditional_t<Q8, uint8_t, float>;
+    auto* tm = uniform(static_cast<S*>(t.m));
+    auto* tv = uniform(static_cast<S*>(t.v));
     const int64_t base = (c - t.first) * kAdamChunk;
     const float keep = 1.f - r.lr_wd * t.decay;
     auto at = [&](int u) { return base + u * 1024 + (int64_t)threadIdx.x * 4; };
@@ -114,12 +143,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
       if constexpr (STREAM) pack.store_nt(to);
       else pack.store(to);
     };
-    auto take4 = [](const void* from, int64_t i) {
-      const auto* q = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(from) + i);
+    auto take4 = [](const uint8_t* from, uint32_t i) {
+      const auto* q = reinterpret_cast<const uint32_t*>(from + i);
       return STREAM ? __builtin_nontemporal_load(q) : *q;
     };
-    auto put4 = [](void* to, int64_t i, uint32_t w) {
-      auto* q = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(to) + i);
+    auto put4 = [](uint8_t* to, uint32_t i, uint32_t w) {
+      auto* q = reinterpret_cast<uint32_t*>(to + i);
       if constexpr (STREAM) __builtin_nontemporal_store(w, q);
       else *q = w;
     };
@@ -130,13 +159,22 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
         const float gr = gv[e] * gscale;
         mv[e] = mv[e] * r.b1 + gr * r.c1;
         vv[e] = vv[e] * r.b2 + (gr * gr) * r.c2;
-        const float d = sqrtf(vv[e]) * r.root + r.eps;
+        // With states in 32 bits the root and the quotient are good to one unit each: 2^25 values in 166 us, 171 rounded
+        // in full.  With 8 bits a lane waits less for them, and in full they cost nothing (200 million values 525 us, 541).
+        const float d = (Q8 ? sqrtf(vv[e]) : quick_sqrt(vv[e])) * r.root + r.eps;
         // 0 / 0 only where eps is 0 and nothing has moved
-        const float q = mv[e] == 0.f && d == 0.f ? 0.f : mv[e] / d;
+        const float q = mv[e] == 0.f && d == 0.f ? 0.f : Q8 ? mv[e] / d : mv[e] * __builtin_amdgcn_rcpf(d);
         pv[e] = pv[e] * keep - q * r.rate;
       }
     };
     if (t.aligned && base + kAdamChunk <= t.numel) {  // uniform over the workgroup
+      // (one address for the workgroup, and a lane's distance from it)
+      const uint32_t own = threadIdx.x * 4;
+      auto* p0 = p + base;
+      const auto* g0 = g + base;
+      float* w0 = t.master + base;
+      auto *m0 = tm + base, *v0 = tv + base;
+      float *sm0 = t.sm + base / kAdamBlock, *sv0 = t.sv + base / kAdamBlock;
       Pack<TP, 4> pp[U];
       Pack<F32, 4> pm[U], m[U], v[U];
       Pack<TG, 4> gg[U];
@@ -144,22 +182,22 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
       float sm[U], sv[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t i = at(u);
-        if constexpr (MASTER) take(pm[u], t.master + i);
-        else take(pp[u], p + i);
-        take(gg[u], g + i);
+        const uint32_t i = own + u * 1024;
+        if constexpr (MASTER) take(pm[u], w0 + i);
+        else take(pp[u], p0 + i);
+        take(gg[u], g0 + i);
         if constexpr (Q8) {
-          mq[u] = take4(t.m, i);
-          vq[u] = take4(t.v, i);
-          sm[u] = t.sm[i / kAdamBlock], sv[u] = t.sv[i / kAdamBlock];
+          mq[u] = take4(m0, i);
+          vq[u] = take4(v0, i);
+          sm[u] = sm0[i / kAdamBlock], sv[u] = sv0[i / kAdamBlock];
         } else {
-          take(m[u], static_cast<const float*>(t.m) + i);
-          take(v[u], static_cast<const float*>(t.v) + i);
+          take(m[u], m0 + i);
+          take(v[u], v0 + i);
         }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t i = at(u);
+        const uint32_t i = own + u * 1024;
         float pv[4], gv[4], mv[4], vv[4];
         if constexpr (MASTER) pm[u].unpack(pv);
         else pp[u].unpack(pv);
@@ -175,22 +213,22 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
         }
         step(pv, gv, mv, vv);
         pp[u].pack(pv);
-        put(pp[u], p + i);
+        put(pp[u], p0 + i);
         if constexpr (MASTER) {
           pm[u].pack(pv);
-          put(pm[u], t.master + i);
+          put(pm[u], w0 + i);
         }
         if constexpr (Q8) {
           float a, b;
           const uint32_t ma = to_codes<E4M3>(mv, a), va = to_codes<E5M2>(vv, b);
-          put4(t.m, i, ma);
-          put4(t.v, i, va);
-          if (i % kAdamBlock == 0) t.sm[i / kAdamBlock] = a, t.sv[i / kAdamBlock] = b;
+          put4(m0, i, ma);
+          put4(v0, i, va);
+          if (i % kAdamBlock == 0) sm0[i / kAdamBlock] = a, sv0[i / kAdamBlock] = b;
         } else {
           m[u].pack(mv);
           v[u].pack(vv);
-          put(m[u], static_cast<float*>(t.m) + i);
-          put(v[u], static_cast<float*>(t.v) + i);
+          put(m[u], m0 + i);
+          put(v[u], v0 + i);
         }
       }
     } else {
@@ -205,11 +243,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
           pv[e] = MASTER ? t.master[i + e] : TP::to_f32(p[i + e]);
           gv[e] = TG::to_f32(g[i + e]);
           if constexpr (Q8) {
-            mq |= (uint32_t) static_cast<const uint8_t*>(t.m)[i + e] << 8 * e;
-            vq |= (uint32_t) static_cast<const uint8_t*>(t.v)[i + e] << 8 * e;
+            mq |= (uint32_t)tm[i + e] << 8 * e;
+            vq |= (uint32_t)tv[i + e] << 8 * e;
           } else {
-            mv[e] = static_cast<const float*>(t.m)[i + e];
-            vv[e] = static_cast<const float*>(t.v)[i + e];
+            mv[e] = tm[i + e];
+            vv[e] = tv[i + e];
           }
         }
         if constexpr (Q8) {
@@ -231,11 +269,11 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
           p[i + e] = round_to<TP>(pv[e]);
           if constexpr (MASTER) t.master[i + e] = pv[e];
           if constexpr (Q8) {
-            static_cast<uint8_t*>(t.m)[i + e] = (uint8_t)(mq >> 8 * e);
-            static_cast<uint8_t*>(t.v)[i + e] = (uint8_t)(vq >> 8 * e);
+            tm[i + e] = (uint8_t)(mq >> 8 * e);
+            tv[i + e] = (uint8_t)(vq >> 8 * e);
           } else {
-            static_cast<float*>(t.m)[i + e] = mv[e];
-            static_cast<float*>(t.v)[i + e] = vv[e];
+            tm[i + e] = mv[e];
+            tv[i + e] = vv[e];
           }
         }
       }
