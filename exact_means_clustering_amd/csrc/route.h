@@ -209,7 +209,10 @@ __device__ __forceinline__ int decide_row(const RouteArgs<T>& a, int64_t row, co
   return id;
 }
 
-// One row of any length by one wave, scores in 64 bits, computed again for each selection.
+// One row of any length by one wave, scores in 64 bits.  A lane keeps the kLaneBest best of its choices in registers, in
+// order; the best of the lanes' first is the row's next selection, and a lane that has given all of them looks for more
+// (they come in turn, so seldom).
+constexpr int kLaneBest = 8;
 template <class T>
 __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t row) {
   const int lane = lane_id();
@@ -259,18 +262,36 @@ __device__ __forceinline__ void route_row_exact(const RouteArgs<T>& a, int64_t r
       }
       kept = groups_kept(worth, a.G, a.keep);
     }
-    double pc = INFINITY;  // the selection before
+    double pc = INFINITY, best[kLaneBest];  // the selection before, and the lane's best
     int64_t pk = -1;
+    uint32_t at[kLaneBest];
+    int given = 0;
+    bool look = true, more = false;  // more: choices behind the lane's best
     for (int j = 0; j < a.S; ++j) {
-      double bc = -INFINITY;
-      uint32_t bk = ~0u;
-#pragma unroll 4
-      for (uint32_t k = lane; k < K; k += 64) {
-        if (!(kept >> (a.G > 1 ? k / gs : 0) & 1)) continue;
-        const double f = key(k);
-        if ((f < pc || (f == pc && k > pk)) && f > bc) bc = f, bk = k;
+      if (look) {
+#pragma unroll
+        for (int i = 0; i < kLaneBest; ++i) best[i] = -INFINITY, at[i] = ~0u;
+        for (uint32_t k = lane; k < K; k += 64) {
+          if (!(kept >> (a.G > 1 ? k / gs : 0) & 1)) continue;
+          const double f = key(k);
+          if (!(f > best[kLaneBest - 1]) || !(f < pc || (f == pc && k > pk))) continue;
+#pragma unroll
+          for (int i = kLaneBest - 1; i >= 0; --i) {  // (of equal scores the one in front came first)
+            const bool down = i > 0 && f > best[i > 0 ? i - 1 : 0], here = !down && f > best[i];
+            best[i] = down ? best[i > 0 ? i - 1 : 0] : here ? f : best[i];
+            at[i] = down ? at[i > 0 ? i - 1 : 0] : here ? k : at[i];
+          }
+        }
+        given = 0, more = best[kLaneBest - 1] > -INFINITY;
       }
-      if (!next_choice(bc, bk, pc, pk)) break;
+      if (!next_choice(best[0], at[0], pc, pk)) break;
+      look = false;
+      if (at[0] == pk) {
+#pragma unroll
+        for (int i = 0; i + 1 < kLaneBest; ++i) best[i] = best[i + 1], at[i] = at[i + 1];
+        best[kLaneBest - 1] = -INFINITY, at[kLaneBest - 1] = ~0u;
+        look = ++given == kLaneBest && more;
+      }
       if (lane == j) id = (int)pk;
     }
     if (id >= 0) z = T::to_f32(x[id]);

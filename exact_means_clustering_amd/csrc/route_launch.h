@@ -63,7 +63,8 @@ template <class T>
 hipError_t route_t(const RouteCall& c, hipStream_t s) {
   const RouteArgs<T> a{static_cast<const typename T::raw*>(c.logits), c.n, c.K, c.bias, c.groups, c.keep, c.best, c.S,
                        c.softmax, c.renorm, c.scale, c.valid, c.ids, c.weights, c.chosen};
-  // lists of more than 32 keys, and scores of rows longer than a wave's registers, are left to the kernel without either
+  // Lists of more than 32 keys, and scores of rows longer than a wave's registers, are left to the kernel without either
+  // (8,192 x 128 bf16 with 32 selections 26 us, with 33 42; 8,192 x 2,048 bf16 with a bias 80 us, x 4,096 252).
   if (a.S > 32 || (a.K > 2048 && (a.arith() || a.G > 1))) {
     const int64_t blocks = (a.n + 3) / 4;
     route_exact_kernel<T><<<dim3((unsigned)(blocks < (1 << 20) ? blocks : (1 << 20))), dim3(256), 0, s>>>(a);

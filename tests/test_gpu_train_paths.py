@@ -137,6 +137,27 @@ def test_route_of_long_rows(km, K, S):
         check_route(km.route(x.cuda(), S, bias=b.cuda(), score="sigmoid"), x, S, bias=b, score="sigmoid")
 
 
+@pytest.mark.parametrize("K, groups, S", [(8192, 1, 64), (8192, 64, 33), (8193, 3, 9), (2052, 4, 3), (40, 5, 36), (1, 1, 1)])
+def test_route_of_rows_taken_in_64_bits(km, K, groups, S):
+    """Rows with scores that are too long for a wave's registers, and more selections than its lists, or than a lane's
+    best; with equal scores, choices that are out and rows without any."""
+    n = 37
+    x = some_logits(n, K, F32, K)
+    x[1] = -math.inf
+    x[2, : K - K // 3] = -math.inf
+    x[3] = 0.25
+    x[4, ::2] = x[4, 0]
+    b = some_bias(K, 1)
+    valid = torch.ones(n, dtype=torch.bool)
+    valid[5] = False
+    for score in ("softmax", "sigmoid"):
+        kw = dict(score=score, groups=groups, top_groups=(groups + 1) // 2)
+        if S * groups > K * kw["top_groups"]:
+            kw["top_groups"] = groups
+        check_route(km.route(x.cuda(), S, bias=b.cuda(), valid=valid.cuda(), **kw), x, S, bias=b, valid=valid, **kw)
+        check_route(km.route(x.cuda(), S, renormalise=False, **kw), x, S, renormalise=False, **kw)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n, K, S", [(30_001, 64, 8), (9_001, 256, 5), (70_001, 8, 2), (3_001, 1024, 2), (2_001, 2048, 3),
                                      (20_011, 100, 64), (333, 4100, 7), (65, 20_000, 16)])
