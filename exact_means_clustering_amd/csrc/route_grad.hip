@@ -221,15 +221,17 @@ __global__ __launch_bounds__(256) void route_grad_rows_kernel(GradArgs<T> a, boo
   }
 }
 
-// Rows of any length, a workgroup each: the row's maximum and sum (fp32 over a thread's values, in 64 bits over its
-// groups of eight), then the row again.  The selections' elements are written last, by their threads.
+// Rows of any length, a workgroup each: a thread's running maximum and sum (fp32 over the elements of a load, in 64 bits
+// over its loads), then the row again.  16 bytes a load at element alignment, a row's last few elements one by one.  The
+// selections' elements are written last, by their threads.
 template <class T>
 __global__ __launch_bounds__(256) void route_grad_wide_kernel(GradArgs<T> a) {
   __shared__ float tmp[2][4];
   __shared__ uint32_t is[64];
   __shared__ float gs[64];
+  constexpr int V = 16 / T::SZ;
   const int tid = threadIdx.x, S = a.S;
-  const uint32_t K = a.K;
+  const uint32_t K = a.K, whole = K / V * V;
   auto join = [&](float v, bool largest, int k) {
     v = largest ? team_max<64>(v) : team_sum<64>(v);
     if ((tid & 63) == 0) tmp[k][tid >> 6] = v;
@@ -247,23 +249,37 @@ __global__ __launch_bounds__(256) void route_grad_wide_kernel(GradArgs<T> a) {
     const typename T::raw* x = a.logits + row * K;
     typename T::raw* out = a.dlogits + row * K;
     if (!any) {
-      if (!a.accumulate)
-        for (uint32_t k = tid; k < K; k += 256) out[k] = round_to<T>(0.f);
+      if (!a.accumulate) {
+        Pack<T, V> none;
+        none.zero();
+        for (uint32_t k = tid * V; k < whole; k += 256 * V) none.store_loose(out + k);
+        if (tid < K - whole) out[whole + tid] = round_to<T>(0.f);
+      }
       continue;
     }
     float m = -INFINITY;
-#pragma unroll 8
-    for (uint32_t k = tid; k < K; k += 256) m = fmaxf(m, T::to_f32(x[k]));
-    m = join(m, true, 0);
-    const float shift = m == -INFINITY ? 0.f : m;
     double sum = 0.0;
-    for (uint32_t k = tid; k < K; k += 2048) {
-      float s = 0.f;
-#pragma unroll
-      for (uint32_t i = 0; i < 2048; i += 256) s += k + i < K ? exp_diff<F32>(T::to_f32(x[k + i]), shift) : 0.f;
-      sum += (double)s;
+    auto add = [&](auto& e) {
+      const float high = fmaxf(m, max_of(e));
+      const float shift = high == -INFINITY ? 0.f : high;
+      for (float& f : e) f = exp_diff<F32>(f, shift);
+      sum = sum * (double)(m == -INFINITY ? 0.f : exp_diff<F32>(m, shift)) + (double)pair_sum(e);
+      m = high;
+    };
+#pragma unroll 4
+    for (uint32_t k = tid * V; k < whole; k += 256 * V) {
+      Pack<T, V> p;
+      p.load_loose(x + k);
+      float e[V];
+      p.unpack(e);
+      add(e);
     }
-    const float inv = 1.f / join((float)sum, false, 1);
+    if (tid < K - whole) {
+      float e[2] = {T::to_f32(x[whole + tid]), -INFINITY};
+      add(e);
+    }
+    const float high = join(m, true, 0), shift = high == -INFINITY ? 0.f : high;
+    const float inv = 1.f / join((float)(sum * (double)(m == -INFINITY ? 0.f : exp_diff<F32>(m, shift))), false, 1);
     // the sum of a choice's derivatives, its probability, and its old value
     float mine = 0.f, p = 0.f, old = 0.f;
     bool lead = false;
@@ -279,10 +295,26 @@ __global__ __launch_bounds__(256) void route_grad_wide_kernel(GradArgs<T> a) {
     }
     __syncthreads();  // (tmp is free, and the old values are read)
     const float mean = join(lead ? p * mine : 0.f, false, 0);
-#pragma unroll 4
-    for (uint32_t k = tid; k < K; k += 256) {
-      const float d = -mean * (exp_diff<F32>(T::to_f32(x[k]), shift) * inv);
-      out[k] = round_to<T>(a.accumulate ? T::to_f32(out[k]) + d : d);
+    auto grad = [&](float f, float was) {
+      const float d = -mean * (exp_diff<F32>(f, shift) * inv);
+      return a.accumulate ? was + d : d;
+    };
+#pragma unroll 2
+    for (uint32_t k = tid * V; k < whole; k += 256 * V) {
+      Pack<T, V> p, q;
+      p.load_loose(x + k);
+      q.zero();
+      if (a.accumulate) q.load_loose(out + k);
+      float f[V], was[V];
+      p.unpack(f), q.unpack(was);
+#pragma unroll
+      for (int v = 0; v < V; ++v) f[v] = grad(f[v], was[v]);
+      p.pack(f);
+      p.store_loose(out + k);
+    }
+    if (tid < K - whole) {
+      const uint32_t k = whole + tid;
+      out[k] = round_to<T>(grad(T::to_f32(x[k]), a.accumulate ? T::to_f32(out[k]) : 0.f));
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the row's values have arrived before the selections' are sent
     __syncthreads();
