@@ -118,8 +118,9 @@ KM_API int kmeans_adamw_table(const km_adamw_tensor* tensors, int32_t count, int
  *   p = p (1 - lr weight_decay decay)
  *       - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
  * p is the master copy where there is one, and the parameter its value rounded
- * once to param_dtype; arithmetic is fp32; 0 / 0 (eps 0, nothing moved) is 0.  count, param_dtype, grad_dtype,
- * bits and masters (0 or 1) are those the table was made for.
+ * once to param_dtype; arithmetic is fp32 (eps is rounded to it); 0 / 0 (eps 0,
+ * nothing moved) is 0.  count, chunks, param_dtype, grad_dtype, bits and
+ * masters (0 or 1) are those the table was made for.
  * States in 8 bits: a block's scale is its largest magnitude times 2^-8 (m) or
  * 2^-15 (v), a value is its code times the scale, rounded to nearest even, so
  * the largest is held exactly; a positive v is at least the smallest code
@@ -128,7 +129,7 @@ KM_API int kmeans_adamw_table(const km_adamw_tensor* tensors, int32_t count, int
  * itself uses m and v before they are rounded.  A NaN stays with its element;
  * an infinite m is held as NaN.
  * Step count and rates that change between replays of a captured call are read
- * on the device: step_at (int64, nullable) in place of step >= 1, lr_at (fp32,
+ * on the device: step_at (int64 >= 1, nullable) in place of step, lr_at (fp32,
  * nullable) in place of lr.  grad_scale_at (fp32, nullable) is grad_scale (1
  * if null); skip_at (a byte, nullable): nothing is changed where it is not 0. */
 KM_API int kmeans_adamw(const void* table, int32_t count, int64_t chunks, int32_t param_dtype, int32_t grad_dtype,
