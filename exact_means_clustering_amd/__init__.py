@@ -751,7 +751,8 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None,
     of any of the three types (they may be mixed; each pair of types is a launch of its own), exp_avg and exp_avg_sq
     fp32, or float8_e4m3fn and float8_e5m2 with ``scales`` (two lists of fp32 tensors, see adamw_states); masters: a list
     of fp32 copies of the parameters on which the step is taken, with None for those without (and for fp32 parameters),
-    or None; decay: a factor of weight_decay for each tensor, or None (1)."""
+    or None; decay: a factor of weight_decay for each tensor, or None (1).  The plan holds these tensors' memory: later
+    gradients are written into the same tensors, and a captured step needs the plan as long as it is replayed."""
     params = list(params)
     n = len(params)
     if n == 0:

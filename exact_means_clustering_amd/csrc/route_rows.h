@@ -429,7 +429,8 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
                 m1 = fmaxf(m1, c);
               }
             }
-            worth[it] = a.best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+            // (a sum below fp32 is no -inf, which is a group without choices; biases of that size leave all for the end)
+            worth[it] = a.best == 2 && m2 > -INFINITY ? fmaxf(m1 + m2, -0x1.fffffep127f) : m1;
           }
           wave_sync();
           for (int it = lane; it < SL * a.G; it += 64) {

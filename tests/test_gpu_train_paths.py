@@ -137,6 +137,23 @@ def test_route_of_long_rows(km, K, S):
         check_route(km.route(x.cuda(), S, bias=b.cuda(), score="sigmoid"), x, S, bias=b, score="sigmoid")
 
 
+@pytest.mark.parametrize("K", [12, 64, 320, 2304])
+def test_route_of_extreme_biases(km, K):
+    """Biases that absorb the scores (ties then go to the lowest index), whose sums pass fp32, and that force choices in
+    and out."""
+    x = some_logits(40, K, F32, K)
+    x[1] = -math.inf
+    x[2, : K // 2] = -math.inf
+    kinds = torch.tensor([3e38, 3e38, -3e38, 1e30, 0.0, 0.001, -0.002, math.inf, -math.inf])
+    for seed, some in enumerate((slice(0, 7), slice(0, 9), slice(3, 6), slice(7, 9), slice(2, 3))):
+        of = kinds[some]
+        b = of[torch.randint(0, len(of), (K,), generator=gen(seed))]
+        for score in ("softmax", "sigmoid"):
+            for kw in (dict(), dict(groups=4, top_groups=2), dict(groups=4, top_groups=3, group_best=1)):
+                kw = dict(score=score, bias=b, **kw)
+                check_route(km.route(x.cuda(), 5, **{**kw, "bias": b.cuda()}), x, 5, **kw)
+
+
 @pytest.mark.parametrize("K, groups, S", [(8192, 1, 64), (8192, 64, 33), (8193, 3, 9), (2052, 4, 3), (40, 5, 36), (1, 1, 1)])
 def test_route_of_rows_taken_in_64_bits(km, K, groups, S):
     """Rows with scores that are too long for a wave's registers, and more selections than its lists, or than a lane's
