@@ -239,19 +239,21 @@ struct RouteLds {
     o.exact = at, at += scored ? 2 * K : 0;  // one row's scores in 64 bits
     o.extra = at, at += scored ? 2 * SL : 0;  // the key of a choice that may belong to the selection
     o.info = at, at += 2 * SL;               // a row's largest logit, 1 / sum of exponentials
-    o.flag = at, at += SL;                   // kOpen, kLast
+    o.flag = at, at += SL;                   // kOpen, kLast, kCopies
     o.total = (at + 3) & ~3;
     return o;
   }
 };
-constexpr int kOpen = 2, kLast = 1;  // a row whose candidates are put in order in 64 bits; one that is so as a whole
+// A row whose candidates are put in order in 64 bits, one that is so as a whole, and one whose extra candidate has copies
+// (of the same logit and bias) behind it.
+constexpr int kOpen = 2, kLast = 1, kCopies = 4;
 
 // What a kernel is made for: rows of K <= LPR * E choices whose order is the logits' own; the same of any K, taken
 // LPR * E at a time; and rows of K <= LPR * E with scores, a bias or groups.
 enum RouteMode { kPlain, kWide, kScored };
 
 template <class T, int E, int LPR, int L, RouteMode MODE>
-__global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 : 4) void route_rows_kernel(
+__global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && (E == 32 || L == 16) ? 3 : 4) void route_rows_kernel(
     RouteArgs<T> a, bool loose, RouteLds o, uint32_t magic, uint32_t group_magic) {
   using Sl = Slice<T, E, LPR>;
   constexpr int V = Sl::V, NV = Sl::NV, SL = 64 / LPR;
@@ -374,6 +376,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
         join_lists<L, LPR>(top);
       } else {
         int unsure = 0;
+        bool copies = false;
         if (arith && !a.softmax) {
           add_bias([&](int i, float b) { return quick_sigmoid(x[i]) + b; });
         }
@@ -483,7 +486,8 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
             asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, 0, %0, vcc" : "+v"(count) : "v"(x[i]), "v"(border) : "vcc");
           count = (uint32_t)team_sum<LPR>((float)count);
           const bool many = vs > -INFINITY && (int)count > S && live && !bad;
-          if (__ballot(many)) {  // the largest of them joins; others than it and its equals are for the end
+          copies = many && (int)count > S + 1;
+          if (__ballot(many)) {  // the largest of them joins; others than it and its copies are for the end
             auto score = [&](int k, float& f, float& b) {
               f = T::to_f32(a.logits[row * a.K + k]), b = bias[k];
               const bool out = a.G > 1 && lds[o.worth + (SL + slot) * a.G + k / (a.K / a.G)] == 0.f;  // (stays?)
@@ -500,7 +504,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
               }
             join_lists<1, LPR>(best);
             extra = best[0];
-            if (many && (int)count > S + 1) {
+            if (copies) {
               const float fe = T::to_f32(a.logits[row * a.K + key_col(extra)]), be = bias[key_col(extra)];
               for (int k = g; k < a.K; k += LPR) {
                 const double key = key_of(score(k, f, b), k);
@@ -512,7 +516,10 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
         }
         wave_sync();
         if (g == 0) {
-          flag[slot] = !arith || !live || bad ? 0 : unsure ? kLast : key_score(extra) > -INFINITY ? kOpen : 0;
+          flag[slot] = !arith || !live || bad               ? 0
+                       : unsure                              ? kLast
+                       : key_score(extra) > -INFINITY ? (copies ? kOpen | kCopies : kOpen)
+                                                             : 0;
           reinterpret_cast<double*>(lds + o.extra)[slot] = extra;
         }
       }
@@ -550,7 +557,7 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
         }
         wave_sync();
         const int state = lane < SL ? flag[lane] : 0;
-        uint64_t open = __ballot(state == kOpen), whole = __ballot(state & kLast);
+        uint64_t open = __ballot((state & (kOpen | kLast)) == kOpen), whole = __ballot(state & kLast);
         while (open) {  // lane j takes candidate j, the extra one is the last
           const int r = __builtin_ctzll(open);
           open &= open - 1;
@@ -579,6 +586,8 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && E == 32 ? 3 :
                 last |= lane_value(z, i) != z || lane_value(b, i) != b;
             }
           }
+          // (behind the extra one there may be room for its copies)
+          last |= lane == S && some && rank < S - 1 && (flag[r] & kCopies);
           if (__ballot(last)) {
             whole |= 1ull << r;
           } else if (lane <= S && rank < S) {

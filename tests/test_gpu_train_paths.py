@@ -137,6 +137,24 @@ def test_route_of_long_rows(km, K, S):
         check_route(km.route(x.cuda(), S, bias=b.cuda(), score="sigmoid"), x, S, bias=b, score="sigmoid")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n, K, S", [(9, 8, 2), (9, 60, 4), (2_300, 1000, 8), (17, 256, 12), (5_000, 511, 5), (3, 2048, 32)])
+def test_route_of_copies_behind_the_selection(km, score, n, K, S):
+    """Equal choices at a row's end that 32 bits do not tell from lower ones in front of them, and that belong to the
+    selection: two of them, as many as there are selections, and more."""
+    x = torch.full((n, K), -9.0) - torch.rand(n, K, generator=gen(K))
+    b = torch.zeros(K)
+    low, high = torch.tensor(-5.0), torch.nextafter(torch.tensor(-5.0), torch.tensor(0.0))
+    b[: K // 2], b[K // 2:] = 1.0, 1.0
+    for i in range(n):
+        copies = (2, S, S + 2)[i % 3]
+        x[i, 1:1 + S] = low
+        x[i, K - copies:] = high
+        if i % 2:
+            x[i, 0] = 2.0
+    check_route(km.route(x.cuda(), S, score=score, bias=b.cuda()), x, S, score=score, bias=b)
+
+
 @pytest.mark.parametrize("K", [12, 64, 320, 2304])
 def test_route_of_extreme_biases(km, K):
     """Biases that absorb the scores (ties then go to the lowest index), whose sums pass fp32, and that force choices in
