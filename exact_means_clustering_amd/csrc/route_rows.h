@@ -480,10 +480,9 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && (E == 32 || L
           for (int i = 1; i < L; ++i) last = i == S - 1 ? top[i] : last;
           const float vs = key_score(last);
           const float border = vs - 2.2f * (kU * (base + fabsf(vs)) + 0x1p-120f);
-          uint32_t count = 0;  // (a comparison and an addition of its bit each)
+          uint32_t count = 0;  // (a comparison and an addition of its bit each; the compiler puts the waits between them)
 #pragma unroll
-          for (int i = 0; i < E; ++i)
-            asm("v_cmp_ge_f32 vcc, %1, %2\n\tv_addc_co_u32 %0, vcc, 0, %0, vcc" : "+v"(count) : "v"(x[i]), "v"(border) : "vcc");
+          for (int i = 0; i < E; ++i) count += x[i] >= border;
           count = (uint32_t)team_sum<LPR>((float)count);
           const bool many = vs > -INFINITY && (int)count > S && live && !bad;
           copies = many && (int)count > S + 1;
