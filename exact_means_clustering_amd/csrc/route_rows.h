@@ -334,7 +334,8 @@ __global__ __launch_bounds__(256, L == 32 ? 2 : MODE == kScored && (E == 32 || L
       }
       if (sums) {
         const float m = team_max<LPR>(high);
-        sum = team_sum<LPR>(high == -INFINITY ? 0.f : sum * exp_diff<F32>(high, m));
+        // (a lane of -inf only has nothing, but for the NaN that maxima pass over and that its sum holds)
+        sum = team_sum<LPR>(high == -INFINITY && sum == sum ? 0.f : sum * exp_diff<F32>(high, m));
         high = m, inv = 1.f / sum;
         bad = sum != sum;
       } else {
