@@ -44,4 +44,20 @@ def test_route_of_a_nan_among_masked_choices(km, K, negative, dt):  # noqa: F811
                 H.check_route(got, x, S, score=score, renormalise=renormalise)
 
 
+def test_route_of_group_sums_past_fp32(km):  # noqa: F811
+    """Two groups whose worths both overflow 32 bits are told apart in 64; a worth of +inf is larger than either."""
+    K, G = 32, 8
+    x = H.some_logits(40, K, F32, 3)
+    for values in ([2e38, 2e38, 3e38, 3e38], [3e38, 1e38, 2e38, 3e38], [2e38, 2e38, math.inf, 0.0], [math.inf, -1e38, math.inf, 3e38],
+                   [-3e38, -3e38, -2e38, -2e38]):
+        for first in (0, 12):
+            bias = torch.zeros(K) if values[0] > 0 else torch.full((K,), -3.2e38)
+            bias[first:first + 2] = torch.tensor(values[:2])
+            bias[first + 8:first + 10] = torch.tensor(values[2:])
+            for keep in (1, 2):
+                for score in ("softmax", "sigmoid"):
+                    kw = dict(score=score, groups=G, top_groups=keep, renormalise=False)
+                    H.check_route(km.route(x.cuda(), 3, bias=bias.cuda(), **kw), x, 3, bias=bias, **kw)
+
+
 # ---- AdamW ------------------------------------------------------------------------------------------------------------
