@@ -73,6 +73,7 @@ __device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) 
 #pragma unroll
     for (int e = 0; e < 4; ++e) high = fabsf(x[e]) < INFINITY ? fmaxf(high, fabsf(x[e])) : high;
     high = team_max<64>(high);
+    if (Q::kLeast > 0.f) high = fmaxf(high, 0x1p-100f);  // (a format that holds infinities needs a scale for them)
   }
   const bool some = high >= 0x1p-100f;
   const float inv = some ? Q::kTop / high : 0.f, least = some ? Q::kLeast : 0.f;

@@ -127,7 +127,8 @@ KM_API int kmeans_adamw_table(const km_adamw_tensor* tensors, int32_t count, int
  * (2^-16), so that an element that has moved never divides by eps alone; a
  * block whose largest magnitude is below 2^-100 is held as zeros.  The step
  * itself uses m and v before they are rounded.  A NaN stays with its element;
- * an infinite m is held as NaN.
+ * an infinite m is held as NaN, an infinite v (the square of a large gradient)
+ * as infinity, which stops its element.
  * Step count and rates that change between replays of a captured call are read
  * on the device: step_at (int64 >= 1, nullable) in place of step, lr_at (fp32,
  * nullable) in place of lr.  grad_scale_at (fp32, nullable) is grad_scale (1

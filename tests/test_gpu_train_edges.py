@@ -61,3 +61,24 @@ def test_route_of_group_sums_past_fp32(km):  # noqa: F811
 
 
 # ---- AdamW ------------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_a_square_past_fp32(km, bits):  # noqa: F811
+    """A gradient whose square is infinite stops its element, whatever else its block holds, and no other."""
+    for others in (0.0, 1e-3):
+        p = torch.ones(600, device="cuda")
+        g = torch.full((600,), others, device="cuda")
+        g[300] = 1e25
+        M, V, scales = km.adamw_states([p], bits)
+        plan = km.adamw_plan([p], [g], M, V, scales=scales)
+        for step in (1, 2, 3):
+            km.adamw(plan, lr=1e-2, step=step, weight_decay=0.0)
+            g[300] = 0.0
+            v = V[0].float() if bits == 8 else V[0]
+            assert bool(torch.isfinite(p).all()) and float(p[300]) == 1.0, step
+            assert float(v[300]) == math.inf and int(torch.isfinite(v).sum()) == 599
+            if bits == 8:
+                assert float(scales[1][0][1]) > 0
+        # (beside an m of 1e24 the others' m is 0 in 8 bits: they have moved once)
+        assert bool((p[:256] == p[0]).all()) and bool((p[512:] == p[0]).all()) and bool((p[0] < 1.0) == (others > 0))
+        assert bool(((p[256:512] < 1.0) == (others > 0))[torch.arange(256) != 44].all())
