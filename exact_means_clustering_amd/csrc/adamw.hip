@@ -63,26 +63,40 @@ struct E5M2 {
 };
 
 // Codes of a wave's 256 values and their scale (in every lane).  A NaN or an infinity leaves the others' scale alone: the
-// maximum passes a NaN over, and infinities are looked for only where it is one.
+// maximum passes a NaN over, and infinities are looked for only where it is one.  Where the largest is below 2^-100, m is
+// held as zeros.  v, of smaller values still, is not: a positive v that went to 0 would leave its element's step to eps.
+// Its scale is 2^-133 at least, so that the least code stays a positive number (2^-149), and its codes are formed from
+// values times 2^100.
 template <class Q>
 __device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) {
   float high = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
   high = team_max<64>(high);
-  if (high == INFINITY) {  // uniform over the wave
-    high = 0.f;
+  float inv, y[4] = {x[0], x[1], x[2], x[3]};
+  if (high >= 0x1p-100f && high < INFINITY) {  // uniform over the wave
+    inv = Q::kTop / high, scale = high * (1.f / Q::kTop);
+  } else {
+    const bool inf = high == INFINITY;
+    if (inf) {
+      high = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) high = fabsf(x[e]) < INFINITY ? fmaxf(high, fabsf(x[e])) : high;
-    high = team_max<64>(high);
-    if (Q::kLeast > 0.f) high = fmaxf(high, 0x1p-100f);  // (a format that holds infinities needs a scale for them)
+      for (int e = 0; e < 4; ++e) high = fabsf(x[e]) < INFINITY ? fmaxf(high, fabsf(x[e])) : high;
+      high = team_max<64>(high);
+    }
+    if (high >= 0x1p-100f) {
+      inv = Q::kTop / high, scale = high * (1.f / Q::kTop);
+    } else if (Q::kLeast > 0.f && (high > 0.f || inf)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] *= 0x1p100f;
+      high = fmaxf(high * 0x1p100f, 0x1p-33f * Q::kTop);
+      inv = Q::kTop / high, scale = high * (0x1p-100f / Q::kTop);
+    } else {
+      inv = scale = 0.f;
+    }
   }
-  const bool some = high >= 0x1p-100f;
-  const float inv = some ? Q::kTop / high : 0.f, least = some ? Q::kLeast : 0.f;
-  scale = some ? high * (1.f / Q::kTop) : 0.f;
-  float y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    y[e] = x[e] * inv;
-    if (Q::kLeast > 0.f && x[e] > 0.f) y[e] = y[e] < least ? least : y[e];
+    y[e] *= inv;
+    if (Q::kLeast > 0.f && x[e] > 0.f) y[e] = y[e] < Q::kLeast ? Q::kLeast : y[e];
   }
   return Q::pack(y);
 }

@@ -122,11 +122,12 @@ KM_API int kmeans_adamw_table(const km_adamw_tensor* tensors, int32_t count, int
  * nothing moved) is 0.  count, chunks, param_dtype, grad_dtype, bits and
  * masters (0 or 1) are those the table was made for.
  * States in 8 bits: a block's scale is its largest magnitude times 2^-8 (m) or
- * 2^-15 (v), a value is its code times the scale, rounded to nearest even, so
- * the largest is held exactly; a positive v is at least the smallest code
- * (2^-16), so that an element that has moved never divides by eps alone; a
- * block whose largest magnitude is below 2^-100 is held as zeros.  The step
- * itself uses m and v before they are rounded.  A NaN stays with its element;
+ * 2^-15 (v; 2^-133 at least), a value is its code times the scale, rounded to
+ * nearest even, so the largest is held exactly; a positive v is at least the
+ * smallest code (2^-16) and stays positive, so that an element whose v is not
+ * 0 in fp32 never divides by eps alone; an m in a block whose largest magnitude
+ * is below 2^-100 is held as 0.  The step itself uses m and v before they are
+ * rounded.  A NaN stays with its element;
  * an infinite m is held as NaN, an infinite v (the square of a large gradient)
  * as infinity, which stops its element.
  * Step count and rates that change between replays of a captured call are read

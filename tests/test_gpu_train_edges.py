@@ -82,3 +82,32 @@ def test_adamw_of_a_square_past_fp32(km, bits):  # noqa: F811
         # (beside an m of 1e24 the others' m is 0 in 8 bits: they have moved once)
         assert bool((p[:256] == p[0]).all()) and bool((p[512:] == p[0]).all()) and bool((p[0] < 1.0) == (others > 0))
         assert bool(((p[256:512] < 1.0) == (others > 0))[torch.arange(256) != 44].all())
+
+
+@pytest.mark.parametrize("size", [1e-13, 3e-15, 1e-16, 1e-18])
+@pytest.mark.parametrize("eps", [0.0, 1e-30, 1e-8])
+def test_adamw_8bit_of_small_gradients(km, size, eps):  # noqa: F811
+    """Gradients whose squares are next to nothing, then none: an element that has moved never divides by eps alone.  A step
+    is off by half a step of m's code (2^-4) and half of that of v's (2^-3), and in 64 bits' terms by the rounding of v
+    below the normal range (1e-39 in steps of 2^-149 = 1.4e-45: nothing beside them)."""
+    n = 700
+    u = 1.0 + 2.0 * torch.rand(n, generator=H.gen(1))
+    g0 = (size * u).to(F32)
+    p, g = torch.zeros(n, device="cuda"), g0.cuda()
+    M, V, scales = km.adamw_states([p], 8)
+    plan = km.adamw_plan([p], [g], M, V, scales=scales)
+    m, v = torch.zeros(n, dtype=torch.float64), torch.zeros(n, dtype=torch.float64)
+    b1, b2, lr = 0.9, 0.999, 0.25
+    for step in range(1, 5):
+        before = p.cpu().double()
+        km.adamw(plan, lr=lr, step=step, betas=(b1, b2), eps=eps, weight_decay=0.0)
+        gr = g0.double() if step == 1 else 0.0
+        m, v = b1 * m + (1 - b1) * gr, b2 * v + (1 - b2) * gr * gr
+        want = -lr / (1 - b1 ** step) * m / (torch.sqrt(v / (1 - b2 ** step)) + eps)
+        # (a code of the step before is off by its half step, and each step adds another)
+        off = (step - 1) * (2.0 ** -4 + 2.0 ** -4 * 1.1) * 1.1 + 1e-5
+        moved = p.cpu().double() - before
+        assert bool(torch.isfinite(moved).all()), step
+        assert bool(((moved - want).abs() <= off * want.abs() + 1e-6 * p.cpu().double().abs()).all()), (
+            step, float(((moved - want) / want).abs().max()))
+        g.zero_()
