@@ -739,11 +739,11 @@ def adamw_states(params, bits: int = 32):
 
 
 class AdamWPlan:
-    """The tensors of adamw calls, checked and laid out once (made by adamw_plan): it keeps them alive, and holds as long
-    as their memory stays in place."""
+    """The tensors of adamw calls, checked and laid out once (made by adamw_plan): it keeps their memory alive, and steps
+    what is there, also after a tensor was given other memory."""
 
-    def __init__(self, groups, device, stream, tensors):
-        self._groups, self.device, self._stream, self._tensors = groups, device, stream, tensors
+    def __init__(self, groups, device, stream, memory):
+        self._groups, self.device, self._stream, self._memory = groups, device, stream, memory
 
 
 def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None, decay=None):
@@ -751,8 +751,9 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None,
     of any of the three types (they may be mixed; each pair of types is a launch of its own), exp_avg and exp_avg_sq
     fp32, or float8_e4m3fn and float8_e5m2 with ``scales`` (two lists of fp32 tensors, see adamw_states); masters: a list
     of fp32 copies of the parameters on which the step is taken, with None for those without (and for fp32 parameters),
-    or None; decay: a factor of weight_decay for each tensor, or None (1).  The plan holds these tensors' memory: later
-    gradients are written into the same tensors, and a captured step needs the plan as long as it is replayed."""
+    or None; decay: a factor of weight_decay for each tensor, or None (1).  The plan holds these tensors' memory and does
+    not follow a tensor that is given other memory (``p.data = ...``, a gradient made anew): later gradients are written
+    into the same tensors, else a new plan is made.  A captured step needs the plan as long as it is replayed."""
     params = list(params)
     n = len(params)
     if n == 0:
@@ -767,7 +768,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None,
             raise KMeansError(KM_EINVAL, f"{name} must have {n} entries (got {len(v)})")
     bits = 32 if scales is None else 8
     kinds = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
-    groups = {}
+    groups, memory = {}, []
     for i, p in enumerate(params):
         g, m, v, w = (lists[k][i] for k in ("grads", "exp_avg", "exp_avg_sq", "masters"))
         _need(p, f"params[{i}]", like=params[0])
@@ -784,12 +785,13 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None,
             for k, x in enumerate((a, b)):
                 _into(x, f"scales[{k}][{i}]", (-(-p.numel() // ADAMW_BLOCK),), torch.float32, params[0])
             t.exp_avg_scale, t.exp_avg_sq_scale = a.data_ptr(), b.data_ptr()
+        # (the storages themselves: a tensor may let go of its own)
+        memory += [x.untyped_storage() for x in (p, g, m, v, w, *((a, b) if bits == 8 else ())) if x is not None]
         if p.numel():
             groups.setdefault((_dtype(p), _dtype(g), w is not None), []).append(t)
         else:
             _dtype(p), _dtype(g)
     made = []
-    everything = [t for ts in groups.values() for t in ts]
     device = params[0].device
     with torch.cuda.device(device):
         for (pdt, gdt, has), ts in groups.items():
@@ -804,7 +806,7 @@ def adamw_plan(params, grads, exp_avg, exp_avg_sq, *, scales=None, masters=None,
         if len(groups) > 1:  # nothing may overlap across the launches either
             _across(groups, bits)
         stream = _raw_stream(device.index)
-    return AdamWPlan(made, device, stream, (params, lists, everything))
+    return AdamWPlan(made, device, stream, memory)
 
 
 def _across(groups, bits):

@@ -111,3 +111,22 @@ def test_adamw_8bit_of_small_gradients(km, size, eps):  # noqa: F811
         assert bool(((moved - want).abs() <= off * want.abs() + 1e-6 * p.cpu().double().abs()).all()), (
             step, float(((moved - want) / want).abs().max()))
         g.zero_()
+
+
+def test_adamw_plan_holds_the_memory_of_its_tensors(km):  # noqa: F811
+    """A tensor that is given other memory leaves the plan with the old one, which no one else is given."""
+    n = 1 << 20
+    p, g = torch.ones(n, device="cuda"), torch.ones(n, device="cuda")
+    M, V, scales = km.adamw_states([p], 8)
+    w = torch.ones(n, device="cuda")
+    h = torch.ones(n, device="cuda", dtype=BF16)
+    M2, V2, scales2 = km.adamw_states([h], 8)
+    km.adamw_plan([p], [g], M, V, scales=scales)  # (dropped at once: holds nothing)
+    base = torch.cuda.memory_allocated()
+    plans = [km.adamw_plan([p], [g], M, V, scales=scales), km.adamw_plan([h], [g], M2, V2, scales=scales2, masters=[w])]
+    tables = torch.cuda.memory_allocated() - base
+    for t in (p, g, w, h, *M, *V, *M2, *V2, *scales[0], *scales[1], *scales2[0], *scales2[1]):
+        t.data = torch.empty(0, dtype=t.dtype, device="cuda")
+    assert torch.cuda.memory_allocated() == base + tables
+    del plans
+    assert torch.cuda.memory_allocated() < base - 17 * n
