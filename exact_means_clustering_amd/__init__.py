@@ -721,6 +721,7 @@ class _AdamWTensor(ctypes.Structure):
 
 
 ADAMW_BLOCK = 256  # elements of an 8-bit state that share a scale
+_STOCHASTIC = 256  # KM_ADAMW_STOCHASTIC
 
 
 def adamw_states(params, bits: int = 32):
@@ -847,13 +848,18 @@ def _scalar_at(t, name, dtype, device):
 
 
 def adamw(plan: AdamWPlan, *, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.01,
-          grad_scale=None, skip=None, stream=None):
+          grad_scale=None, skip=None, rounding: str = "nearest", stream=None):
     """One AdamW step over the plan's tensors, in place:
     m = b1 m + (1 - b1) g, v = b2 v + (1 - b2) g^2, p = p (1 - lr weight_decay) - lr mhat / (sqrt(vhat) + eps), with
     g = grad_scale * grad and mhat, vhat without the bias of a zero start after ``step`` steps (the first is 1).  lr may
     be an fp32 CUDA tensor and step an int64 one, of one value, which are read on the device (for captured calls);
     grad_scale is None or an fp32 CUDA tensor; skip is None or a bool or uint8 CUDA tensor: nothing changes where it is
-    true.  Runs on ``stream`` (default: the current one)."""
+    true.  rounding: how states in 8 bits are rounded to their codes.  "nearest" holds each state as near as its format
+    allows, but over a run v stays frozen relative to the largest of its 256 elements (a step moves it by less than half a
+    code), so elements whose gradients change take steps that are several times too small or too large;
+    "stochastic" rounds either way so that what is held follows the averages without bias, and is the one to train with
+    for more than some hundred steps.  Its random numbers come from the step and the element's place, so each step needs
+    its own number, and a run repeats bit for bit.  Runs on ``stream`` (default: the current one)."""
     if not isinstance(plan, AdamWPlan):
         raise KMeansError(KM_EINVAL, "plan must be made by adamw_plan")
     device = plan.device
@@ -867,6 +873,11 @@ def adamw(plan: AdamWPlan, *, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, w
     if skip is not None and (not isinstance(skip, torch.Tensor) or skip.dtype not in (torch.bool, torch.uint8)):
         raise KMeansError(KM_EINVAL, "skip must be a bool or uint8 CUDA tensor")
     skip_at = _scalar_at(skip, "skip", skip.dtype if skip is not None else None, device)
+    if rounding not in ("nearest", "stochastic"):
+        raise KMeansError(KM_EUNSUPPORTED, f"unknown rounding {rounding!r} (nearest or stochastic)")
+    if rounding == "stochastic" and any(group[5] != 8 for group in plan._groups):
+        raise KMeansError(KM_EINVAL, "rounding='stochastic' is for states in 8 bits")
+    how = _STOCHASTIC if rounding == "stochastic" else 0
     with contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device):
         raw = _raw_stream(device.index) if stream is None else stream.cuda_stream
         if raw != plan._stream:  # the table must outlive the step there
@@ -874,7 +885,7 @@ def adamw(plan: AdamWPlan, *, lr, step, betas=(0.9, 0.999), eps: float = 1e-8, w
             for group in plan._groups:
                 group[0].record_stream(on)
         for table, count, chunks, pdt, gdt, bits, masters in plan._groups:
-            _check(_lib.kmeans_adamw(table.data_ptr(), count, chunks, pdt, gdt, bits, masters,
+            _check(_lib.kmeans_adamw(table.data_ptr(), count, chunks, pdt, gdt, bits | how, masters,
                                      0.0 if lr_at else float(lr), float(betas[0]), float(betas[1]), float(eps),
                                      float(weight_decay), 1 if step_at else int(step), lr_at, step_at, scale_at,
                                      skip_at, raw))

@@ -6,7 +6,8 @@
 // time, so every access is up to 16 bytes a lane and a wave's four times 64 values are one block of a scale: its largest
 // magnitude is a reduction over the wave's lanes.  Measured: 8.4 million fp32 values 40 us (5.9 TB/s), 124 million bf16
 // values with copies 605 (5.7), 350 million with states in 8 bits 983 (5.7; a copy of 4 GiB moves 4.7).  With 8 bits the
-// vector units are busy four fifths of that time: a third of the instructions are the codes and their scales.
+// vector units are busy four fifths of that time: a third of the instructions are the codes and their scales; rounded
+// stochastically (a hash for four values, three products, a conversion a code instead of one for two) 1.5 % more time.
 #include <type_traits>
 
 #include "kernels.h"
@@ -21,6 +22,7 @@ namespace {
 struct Rates {
   float b1, c1, b2, c2;  // the betas and 1 - beta
   float eps, lr_wd, rate, root;  // lr * weight_decay, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+  uint32_t key;                  // of the step's random words
 };
 struct Live {  // what is read on the device, where it is there
   const float* lr;
@@ -32,6 +34,10 @@ struct Live {  // what is read on the device, where it is there
 };
 
 __host__ __device__ inline void set_step(Rates& r, double lr, double b1, double b2, double wd, int64_t step) {
+  uint64_t x = (uint64_t)step * 0x9E3779B97F4A7C15ull;
+  x = (x ^ x >> 32) * 0xD6E8FEB86659FD93ull;
+  x = (x ^ x >> 32) * 0xA0761D6478BD642Full;
+  r.key = (uint32_t)(x ^ x >> 32);
   r.lr_wd = (float)(lr * wd);
   r.rate = (float)(lr / (1.0 - pow(b1, (double)step)));
   r.root = (float)(1.0 / sqrt(1.0 - pow(b2, (double)step)));
@@ -39,11 +45,24 @@ __host__ __device__ inline void set_step(Rates& r, double lr, double b1, double 
 
 // A state's value in 8 bits: a format's conversions, its code for a block's largest magnitude (a power of two), and the
 // least code of a positive value.
+// Rounded to nearest, or stochastically: the conversion adds the random word's 20 (e4m3) or 21 (e5m2) upper bits to the
+// bits that it drops, those of subnormal codes among them.  18 and 19 of these are random and a one follows: the
+// expectation is the value itself to 2^-19 of a step, and a block's largest, which scaling may leave one unit of fp32
+// beside its code, is neither carried past it nor dropped below it.
 struct E4M3 {
   static constexpr float kTop = 256.f, kLeast = 0.f;
   __device__ static uint32_t pack(const float (&y)[4]) {
     int w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
+  }
+  __device__ static uint32_t pack(const float (&y)[4], const uint32_t (&random)[4]) {
+    uint32_t r[4];  // (the random bits' other end, so that m's errors are not v's)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = ((random[e] >> 16 | random[e] << 16) & 0xFFFFC000u) | 0x2000u;
+    int w = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], r[0], 0, 0);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], r[1], w, 1);
+    w = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], r[2], w, 2);
+    return (uint32_t)__builtin_amdgcn_cvt_sr_fp8_f32(y[3], r[3], w, 3);
   }
   __device__ static void unpack(uint32_t w, float (&y)[4]) {
     const auto a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
@@ -56,6 +75,15 @@ struct E5M2 {
     int w = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
     return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], w, true);
   }
+  __device__ static uint32_t pack(const float (&y)[4], const uint32_t (&random)[4]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = (random[e] & 0xFFFFE000u) | 0x1000u;
+    int w = __builtin_amdgcn_cvt_sr_bf8_f32(y[0], r[0], 0, 0);
+    w = __builtin_amdgcn_cvt_sr_bf8_f32(y[1], r[1], w, 1);
+    w = __builtin_amdgcn_cvt_sr_bf8_f32(y[2], r[2], w, 2);
+    return (uint32_t)__builtin_amdgcn_cvt_sr_bf8_f32(y[3], r[3], w, 3);
+  }
   __device__ static void unpack(uint32_t w, float (&y)[4]) {
     const auto a = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, false), b = __builtin_amdgcn_cvt_pk_f32_bf8((int)w, true);
     y[0] = a[0], y[1] = a[1], y[2] = b[0], y[3] = b[1];
@@ -67,8 +95,8 @@ struct E5M2 {
 // held as zeros.  v, of smaller values still, is not: a positive v that went to 0 would leave its element's step to eps.
 // Its scale is 2^-133 at least, so that the least code stays a positive number (2^-149), and its codes are formed from
 // values times 2^100.
-template <class Q>
-__device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) {
+template <class Q, bool SR>
+__device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale, const uint32_t (&random)[4]) {
   float high = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
   high = team_max<64>(high);
   float inv, y[4] = {x[0], x[1], x[2], x[3]};
@@ -98,7 +126,18 @@ __device__ __forceinline__ uint32_t to_codes(const float (&x)[4], float& scale) 
     y[e] *= inv;
     if (Q::kLeast > 0.f && x[e] > 0.f) y[e] = y[e] < Q::kLeast ? Q::kLeast : y[e];
   }
-  return Q::pack(y);
+  if constexpr (SR) return Q::pack(y, random);
+  else return Q::pack(y);
+}
+
+// Random words of a lane's four values: a hash of their place in the table and the step's key, and three products of it.
+// (The same for a value whatever its arrays' alignment.)
+__device__ __forceinline__ void random_words(uint32_t place, uint32_t key, uint32_t (&w)[4]) {
+  uint32_t x = place + key;
+  x = (x ^ x >> 16) * 0x9E3779B1u;
+  x = (x ^ x >> 15) * 0x6A09E667u;
+  w[0] = x ^ x >> 16;
+  w[1] = w[0] * 0xBB67AE85u, w[2] = w[0] * 0x3C6EF373u, w[3] = w[0] * 0xA54FF53Bu;
 }
 
 // Square root to one unit in the last place.  (The instruction takes values below the normal range as 0: scaled first.)
@@ -120,7 +159,7 @@ __device__ __forceinline__ X* uniform(X* x) {
 
 // The sums and products of m and v are rounded one by one, as the formula has them: what is held in 8 bits then does
 // not depend on which of them a compiler joins.
-template <class TP, class TG, bool MASTER, int BITS, bool STREAM>
+template <class TP, class TG, bool MASTER, int BITS, bool STREAM, bool SR>
 __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ table, int64_t map_at, int64_t chunks,
                                                     Rates r, Live live) {
 #pragma clang fp contract(off)
@@ -150,6 +189,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
     const int64_t base = (c - t.first) * kAdamChunk;
     const float keep = 1.f - r.lr_wd * t.decay;
     auto at = [&](int u) { return base + u * 1024 + (int64_t)threadIdx.x * 4; };
+    auto words = [&](int u, uint32_t (&w)[4]) {
+      if constexpr (SR) random_words(((uint32_t)c * U + u) * 256 + threadIdx.x, r.key, w);
+    };
     auto take = [](auto& pack, const auto* from) {
       if constexpr (STREAM) pack.load_nt(from);
       else pack.load(from);
@@ -235,7 +277,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
         }
         if constexpr (Q8) {
           float a, b;
-          const uint32_t ma = to_codes<E4M3>(mv, a), va = to_codes<E5M2>(vv, b);
+          uint32_t w[4];
+          words(u, w);
+          const uint32_t ma = to_codes<E4M3, SR>(mv, a, w), va = to_codes<E5M2, SR>(vv, b, w);
           put4(m0, i, ma);
           put4(v0, i, va);
           if (i % kAdamBlock == 0) sm0[i / kAdamBlock] = a, sv0[i / kAdamBlock] = b;
@@ -275,7 +319,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(const char* __restrict__ tab
         step(pv, gv, mv, vv);
         if constexpr (Q8) {
           float a, b;
-          mq = to_codes<E4M3>(mv, a), vq = to_codes<E5M2>(vv, b);  // all lanes of the wave take part
+          uint32_t w[4];
+          words(u, w);
+          mq = to_codes<E4M3, SR>(mv, a, w), vq = to_codes<E5M2, SR>(vv, b, w);  // all lanes of the wave take part
           if (i % kAdamBlock == 0 && i < t.numel) t.sm[i / kAdamBlock] = a, t.sv[i / kAdamBlock] = b;
         }
 #pragma unroll
@@ -302,7 +348,7 @@ constexpr int64_t kStream = (int64_t)1 << 27;
 
 template <class TP, class TG, bool MASTER>
 hipError_t adamw_t(const AdamCall& c, hipStream_t s) {
-  Rates r{(float)c.b1, (float)(1.0 - c.b1), (float)c.b2, (float)(1.0 - c.b2), (float)c.eps, 0.f, 0.f, 0.f};
+  Rates r{(float)c.b1, (float)(1.0 - c.b1), (float)c.b2, (float)(1.0 - c.b2), (float)c.eps, 0.f, 0.f, 0.f, 0u};
   set_step(r, c.lr, c.b1, c.b2, c.wd, c.step_at ? 1 : c.step);
   const Live live{c.lr_at, c.step_at, c.gscale_at, c.skip_at, c.lr, c.b1, c.b2, c.wd, c.step};
   const int64_t grid = c.chunks < (1 << 22) ? c.chunks : (1 << 22);
@@ -313,12 +359,15 @@ hipError_t adamw_t(const AdamCall& c, hipStream_t s) {
   auto go = [&](auto kernel) {
     kernel<<<dim3((unsigned)grid), dim3(256), 0, s>>>(table, map_at, c.chunks, r, live);
   };
-  if (c.bits == 8) {
-    if (stream) go(adamw_kernel<TP, TG, MASTER, 8, true>);
-    else go(adamw_kernel<TP, TG, MASTER, 8, false>);
+  if (c.bits == 8 && c.stochastic) {
+    if (stream) go(adamw_kernel<TP, TG, MASTER, 8, true, true>);
+    else go(adamw_kernel<TP, TG, MASTER, 8, false, true>);
+  } else if (c.bits == 8) {
+    if (stream) go(adamw_kernel<TP, TG, MASTER, 8, true, false>);
+    else go(adamw_kernel<TP, TG, MASTER, 8, false, false>);
   } else {
-    if (stream) go(adamw_kernel<TP, TG, MASTER, 32, true>);
-    else go(adamw_kernel<TP, TG, MASTER, 32, false>);
+    if (stream) go(adamw_kernel<TP, TG, MASTER, 32, true, false>);
+    else go(adamw_kernel<TP, TG, MASTER, 32, false, false>);
   }
   return hipGetLastError();
 }

@@ -372,6 +372,7 @@ struct AdamCall {
   const int64_t* step_at;
   const float* gscale_at;
   const uint8_t* skip_at;
+  bool stochastic;  // how codes are rounded (8 bits)
 };
 hipError_t launch_adamw(int pdt, int gdt, const AdamCall& c, hipStream_t s);
 

@@ -220,6 +220,8 @@ int kmeans_adamw(const void* table, int32_t count, int64_t chunks, int32_t param
   err_buf()[0] = 0;
   if (int rc = check_type(param_dtype, "param dtype")) return rc;
   if (int rc = check_type(grad_dtype, "grad dtype")) return rc;
+  const bool stochastic = bits == (8 | KM_ADAMW_STOCHASTIC);
+  if (stochastic) bits = 8;
   if (int rc = check_bits(bits)) return rc;
   if (count < 1 || count > kMaxTensors) return fail(KM_EINVAL, "count=%d must be 1 to %lld", count, (long long)kMaxTensors);
   if (chunks < 0 || chunks >= kMax31) return fail(KM_EINVAL, "chunks=%lld must be 0 to 2^31 - 1", (long long)chunks);
@@ -237,7 +239,7 @@ int kmeans_adamw(const void* table, int32_t count, int64_t chunks, int32_t param
   if ((uintptr_t)grad_scale_at % 4) return fail(KM_EINVAL, "misaligned pointer: grad_scale_at needs 4 bytes");
   if (chunks == 0) return KM_OK;
   const AdamCall c{table, count, chunks, bits,  masters != 0, lr,      beta1,         beta2,
-                   eps,   weight_decay,  step,  lr_at, step_at, grad_scale_at, skip_at};
+                   eps,   weight_decay,  step,  lr_at, step_at, grad_scale_at, skip_at, stochastic};
   KM_HIP(launch_adamw(param_dtype, grad_dtype, c, (hipStream_t)stream), "adamw launch");
   return KM_OK;
 }
