@@ -5,7 +5,7 @@
 // that have copies are not read).  A workgroup takes a chunk of 4,096 values of one tensor, a lane four neighbours at a
 // time, so every access is up to 16 bytes a lane and a wave's four times 64 values are one block of a scale: its largest
 // magnitude is a reduction over the wave's lanes.  Measured: 8.4 million fp32 values 40 us (5.9 TB/s), 124 million bf16
-// values with copies 605 (5.7), 350 million with states in 8 bits 983 (5.7; a copy of 4 GiB moves 4.7).  With 8 bits the
+// values with copies 610 (5.7), 350 million with states in 8 bits 993 (5.7; a copy of 4 GiB moves 4.7).  With 8 bits the
 // vector units are busy four fifths of that time: a third of the instructions are the codes and their scales; rounded
 // stochastically (a hash for four values, three products, a conversion a code instead of one for two) 1.5 % more time.
 #include <type_traits>

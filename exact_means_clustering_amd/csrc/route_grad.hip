@@ -32,7 +32,9 @@ struct GradArgs {
 // words whatever K and the address; of rows longer than the tile a workgroup takes `width` columns of one.  Bound by the
 // bytes written (8 x 4,095 x 128 bf16, eight a row, 5.7 us, most of it latency; 262,144 x 1,024 bf16 94 us, 5.7 TB/s; 16 KB
 // of rows leave LDS for seven workgroups a CU).  Accumulated, a selection's element is read, added to and written by its
-// thread: bound by the sectors that these touch, two a selection (65,536 x 256 fp32, eight a row, 14.1 us; fresh 15.5).
+// thread: bound by the chain of two reads, ids and then elements, that all
+// workgroups are in at once (65,536 x 256 fp32, eight a row, 14.0 us; fresh 15.5; the sectors of 32 bytes that are read and
+// written alone are 8.1).
 constexpr int kGradTile = 16384;  // bytes of rows in LDS
 
 template <class T, bool ACC>

@@ -16,11 +16,12 @@
 // leaves undecided), a few rows in ten thousand on random scores, is decided by the whole wave, all in 64 bits.
 //
 // Bound by vector instructions, not by the bytes: 630 of them for a lane's 32 values in rows of 1,024 bf16 of which two are
-// taken (softmax, keys, sort, merges), issued in 143 of the 133 to 165 us that 262,144 such rows take (4.0 TB/s of logits;
-// fp32, half the rows, 89 us and 6.0 TB/s).  So a row goes straight into registers, 16 bytes a lane and load, and a lane
-// holds 32 values: the more it sorts alone, the fewer merges across lanes.  Measured besides: 32,768 x 128 bf16, eight a
-// row, 6.6 us; 65,536 x 256 fp32 plain 15, with sigmoids and a bias 30, and in 8 groups 44 (a row decided as a whole holds
-// its wave up for 7 us).
+// taken (softmax, keys, sort, merges).  262,144 such rows are 80,500 of them a SIMD, of four cycles each: 134 us at 2.4 GHz,
+// which is what they take (4.0 TB/s of logits; fp32, half the rows, 89 us and 6.0 TB/s).  So a row goes straight into
+// registers, 16 bytes a lane and load, and a lane holds 32 values: the more it sorts alone, the fewer merges across lanes.
+// Measured besides: 32,768 x 128 bf16, eight a row, 6.6 us; 65,536 x 256 fp32 plain 15, with sigmoids and a bias 30, and in
+// 8 groups 43 (a row decided as a whole holds its wave up for 7 us: where most rows are left open, as in a router that
+// starts at zero, up to 370).
 #pragma once
 
 #include "route.h"
